@@ -90,6 +90,11 @@ typedef enum {
                               tiles per row) taken in ticket order by `grid_rows` CTAs, each
                               tile read once; carries by decoupled look-back through scratch
                               (rows * blocks_per_row <= 32768). Not chosen by the planner */
+    ARGR_PATH_LOGITS = 9,  /* vocabulary rows, forward (argreduce_logprobs, argreduce_distill): `block`
+                              threads per CTA, `cluster` CTAs per row (1 = none), `grid_rows`
+                              row slots */
+    ARGR_PATH_LOGITS_GRAD = 10, /* vocabulary rows, gradients: a row in `blocks_per_row` chunks, a
+                              CTA of `block` threads each */
     ARGR_PATH_STREAM = 4   /* every warp streams a contiguous range of rows through its own
                               `stages` shared-memory buffers of `stage_bytes`, filled by bulk
                               (TMA) copies; `group` lanes per row for rows that fit a buffer,
@@ -378,6 +383,124 @@ argr_status argreduce_read_error(void* scratch, argr_stream stream);
  */
 argr_status argreduce_noalloc(const void* x, argr_dtype dtype, int64_t rows, int64_t cols, argr_op op,
                               int64_t* out_idx, void* out_val, argr_stream stream);
+
+/*
+ * Vocabulary rows: log probabilities, entropy and top alternatives of rows of
+ * logits, a distillation loss from a teacher's top logits, and the gradients
+ * of both with respect to the logits.
+ *
+ * x is [rows, cols] logits of type ARGR_F32, ARGR_F16 or ARGR_BF16 (other
+ * types: ARGR_EUNSUPPORTED), row r at element r * row_stride (row_stride >= 0;
+ * 0 reads the same row for every r). Element-aligned addresses suffice.
+ * Exponentials, sums and statistics are binary32 throughout. With
+ *     z = x / temperature,  m = max x,  s = sum_j exp((x_j - m) / temperature),
+ *     lse = m / temperature + ln s,  p = exp(z - lse):
+ *
+ *   - A logit of -inf has p = 0 and adds nothing to any sum. A row of -inf
+ *     alone is empty: lse = -inf, every log p = -inf, entropy 0, gradient 0.
+ *   - A row with a NaN or +inf has NaN log probabilities, loss and gradients.
+ *   - A token (slot id) < 0 names nothing: the position has no token (the
+ *     slot is empty). One >= cols is a mistake that the host cannot see: the
+ *     row's log probability (loss) and gradient become NaN, and nothing is
+ *     read or written outside the row.
+ *
+ * temperature must be positive and finite. Results do not depend on timing:
+ * no floating-point atomics are used.
+ */
+
+/* The operators, for argreduce_logits_plan(). */
+typedef enum {
+    ARGR_LOGITS_LOGPROBS = 0,
+    ARGR_LOGITS_LOGPROBS_GRAD = 1,
+    ARGR_LOGITS_DISTILL = 2,
+    ARGR_LOGITS_DISTILL_GRAD = 3,
+    ARGR_LOGITS_DISTILL_STEP = 4
+} argr_logits_op;
+
+#define ARGR_LOGITS_MAX_TOP 128    /* top alternatives of a row, at most */
+#define ARGR_LOGITS_MAX_SLOTS 1024 /* distillation slots of a row, at most */
+
+/*
+ * For each row: logprob = log p of tokens[r] (0 where tokens[r] < 0), entropy =
+ * -sum_j p_j log p_j, lse, and the top_k largest logits in descending order,
+ * ties to the lowest index, NaNs after every number: their indices and their
+ * log p. Any output may be NULL (top_ids and top_logprobs also separately);
+ * tokens may be NULL when logprob is. stats receives 4 floats per row,
+ * {m, ln s, entropy, 0}: what argreduce_logprobs_backward() needs (an empty
+ * row: {-inf, -inf, 0, 0}). 0 <= top_k <= min(cols, ARGR_LOGITS_MAX_TOP).
+ * plan: NULL for the planner's. Errors as for argreduce(); stats 16-byte
+ * aligned.
+ */
+argr_status argreduce_logprobs(const void* x, argr_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                               float temperature, const int64_t* tokens, int32_t top_k, float* logprob,
+                               float* entropy, float* lse, int64_t* top_ids, float* top_logprobs, float* stats,
+                               const argr_plan* plan, argr_stream stream);
+
+/*
+ * The gradient of sum_r (g * logprob + h * entropy + c * lse) with respect to x:
+ *     grad[r, j] = (g ([j == token] - p_j) - h p_j (log p_j + entropy) + c p_j) / temperature
+ * g = grad_logprob[r] (0 where the row has no token), h = grad_entropy[r], c =
+ * grad_lse[r]; each may be NULL (zeros). stats: as argreduce_logprobs() wrote
+ * it for the same x and temperature. grad has x's type, rows grad_stride
+ * elements apart (>= cols); rounded once from binary32. It may be x itself
+ * (same pointer and stride) but must not overlap x otherwise: ARGR_EINVAL.
+ */
+argr_status argreduce_logprobs_backward(const void* x, argr_dtype dtype, int64_t rows, int64_t cols,
+                                        int64_t row_stride, float temperature, const int64_t* tokens,
+                                        const float* stats, const float* grad_logprob, const float* grad_entropy,
+                                        const float* grad_lse, void* grad, int64_t grad_stride,
+                                        const argr_plan* plan, argr_stream stream);
+
+/*
+ * Distillation of a student (x) from a teacher's top logits. ids[rows, slots]
+ * name distinct indices of the row (negative: an empty slot), teacher[rows,
+ * slots] holds the teacher's value for each.
+ *   tail == 0: q = softmax of teacher / temperature over the row's filled slots;
+ *              loss = sum_i q_i (ln q_i - ln p_{id_i}).
+ *   tail != 0: q_i = exp(teacher_i): teacher holds log probabilities (taken at
+ *              the same temperature). What is left, rest = max(0, 1 - sum q),
+ *              is one more outcome: loss = sum_i q_i (ln q_i - ln p_{id_i}) +
+ *              rest (ln rest - ln p_rest), p_rest being the student's probability
+ *              of every index no slot names, summed over those indices (not
+ *              taken as a difference from 1). The last term is left out where
+ *              p_rest = 0.
+ * A slot with q = 0 adds nothing; one with q > 0 and p = 0 makes the loss
+ * +inf. A row without a filled slot (tail == 0: or with teacher -inf in all of
+ * them) has loss 0 and gradient 0. stats receives
+ * 4 floats per row, {m, ln s, ln s_rest, 0}, s_rest = the part of s over the
+ * indices that no slot names (ln s where tail == 0): what
+ * argreduce_distill_backward() needs. 0 <= slots <= ARGR_LOGITS_MAX_SLOTS.
+ */
+argr_status argreduce_distill(const void* x, argr_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                              float temperature, const int64_t* ids, const float* teacher, int32_t slots, int tail,
+                              float* loss, float* stats, const argr_plan* plan, argr_stream stream);
+
+/*
+ * The gradient of sum_r grad_loss[r] * loss[r] with respect to x:
+ *     grad[r, j] = grad_loss / temperature * ((sum q + rest) p_j - q_j          where a slot names j,
+ *                                             (sum q + rest) p_j - rest p_j / p_rest  elsewhere).
+ * stats from argreduce_distill() with the same arguments; grad as in
+ * argreduce_logprobs_backward().
+ */
+argr_status argreduce_distill_backward(const void* x, argr_dtype dtype, int64_t rows, int64_t cols,
+                                       int64_t row_stride, float temperature, const int64_t* ids,
+                                       const float* teacher, int32_t slots, int tail, const float* stats,
+                                       const float* grad_loss, void* grad, int64_t grad_stride,
+                                       const argr_plan* plan, argr_stream stream);
+
+/*
+ * Both in one call, for a training step that knows each row's weight
+ * (grad_loss) before the loss: loss, stats and grad as the two calls above
+ * would give them.
+ */
+argr_status argreduce_distill_step(const void* x, argr_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                                   float temperature, const int64_t* ids, const float* teacher, int32_t slots,
+                                   int tail, const float* grad_loss, float* loss, float* stats, void* grad,
+                                   int64_t grad_stride, const argr_plan* plan, argr_stream stream);
+
+/* The planner of these operators. k: top_k or slots. caps as for argreduce_plan(). */
+argr_status argreduce_logits_plan(argr_logits_op what, int64_t rows, int64_t cols, argr_dtype dtype, int32_t k,
+                                  const argr_caps* caps, argr_plan* out);
 
 /* Properties of `device` as the planner sees them (queried once, cached). */
 argr_status argreduce_device_caps(int device, argr_caps* out);

@@ -18,7 +18,7 @@ from . import _lib
 from ._lib import (ARGR_BF16, ARGR_F16, ARGR_F32, ARGR_F64, ARGR_MAX, ARGR_MIN,  # noqa: F401
                    ARGR_OK, ArgreduceError, DTYPE_CODES, OP_CODES, argr_caps, argr_plan, argreduce_axis_plan,
                    argreduce_cum_plan, argreduce_cum_scratch_bytes,
-                   argreduce_device_caps,
+                   argreduce_device_caps, argreduce_logits_plan,
                    argreduce_plan, argreduce_plan_check, argreduce_plan_scratch_bytes, argreduce_read_error,
                    argreduce_scratch_bytes,
                    argreduce_scratch_init, argreduce_status_string, argreduce_version, load, make_caps)
@@ -29,6 +29,8 @@ __all__ = [
     "argmax", "argmin", "argreduce_with_plan", "argreduce_plan", "argreduce_plan_check", "argreduce_scratch_bytes",
     "argreduce_scratch_init", "argreduce_read_error", "argreduce_device_caps", "argreduce_status_string",
     "argreduce_version", "argreduce_plan_scratch_bytes", "ArgreduceError", "Scratch", "make_caps",
+    "token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward", "distill_topk_step",
+    "TokenLogprobs", "DistillLoss", "argreduce_logits_plan",
 ]
 
 
@@ -317,3 +319,16 @@ def argmax(x, **kw):
 
 def argmin(x, **kw):
     return argreduce(x, "min", **kw)[0]
+
+
+_LOGITS = ("token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward", "distill_topk_step",
+           "TokenLogprobs", "DistillLoss")
+
+
+def __getattr__(name):
+    """The vocabulary-row operators, loaded with torch when first asked for."""
+    if name in _LOGITS:
+        from . import logits
+        globals().update((n, getattr(logits, n)) for n in _LOGITS)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

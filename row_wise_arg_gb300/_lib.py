@@ -19,6 +19,7 @@ ARGR_MAX, ARGR_MIN, ARGR_MAX_LAST, ARGR_MIN_LAST = 0, 1, 2, 3
 (ARGR_OK, ARGR_EINVAL, ARGR_ESCRATCH, ARGR_EUNSUPPORTED, ARGR_ECUDA, ARGR_ETIMEOUT) = range(6)
 ARGR_PATH_NONE, ARGR_PATH_ROWS, ARGR_PATH_SPLIT, ARGR_PATH_CLUSTER, ARGR_PATH_STREAM, ARGR_PATH_AXIS, \
     ARGR_PATH_CUM, ARGR_PATH_CUM_SPLIT, ARGR_PATH_CUM_STREAM = range(9)
+ARGR_PATH_LOGITS, ARGR_PATH_LOGITS_GRAD = 9, 10
 ARGR_PLAN_PDL = 1
 ARGR_PLAN_BULK = 2
 ARGR_PLAN_TEST_EXPIRE = 4
@@ -33,7 +34,11 @@ DTYPE_CODES = {"f32": ARGR_F32, "f16": ARGR_F16, "bf16": ARGR_BF16, "f64": ARGR_
 OP_CODES = {"max": ARGR_MAX, "min": ARGR_MIN, "max_last": ARGR_MAX_LAST, "min_last": ARGR_MIN_LAST}
 PATH_NAMES = {ARGR_PATH_NONE: "none", ARGR_PATH_ROWS: "rows", ARGR_PATH_SPLIT: "split",
               ARGR_PATH_CLUSTER: "cluster", ARGR_PATH_STREAM: "stream", ARGR_PATH_AXIS: "axis",
-              ARGR_PATH_CUM: "cum", ARGR_PATH_CUM_SPLIT: "cum_split", ARGR_PATH_CUM_STREAM: "cum_stream"}
+              ARGR_PATH_CUM: "cum", ARGR_PATH_CUM_SPLIT: "cum_split", ARGR_PATH_CUM_STREAM: "cum_stream",
+              ARGR_PATH_LOGITS: "logits", ARGR_PATH_LOGITS_GRAD: "logits_grad"}
+LOGITS_CODES = {"logprobs": 0, "logprobs_backward": 1, "distill": 2, "distill_backward": 3, "distill_step": 4}
+LOGITS_MAX_TOP = 128
+LOGITS_MAX_SLOTS = 1024
 
 # Every function the header declares (checked by the tests).
 EXPORTS = (
@@ -42,6 +47,8 @@ EXPORTS = (
     "argreduce_device_caps", "argreduce_status_string", "argreduce_version", "argreduce_noalloc",
     "argreduce_axis", "argreduce_axis_plan", "argreduce_axis_with_plan", "argreduce_cum", "argreduce_cum_plan",
     "argreduce_cum_with_plan", "argreduce_cum_scratch_bytes", "argreduce_plan_check",
+    "argreduce_logprobs", "argreduce_logprobs_backward", "argreduce_distill", "argreduce_distill_backward",
+    "argreduce_distill_step", "argreduce_logits_plan",
 )
 
 
@@ -128,6 +135,17 @@ def load() -> ctypes.CDLL:
         lib.argreduce_cum_scratch_bytes.restype = sz
         lib.argreduce_noalloc.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
         lib.argreduce_noalloc.restype = i32
+        f32, pp = ctypes.c_float, ctypes.POINTER(argr_plan)
+        logits_rows = [vp, i32, i64, i64, i64, f32]
+        lib.argreduce_logprobs.argtypes = logits_rows + [vp, i32, vp, vp, vp, vp, vp, vp, pp, vp]
+        lib.argreduce_logprobs_backward.argtypes = logits_rows + [vp, vp, vp, vp, vp, vp, i64, pp, vp]
+        lib.argreduce_distill.argtypes = logits_rows + [vp, vp, i32, i32, vp, vp, pp, vp]
+        lib.argreduce_distill_backward.argtypes = logits_rows + [vp, vp, i32, i32, vp, vp, vp, i64, pp, vp]
+        lib.argreduce_distill_step.argtypes = logits_rows + [vp, vp, i32, i32, vp, vp, vp, vp, i64, pp, vp]
+        lib.argreduce_logits_plan.argtypes = [i32, i64, i64, i32, i32, ctypes.POINTER(argr_caps), pp]
+        for f in (lib.argreduce_logprobs, lib.argreduce_logprobs_backward, lib.argreduce_distill,
+                  lib.argreduce_distill_backward, lib.argreduce_distill_step, lib.argreduce_logits_plan):
+            f.restype = i32
         lib.argreduce_version.argtypes = []
         lib.argreduce_version.restype = ctypes.c_char_p
         del i64p
@@ -243,6 +261,18 @@ def argreduce_cum_plan(rows: int, cols: int, dtype, op, caps: Optional[argr_caps
 
 def argreduce_cum_scratch_bytes(rows: int, cols: int, dtype, op) -> int:
     return int(load().argreduce_cum_scratch_bytes(rows, cols, _code(DTYPE_CODES, dtype), _code(OP_CODES, op)))
+
+
+def argreduce_logits_plan(what, rows: int, cols: int, dtype, k: int = 0,
+                          caps: Optional[argr_caps] = None) -> argr_plan:
+    """The planner of the vocabulary-row operators: `what` is one of
+    LOGITS_CODES, k the top alternatives or the slots."""
+    p = argr_plan()
+    st = load().argreduce_logits_plan(_code(LOGITS_CODES, what), rows, cols, _code(DTYPE_CODES, dtype), k,
+                                      ctypes.byref(caps) if caps is not None else None, ctypes.byref(p))
+    if st != ARGR_OK:
+        raise ArgreduceError(st, "argreduce_logits_plan")
+    return p
 
 
 def argreduce_plan_scratch_bytes(plan: argr_plan, rows: int) -> int:

@@ -35,8 +35,9 @@ NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-
 SOURCES = ["api.cpp", "plan.cpp", "plan_cum.cpp",
            "kernels_f32.cu", "kernels_f16.cu", "kernels_bf16.cu", "kernels_f64.cu",
            "axis_f32.cu", "axis_f16.cu", "axis_bf16.cu", "axis_f64.cu",
-           "cum_f32.cu", "cum_f16.cu", "cum_bf16.cu", "cum_f64.cu", "cum_i32.cu", "cum_i64.cu", "noalloc.cu"]
-HEADERS = ["device_common.cuh", "kernels_impl.cuh", "internal.h", "tma.cuh", "cum_impl.cuh"]
+           "cum_f32.cu", "cum_f16.cu", "cum_bf16.cu", "cum_f64.cu", "cum_i32.cu", "cum_i64.cu", "noalloc.cu",
+           "logits_api.cpp", "plan_logits.cpp", "logits_f32.cu", "logits_f16.cu", "logits_bf16.cu"]
+HEADERS = ["device_common.cuh", "kernels_impl.cuh", "internal.h", "tma.cuh", "cum_impl.cuh", "logits.h", "logits_impl.cuh"]
 COMPARE_SOURCES = ["compare/cub_argreduce.cu"]
 
 

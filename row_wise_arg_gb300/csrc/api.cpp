@@ -41,6 +41,8 @@ argr_status query_caps(int dev, argr_caps* out) {
     return ARGR_OK;
 }
 
+}  // namespace
+
 argr_status current_caps(argr_caps* out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -49,6 +51,8 @@ argr_status current_caps(argr_caps* out) {
     }
     return query_caps(dev, out);
 }
+
+namespace {
 
 bool valid_dtype(int d) { return d == ARGR_F32 || d == ARGR_F16 || d == ARGR_BF16 || d == ARGR_F64; }
 bool valid_op(int o) { return o == ARGR_MAX || o == ARGR_MIN || o == ARGR_MAX_LAST || o == ARGR_MIN_LAST; }

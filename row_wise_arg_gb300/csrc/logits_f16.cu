@@ -1,0 +1,4 @@
+// Vocabulary-row kernels of one element type.
+#include "logits_impl.cuh"
+
+ARGR_DEFINE_LOGITS(f16, argr::TagF16)

@@ -1,0 +1,49 @@
+// Planner of the vocabulary-row operators: pure host code.
+#include <algorithm>
+#include <climits>
+#include <cstring>
+
+#include "logits.h"
+
+namespace argr {
+namespace {
+
+bool forward(int what) { return what == ARGR_LOGITS_LOGPROBS || what == ARGR_LOGITS_DISTILL || what == ARGR_LOGITS_DISTILL_STEP; }
+
+bool valid_problem(int what, int64_t rows, int64_t cols, int dtype, int k) {
+    return what >= ARGR_LOGITS_LOGPROBS && what <= ARGR_LOGITS_DISTILL_STEP && rows >= 0 && cols >= 1 &&
+           cols <= INT_MAX && k >= 0 && k <= ARGR_LOGITS_MAX_SLOTS &&
+           (dtype == ARGR_F32 || dtype == ARGR_F16 || dtype == ARGR_BF16);
+}
+
+}  // namespace
+
+argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, int k, const argr_caps& caps,
+                             argr_plan* out) {
+    std::memset(out, 0, sizeof(*out));
+    if (dtype == ARGR_F64 || dtype == ARGR_I32 || dtype == ARGR_I64) return ARGR_EUNSUPPORTED;
+    if (!valid_problem(what, rows, cols, dtype, k) || caps.sm_count < 1) return ARGR_EINVAL;
+    if (rows == 0) return ARGR_OK;
+    out->block = 512;
+    out->cluster = 1;
+    out->blocks_per_row = 1;
+    out->flags = ARGR_PLAN_PDL;
+    out->grid_rows = std::min<int64_t>(rows, 1 << 20);
+    out->path = forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD;
+    if (out->path == ARGR_PATH_LOGITS_GRAD) out->blocks_per_row = std::min<int64_t>(4096, (cols + 8191) / 8192);
+    return ARGR_OK;
+}
+
+argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_t cols, int dtype, int k,
+                              const argr_caps& caps) {
+    if (!valid_problem(what, rows, cols, dtype, k) || caps.sm_count < 1) return ARGR_EINVAL;
+    if (p.path != (forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD)) return ARGR_EINVAL;
+    if (p.block < 32 || p.block > 512 || p.block % 32) return ARGR_EINVAL;
+    if (p.flags & ~ARGR_PLAN_PDL) return ARGR_EINVAL;
+    if (p.grid_rows < 1 || p.grid_rows > (1 << 20) || p.blocks_per_row < 1 || p.blocks_per_row > 4096) return ARGR_EINVAL;
+    if (p.cluster != 1) return ARGR_EINVAL;
+    if (p.path == ARGR_PATH_LOGITS && p.blocks_per_row != 1) return ARGR_EINVAL;
+    return ARGR_OK;
+}
+
+}  // namespace argr

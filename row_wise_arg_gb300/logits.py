@@ -1,0 +1,269 @@
+"""Vocabulary rows: log probabilities of given tokens with entropy and top
+alternatives, a distillation loss from a teacher's top logits, and the
+gradients of both (argreduce_logprobs, argreduce_distill and their gradients in
+include/argreduce.h, where the semantics stand).
+
+``logits`` is a CUDA tensor [..., vocab] of float32, float16 or bfloat16, its
+last dimension contiguous and its leading ones evenly spaced (a vocabulary cut
+from padded rows will do). Where gradients are asked for, ``token_logprobs`` and
+``distill_topk`` take part in automatic differentiation: the first gives the
+gradients of logprob, entropy and lse, the second that of the loss, each to the
+logits alone.
+
+A teacher's ``token_logprobs(..., top_k=K)`` gives what ``distill_topk`` takes:
+``top_ids`` as the slots' ids and ``top_logprobs`` as the teacher's values.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from ._lib import ARGR_OK, ArgreduceError
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]  #: [...] log p of the given token, 0 where it is negative; None without tokens
+    entropy: torch.Tensor            #: [...] -sum p log p, in nats
+    lse: torch.Tensor                #: [...] log sum exp(logits / temperature)
+    top_ids: Optional[torch.Tensor]  #: [..., top_k] int64, the largest logits first, ties to the lowest index
+    top_logprobs: Optional[torch.Tensor]  #: [..., top_k] their log p
+    stats: torch.Tensor              #: [..., 4] what the backward pass needs: row maximum, log sum, entropy, 0
+
+
+class DistillLoss(NamedTuple):
+    loss: torch.Tensor   #: [...]
+    stats: torch.Tensor  #: [..., 4] what the backward pass needs: row maximum, log sum, log sum of the tail, 0
+
+
+def _rows(x, dtype):
+    """(rows, cols, row stride, type code) of logits."""
+    from . import dtype_code
+    if not x.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
+    code = dtype_code(x, dtype)
+    if code > _lib.ARGR_BF16:
+        raise TypeError("logits must be float32, float16 or bfloat16")
+    n = x.dim()
+    if n == 0:
+        raise ValueError("logits must have at least one dimension")
+    shape = x.shape
+    cols = shape[-1]
+    if cols == 0:
+        raise ValueError("logits must have a vocabulary of at least one")
+    if cols > 1 and x.stride(-1) != 1:
+        raise ValueError("the last dimension of logits must be contiguous")
+    if n == 1:
+        return 1, cols, cols, code
+    if n > 2:
+        try:
+            x = x.view(-1, cols)
+        except RuntimeError:
+            raise ValueError("the leading dimensions of logits must be evenly spaced (make it contiguous)") from None
+    rows = x.shape[0]
+    return rows, cols, x.stride(0) if rows > 1 else cols, code
+
+
+def _arg(t, what, dtype, shape, like):
+    """Data pointer of an argument that must be a contiguous tensor of this type and shape on the logits' device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor on {like.device}")
+    return t.data_ptr()
+
+
+def _stream(x, stream):
+    from . import _stream_ptr
+    return _stream_ptr(stream, x.get_device()) or None
+
+
+def _plan(plan):
+    return ctypes.byref(plan) if plan is not None else None
+
+
+def _check(st, what):
+    if st != ARGR_OK:
+        raise ArgreduceError(st, what)
+
+
+def _grad_out(x, grad):
+    """The gradient's tensor and its row stride."""
+    if grad is None:
+        grad = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return grad, x.shape[-1]
+    if grad.shape != x.shape or grad.dtype is not x.dtype or grad.device != x.device:
+        raise ValueError("grad must have the shape, type and device of logits")
+    _, _, stride, _ = _rows(grad, "f32" if grad.element_size() == 4 else "bf16")
+    return grad, stride
+
+
+def _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream):
+    rows, cols, stride, code = _rows(x, dtype)
+    lead = x.shape[:-1]
+    tok = _arg(tokens, "tokens", torch.int64, lead, x)
+    if not 0 <= top_k <= min(cols, _lib.LOGITS_MAX_TOP):
+        raise ValueError(f"top_k must be in [0, {min(cols, _lib.LOGITS_MAX_TOP)}], got {top_k}")
+    dev = x.device
+    logprob, entropy, lse = torch.empty((3,) + lead, dtype=torch.float32, device=dev).unbind(0)
+    stats = torch.empty(lead + (4,), dtype=torch.float32, device=dev)
+    ids = top = None
+    if top_k:
+        ids = torch.empty(lead + (top_k,), dtype=torch.int64, device=dev)
+        top = torch.empty(lead + (top_k,), dtype=torch.float32, device=dev)
+    st = _lib.load().argreduce_logprobs(
+        x.data_ptr(), code, rows, cols, stride, temperature, tok, top_k,
+        logprob.data_ptr() if tok is not None else None, entropy.data_ptr(), lse.data_ptr(),
+        ids.data_ptr() if top_k else None, top.data_ptr() if top_k else None, stats.data_ptr(), _plan(plan),
+        _stream(x, stream))
+    _check(st, "argreduce_logprobs")
+    return logprob if tok is not None else None, entropy, lse, ids, top, stats
+
+
+class _TokenLogprobsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, tokens, top_k, temperature, dtype, plan, stream):
+        out = _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream)
+        ctx.save_for_backward(x, tokens, out[5])
+        ctx.temperature, ctx.dtype, ctx.stream = temperature, dtype, stream
+        ctx.mark_non_differentiable(*(t for t in out[3:] if t is not None))
+        ctx.set_materialize_grads(False)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_logprob, grad_entropy, grad_lse, *_):
+        x, tokens, stats = ctx.saved_tensors
+        if grad_logprob is None and grad_entropy is None and grad_lse is None:
+            return (None,) * 7
+        given = [None if g is None else g.contiguous() for g in (grad_logprob, grad_entropy, grad_lse)]
+        return (token_logprobs_backward(x, tokens, stats, *given, temperature=ctx.temperature, dtype=ctx.dtype,
+                                        stream=ctx.stream),) + (None,) * 6
+
+
+def token_logprobs(logits, tokens=None, top_k: int = 0, *, temperature: float = 1.0, dtype: Optional[str] = None,
+                   plan=None, stream=None) -> TokenLogprobs:
+    """For each row of logits: log p of its token (``tokens``, int64 of the
+    leading shape; negative: none), the entropy, the log of the sum of
+    exponentials, and the ``top_k`` (at most 128) likeliest tokens with their
+    log p. Runs on ``stream`` (default: torch's current stream) without
+    synchronising."""
+    if torch.is_grad_enabled() and logits.requires_grad:
+        return TokenLogprobs(*_TokenLogprobsFunction.apply(logits, tokens, top_k, temperature, dtype, plan, stream))
+    return TokenLogprobs(*_forward_logprobs(logits, tokens, top_k, temperature, dtype, plan, stream))
+
+
+def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entropy=None, grad_lse=None, *,
+                            temperature: float = 1.0, grad=None, dtype: Optional[str] = None, plan=None, stream=None):
+    """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy +
+    grad_lse * lse) to the logits; ``stats`` from ``token_logprobs`` of the
+    same logits and temperature. ``grad``: a tensor for the result, which may be
+    ``logits`` itself (then overwritten)."""
+    rows, cols, stride, code = _rows(logits, dtype)
+    lead = logits.shape[:-1]
+    f32 = torch.float32
+    tok = _arg(tokens, "tokens", torch.int64, lead, logits)
+    if tok is None and grad_logprob is not None:
+        raise ValueError("grad_logprob needs tokens")
+    args = (tok, _arg(stats, "stats", f32, lead + (4,), logits), _arg(grad_logprob, "grad_logprob", f32, lead, logits),
+            _arg(grad_entropy, "grad_entropy", f32, lead, logits), _arg(grad_lse, "grad_lse", f32, lead, logits))
+    grad, grad_stride = _grad_out(logits, grad)
+    _check(_lib.load().argreduce_logprobs_backward(logits.data_ptr(), code, rows, cols, stride, temperature, *args,
+                                                   grad.data_ptr(), grad_stride, _plan(plan),
+                                                   _stream(logits, stream)), "argreduce_logprobs_backward")
+    return grad
+
+
+def _slots(x, ids, teacher):
+    """(ids, teacher, slots) of the C calls."""
+    lead = x.shape[:-1]
+    if ids.dim() != x.dim() or ids.shape[:-1] != lead:
+        raise ValueError(f"ids must have shape {tuple(lead)} + (slots,), got {tuple(ids.shape)}")
+    slots = ids.shape[-1]
+    if slots > _lib.LOGITS_MAX_SLOTS:
+        raise ValueError(f"at most {_lib.LOGITS_MAX_SLOTS} slots, got {slots}")
+    return (_arg(ids, "ids", torch.int64, ids.shape, x), _arg(teacher, "teacher", torch.float32, ids.shape, x), slots)
+
+
+def _forward_distill(x, ids, teacher, temperature, tail, dtype, plan, stream):
+    rows, cols, stride, code = _rows(x, dtype)
+    i, t, slots = _slots(x, ids, teacher)
+    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    stats = torch.empty(x.shape[:-1] + (4,), dtype=torch.float32, device=x.device)
+    _check(_lib.load().argreduce_distill(x.data_ptr(), code, rows, cols, stride, temperature, i, t, slots, bool(tail),
+                                         loss.data_ptr(), stats.data_ptr(), _plan(plan), _stream(x, stream)),
+           "argreduce_distill")
+    return loss, stats
+
+
+class _DistillFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, ids, teacher, temperature, tail, dtype, plan, stream):
+        loss, stats = _forward_distill(x, ids, teacher, temperature, tail, dtype, plan, stream)
+        ctx.save_for_backward(x, ids, teacher, stats)
+        ctx.given = dict(temperature=temperature, tail=tail, dtype=dtype, stream=stream)
+        ctx.mark_non_differentiable(stats)
+        return loss, stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss, _):
+        x, ids, teacher, stats = ctx.saved_tensors
+        return (distill_topk_backward(x, ids, teacher, stats, grad_loss.contiguous(), **ctx.given),) + (None,) * 7
+
+
+def distill_topk(logits, ids, teacher, *, temperature: float = 1.0, tail: bool = False, dtype: Optional[str] = None,
+                 plan=None, stream=None) -> DistillLoss:
+    """Loss of a student's logits against a teacher's top ones, for each row:
+    ``ids`` [..., slots] int64 names distinct tokens (negative: an empty slot),
+    ``teacher`` [..., slots] float32 holds the teacher's logits for them, whose
+    softmax (at ``temperature``) over the slots is taught, or, with ``tail``,
+    the teacher's log probabilities, taught together with what they leave of 1
+    as one more outcome. Sums over rows, and a factor of temperature ** 2 where
+    one is wanted, are the caller's."""
+    if torch.is_grad_enabled() and logits.requires_grad:
+        return DistillLoss(*_DistillFunction.apply(logits, ids, teacher, temperature, tail, dtype, plan, stream))
+    return DistillLoss(*_forward_distill(logits, ids, teacher, temperature, tail, dtype, plan, stream))
+
+
+def distill_topk_backward(logits, ids, teacher, stats, grad_loss, *, temperature: float = 1.0, tail: bool = False,
+                          grad=None, dtype: Optional[str] = None, plan=None, stream=None):
+    """The gradient of sum(grad_loss * loss) to the logits; ``stats`` from
+    ``distill_topk`` with the same arguments. ``grad`` as in
+    ``token_logprobs_backward``."""
+    rows, cols, stride, code = _rows(logits, dtype)
+    lead = logits.shape[:-1]
+    i, t, slots = _slots(logits, ids, teacher)
+    st = _arg(stats, "stats", torch.float32, lead + (4,), logits)
+    g = _arg(grad_loss, "grad_loss", torch.float32, lead, logits)
+    grad, grad_stride = _grad_out(logits, grad)
+    _check(_lib.load().argreduce_distill_backward(logits.data_ptr(), code, rows, cols, stride, temperature, i, t,
+                                                  slots, bool(tail), st, g, grad.data_ptr(), grad_stride,
+                                                  _plan(plan), _stream(logits, stream)), "argreduce_distill_backward")
+    return grad
+
+
+def distill_topk_step(logits, ids, teacher, grad_loss, *, temperature: float = 1.0, tail: bool = False, grad=None,
+                      dtype: Optional[str] = None, plan=None, stream=None):
+    """(loss, gradient) in one call, for a training step that knows each row's
+    weight ``grad_loss`` beforehand: what ``distill_topk`` and
+    ``distill_topk_backward`` would give."""
+    rows, cols, stride, code = _rows(logits, dtype)
+    lead = logits.shape[:-1]
+    i, t, slots = _slots(logits, ids, teacher)
+    g = _arg(grad_loss, "grad_loss", torch.float32, lead, logits)
+    grad, grad_stride = _grad_out(logits, grad)
+    loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
+    stats = torch.empty(lead + (4,), dtype=torch.float32, device=logits.device)
+    _check(_lib.load().argreduce_distill_step(logits.data_ptr(), code, rows, cols, stride, temperature, i, t, slots,
+                                              bool(tail), g, loss.data_ptr(), stats.data_ptr(), grad.data_ptr(),
+                                              grad_stride, _plan(plan), _stream(logits, stream)),
+           "argreduce_distill_step")
+    return loss, grad
