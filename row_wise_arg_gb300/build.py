@@ -37,7 +37,8 @@ SOURCES = ["api.cpp", "plan.cpp", "plan_cum.cpp",
            "axis_f32.cu", "axis_f16.cu", "axis_bf16.cu", "axis_f64.cu",
            "cum_f32.cu", "cum_f16.cu", "cum_bf16.cu", "cum_f64.cu", "cum_i32.cu", "cum_i64.cu", "noalloc.cu",
            "logits_api.cpp", "plan_logits.cpp", "logits_f32.cu", "logits_f16.cu", "logits_bf16.cu"]
-HEADERS = ["device_common.cuh", "kernels_impl.cuh", "internal.h", "tma.cuh", "cum_impl.cuh", "logits.h", "logits_impl.cuh"]
+HEADERS = ["device_common.cuh", "kernels_impl.cuh", "internal.h", "tma.cuh", "cum_impl.cuh", "logits.h", "logits_common.cuh",
+           "logits_forward.cuh", "logits_grad.cuh", "logits_impl.cuh"]
 COMPARE_SOURCES = ["compare/cub_argreduce.cu"]
 
 

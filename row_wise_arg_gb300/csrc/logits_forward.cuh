@@ -1,0 +1,593 @@
+// Forward passes over vocabulary rows: log probabilities with entropy and top
+// alternatives, and the distillation loss. One cluster of C CTAs (C = 1: one
+// CTA) per row reads the row once.
+//
+// A row is cut into groups of 64 bytes: the 32-byte aligned body, with a head
+// and a tail of less than a group around it. Thread t of a CTA takes the groups t,
+// t + blockDim, ... of its CTA's range, loads the next one (two 32-byte loads)
+// while it adds up the current one, and keeps (m, s, t) in registers: the
+// group's largest element first, then one pass of packed binary32 arithmetic
+// against a reference that only a larger group maximum moves.
+//
+// Top alternatives cost the pass one shared-memory word per group, its largest
+// element. Groups are contiguous, so in the order (largest element, position)
+// the k first groups hold the k first elements: an element of any other group
+// comes after the largest elements of k groups. A threshold that k of the
+// threads' own largest elements reach (found bit by bit with barrier counts)
+// picks the groups, usually hardly more than k of them; their elements are read
+// again (from L2) and the few that reach the threshold are ranked by counting. Where ties
+// make more groups reach it, the k first groups are found exactly.
+#pragma once
+
+#include "logits_common.cuh"
+
+namespace argr {
+
+constexpr int kFwdMaxBlock = 512;
+constexpr int kGroupBytes = 64;
+constexpr int kSegGroups = 8192;  // groups of a CTA's range that are handled at a time
+constexpr int kListGroups = 1024; // groups picked by a threshold, at most
+constexpr int kRankMax = 512;     // candidates ranked by counting, at most
+
+template <class Tag> constexpr int kGroupElems = kGroupBytes / static_cast<int>(sizeof(typename Tag::raw));
+
+template <class Tag>
+struct Group {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const typename Tag::raw* p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
+                           "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
+                         : "l"(reinterpret_cast<const char*>(p) + 32 * h));
+    }
+    // Elements 2i and 2i + 1 of a word pair (binary32) or of word i (16 bits).
+    __device__ __forceinline__ void pair(int i, float& lo, float& hi) const {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+            lo = __uint_as_float(w[2 * i]);
+            hi = __uint_as_float(w[2 * i + 1]);
+        } else if constexpr (std::is_same<Tag, TagBF16>::value) {
+            lo = __uint_as_float(w[i] << 16);
+            hi = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            lo = f.x;
+            hi = f.y;
+        }
+    }
+    // The largest element, NaN if there is no other.
+    __device__ __forceinline__ float largest() const {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+            float m = __uint_as_float(w[0]);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+            return m;
+        } else {
+            uint32_t m = w[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                if constexpr (std::is_same<Tag, TagBF16>::value) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+                else asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+            }
+            return fmaxf(Tag::widen(static_cast<uint16_t>(m & 0xffffu)), Tag::widen(static_cast<uint16_t>(m >> 16)));
+        }
+    }
+    // Put -inf in the place of the elements whose bits are set.
+    __device__ __forceinline__ void drop(unsigned bits) {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (bits >> i & 1u) w[i] = 0xff800000u;
+        } else {
+            constexpr uint32_t ninf = std::is_same<Tag, TagBF16>::value ? 0xff80u : 0xfc00u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (bits >> (2 * i) & 1u) w[i] = (w[i] & 0xffff0000u) | ninf;
+                if (bits >> (2 * i + 1) & 1u) w[i] = (w[i] & 0xffffu) | ninf << 16;
+            }
+        }
+    }
+};
+
+// Add a group whose largest element is `big`. Without ENT, t is left alone (and
+// elements of -inf need no bound: exp2 of -inf is 0).
+template <class Tag, bool ENT>
+__device__ __forceinline__ void add_group(SoftSum& c, const Group<Tag>& g, float big, float scale2) {
+    if (big > c.m) {
+        if constexpr (ENT) c.rebase(big, scale2);
+        else {
+            c.s *= ex2((c.m - big) * scale2);
+            c.m = big;
+        }
+    }
+    const f32x2 minus = pack2(-c.m, -c.m), scale = pack2(scale2, scale2);
+    f32x2 s = 0, t = 0;
+#pragma unroll
+    for (int i = 0; i < kGroupElems<Tag> / 2; ++i) {
+        float lo, hi;
+        g.pair(i, lo, hi);
+        unpack2(mul2(add2(pack2(lo, hi), minus), scale), lo, hi);
+        if constexpr (ENT) {
+            lo = max_nan(lo, kYMin);
+            hi = max_nan(hi, kYMin);
+        }
+        const f32x2 e = pack2(ex2(lo), ex2(hi));
+        s = add2(s, e);
+        if constexpr (ENT) t = fma2(e, pack2(lo, hi), t);
+    }
+    float a, b;
+    unpack2(s, a, b);
+    c.s += a + b;
+    if constexpr (ENT) {
+        unpack2(t, a, b);
+        c.t += a + b;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A CTA's part of a row, and a segment of it. Slot i of a segment's groups is its
+// head (i = 0, may be empty), group i - 1 of its body, or its tail (i = body + 1,
+// may be empty); positions are elements of the row.
+// ---------------------------------------------------------------------------
+template <class Tag>
+struct Segment {
+    int head_lo, body_lo, body, tail_lo, tail_hi;  // [head_lo, body_lo) head, [tail_lo, tail_hi) tail
+    __device__ __forceinline__ int slots() const { return body + 2; }
+    __device__ __forceinline__ void range(int i, int& lo, int& n) const {
+        lo = i == 0 ? head_lo : body_lo + (i - 1) * kGroupElems<Tag>;
+        n = i == 0 ? body_lo - head_lo : i <= body ? kGroupElems<Tag> : tail_hi - tail_lo;
+    }
+};
+
+template <class Tag>
+struct Part {
+    int align;         // elements before the first 32-byte boundary
+    int first, count;  // body groups of this CTA
+    int cols;
+    bool is_first, is_last;
+
+    __device__ __forceinline__ Part(const typename Tag::raw* row, int n, int rank, int ranks) {
+        const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 31u);
+        align = static_cast<int>(((32u - off) & 31u) / sizeof(typename Tag::raw));
+        if (align > n) align = n;
+        const int groups = (n - align) / kGroupElems<Tag>;
+        first = static_cast<int>(static_cast<int64_t>(groups) * rank / ranks);
+        count = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / ranks) - first;
+        cols = n;
+        is_first = rank == 0;
+        is_last = rank == ranks - 1;
+    }
+    __device__ __forceinline__ Segment<Tag> segment(int at) const {
+        Segment<Tag> s;
+        s.body = count - at < kSegGroups ? count - at : kSegGroups;
+        s.body_lo = align + (first + at) * kGroupElems<Tag>;
+        s.head_lo = is_first && at == 0 ? 0 : s.body_lo;
+        s.tail_lo = s.body_lo + s.body * kGroupElems<Tag>;
+        s.tail_hi = is_last && at + s.body == count ? cols : s.tail_lo;
+        return s;
+    }
+};
+
+// One pass over a segment. TOP: each slot's largest element goes to big[slot]
+// (order32, 0 for an empty slot), the thread's to `most`. DROP: the elements whose
+// bits are set in named[] (kGroupElems bits per slot) are left out.
+template <class Tag, bool ENT, bool TOP, bool DROP>
+__device__ __forceinline__ void scan_segment(SoftSum& c, const typename Tag::raw* row, const Segment<Tag>& sg,
+                                             float scale2, unsigned* big, const void* named, unsigned& most) {
+    using Bits = std::conditional_t<kGroupElems<Tag> == 32, uint32_t, uint16_t>;
+    const Bits* bits = static_cast<const Bits*>(named);
+    const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
+    const typename Tag::raw* body = row + sg.body_lo;
+    Group<Tag> a, b;
+    int g = t;
+    if (g < sg.body) a.load(body + static_cast<int64_t>(g) * kGroupElems<Tag>);
+    // the ragged ends, an element per lane: the head by the first warp, the tail by the last
+    if (warp == 0 || warp == (nt >> 5) - 1) {
+#pragma unroll
+        for (int end = 0; end < 2; ++end) {
+            if (warp != (end ? (nt >> 5) - 1 : 0)) continue;
+            const int slot = end ? sg.body + 1 : 0;
+            const int lo = end ? sg.tail_lo : sg.head_lo, n = end ? sg.tail_hi - sg.tail_lo : sg.body_lo - sg.head_lo;
+            unsigned o = 0;
+            if (lane < n) {
+                const float x = widen_elem<Tag>(ld_scalar(row + lo + lane));
+                bool in = true;
+                if constexpr (DROP) in = !(bits[slot] >> lane & 1u);
+                if (in) c.add(x, scale2);
+                o = order32(x);
+            }
+            if constexpr (TOP) {
+                o = __reduce_max_sync(0xffffffffu, o);
+                if (lane == 0) {
+                    big[slot] = o;
+                    if (o > most) most = o;
+                }
+            }
+        }
+    }
+    const auto use = [&](Group<Tag>& v, int at) {
+        if constexpr (DROP) {
+            const unsigned d = bits[at + 1];
+            if (d) v.drop(d);
+        }
+        const float m = v.largest();
+        if constexpr (TOP) {
+            const unsigned o = order32(m);
+            big[at + 1] = o;
+            if (o > most) most = o;
+        }
+        add_group<Tag, ENT>(c, v, m, scale2);
+    };
+    while (g < sg.body) {
+        int next = g + nt;
+        if (next < sg.body) b.load(body + static_cast<int64_t>(next) * kGroupElems<Tag>);
+        use(a, g);
+        g = next;
+        if (g >= sg.body) break;
+        next = g + nt;
+        if (next < sg.body) a.load(body + static_cast<int64_t>(next) * kGroupElems<Tag>);
+        use(b, g);
+        g = next;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Top alternatives.
+// ---------------------------------------------------------------------------
+struct TopShared {
+    unsigned* big;              // a segment's slots
+    unsigned short* list;       // kListGroups slots picked
+    unsigned long long* cand;   // room candidates
+    unsigned long long* best;   // 2 * ARGR_LOGITS_MAX_TOP keys: the best so far, in order, and a spare
+    int* count;                 // 2 counters
+    int room;
+};
+
+// Sum of an int over the CTA, in every thread.
+__device__ __forceinline__ int block_count(int v, int* slot) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if (threadIdx.x == 0) *slot = 0;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0 && v) atomicAdd(slot, v);
+    __syncthreads();
+    return *slot;
+}
+
+// The k largest of n distinct keys (0: none), in order, into out[0, min(k, n)).
+// Contains barriers; src is complete for every thread beforehand.
+__device__ __forceinline__ void rank_keys(const unsigned long long* src, int n, int k, unsigned long long* out,
+                                          unsigned long long* spare, int* count) {
+    const int t = threadIdx.x, nt = blockDim.x;
+    if (n > kRankMax && n > k) {
+        // the k-th largest key, bit by bit; then only the keys that reach it
+        unsigned long long at = 0;
+        for (int b = 63; b >= 0; --b) {
+            const unsigned long long trial = at | 1ull << b;
+            int mine = 0;
+            for (int i = t; i < n; i += nt) mine += src[i] >= trial;
+            const int m = block_count(mine, count);
+            if (m >= k) at = trial;
+            if (m == k) break;
+        }
+        __syncthreads();
+        if (t == 0) *count = 0;
+        __syncthreads();
+        for (int i = t; i < n; i += nt)
+            if (src[i] >= at && src[i] != 0) {
+                const int p = atomicAdd(count, 1);
+                if (p < k) spare[p] = src[i];
+            }
+        __syncthreads();
+        src = spare;
+        n = *count < k ? *count : k;
+    }
+    for (int i = t; i < n; i += nt) {
+        const unsigned long long key = src[i];
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += src[j] > key;
+        if (r < k && key != 0) out[r] = key;
+    }
+    __syncthreads();
+}
+
+// Take a scanned segment into the best keys so far; returns their number. `most`
+// is the thread's largest element of the segment (order32).
+template <class Tag>
+__device__ __forceinline__ int take_segment(const typename Tag::raw* row, const Segment<Tag>& sg, int k, int have,
+                                            unsigned most, const TopShared& sh) {
+    constexpr int E = kGroupElems<Tag>;
+    const int t = threadIdx.x, nt = blockDim.x, lane = t & 31;
+    const int slots = sg.slots();
+    // A value that at least k elements reach (or 1: every element does).
+    unsigned at = 0;
+    for (int b = 31; b >= 0; --b) {
+        const unsigned trial = at | 1u << b;
+        const int n = __syncthreads_count(most >= trial);
+        if (n >= k) {
+            at = trial;
+            if (n <= k + k / 4 + 2) break;
+        }
+    }
+    if (have == k) {
+        const unsigned last = static_cast<unsigned>(sh.best[k - 1] >> 32);
+        if (last > at) at = last;
+    }
+    if (at == 0) at = 1;
+    int cut = slots;  // of the slots whose largest element equals `at`, those up to here
+    for (bool exact = false;; exact = true) {
+        if (exact) {
+            // the k first slots by (largest element, position)
+            at = 0;
+            for (int b = 31; b >= 0; --b) {
+                const unsigned trial = at | 1u << b;
+                int mine = 0;
+                for (int i = t; i < slots; i += nt) mine += sh.big[i] >= trial;
+                if (block_count(mine, sh.count) >= k) at = trial;
+            }
+            int lo = 0, hi = slots - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                int mine = 0;
+                for (int i = t; i < slots; i += nt) mine += sh.big[i] > at || (sh.big[i] == at && i <= mid);
+                if (block_count(mine, sh.count) >= k) hi = mid;
+                else lo = mid + 1;
+            }
+            cut = lo;
+        }
+        __syncthreads();
+        if (t == 0) {
+            sh.count[0] = 0;
+            sh.count[1] = have;
+        }
+        for (int i = t; i < have; i += nt) sh.cand[i] = sh.best[i];
+        __syncthreads();
+        for (int i = t; i < slots; i += nt) {
+            const unsigned o = sh.big[i];
+            if (o > at || (o == at && i <= cut)) {
+                const int p = atomicAdd(&sh.count[0], 1);
+                if (p < kListGroups) sh.list[p] = static_cast<unsigned short>(i);
+            }
+        }
+        __syncthreads();
+        const int picked = sh.count[0];
+        if (picked > kListGroups && !exact) continue;
+        // the picked slots' elements, 32 / E slots per warp at a time
+        for (int p0 = (t >> 5) * (32 / E); p0 < picked; p0 += (nt >> 5) * (32 / E)) {
+            const int p = p0 + lane / E;
+            unsigned long long key = 0;
+            if (p < picked) {
+                int lo, n;
+                sg.range(sh.list[p], lo, n);
+                const int j = lane % E;
+                if (j < n) {
+                    key = order_key(widen_elem<Tag>(ld_scalar(row + lo + j)), lo + j);
+                    if (static_cast<unsigned>(key >> 32) < at) key = 0;
+                }
+            }
+            const unsigned got = __ballot_sync(0xffffffffu, key != 0);
+            int base = 0;
+            if (lane == 0 && got) base = atomicAdd(&sh.count[1], __popc(got));
+            base = __shfl_sync(0xffffffffu, base, 0);
+            const int q = base + __popc(got & ((1u << lane) - 1u));
+            if (key != 0 && q < sh.room) sh.cand[q] = key;
+        }
+        __syncthreads();
+        if (sh.count[1] <= sh.room || exact) break;
+    }
+    const int n = sh.count[1] < sh.room ? sh.count[1] : sh.room;
+    __syncthreads();
+    rank_keys(sh.cand, n, k, sh.best, sh.best + ARGR_LOGITS_MAX_TOP, sh.count);
+    return n < k ? n : k;
+}
+
+// ---------------------------------------------------------------------------
+// Clusters: CTAs hand what they have to CTA 0.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void st_cluster(unsigned addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(unsigned addr, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+constexpr int kMaxRanks = 16;
+
+// Shared memory of the forward kernels past their static part.
+inline __host__ __device__ int cand_room(int k, int group_elems) {
+    const int n = k * group_elems + k;
+    return n < kRankMax ? kRankMax : n;
+}
+
+template <class Tag, bool TOP>
+__global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsProblem pr, float scale2, int ranks,
+                                                                   int seg_slots) {
+    using R = typename Tag::raw;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ float red[96];
+    __shared__ float parts[3 * kMaxRanks];
+    __shared__ float row_m, row_ln_s;
+    __shared__ int count[2];
+    const int t = threadIdx.x;
+    const int rank = static_cast<int>(blockIdx.x % ranks);
+    const int k = pr.top_k;
+    TopShared sh;
+    unsigned long long* gathered = nullptr;  // CTA 0: every CTA's best
+    if constexpr (TOP) {
+        sh.room = cand_room(k, kGroupElems<Tag>);
+        sh.cand = reinterpret_cast<unsigned long long*>(dyn);
+        sh.best = sh.cand + sh.room;
+        gathered = sh.best + 2 * ARGR_LOGITS_MAX_TOP;
+        sh.big = reinterpret_cast<unsigned*>(gathered + (ranks > 1 ? ranks * k : 0));
+        sh.list = reinterpret_cast<unsigned short*>(sh.big + seg_slots);
+        sh.count = count;
+    }
+    grid_dependency_wait();
+    allow_dependents();
+    const int64_t slots = gridDim.x / ranks;
+    for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += slots) {
+        if (ranks > 1) cluster_arrive();  // CTA 0 is running, and done with the row before
+        const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
+        int64_t tok = -1;
+        float tok_x = 0.0f;
+        if (rank == 0 && t == 0 && pr.logprob) {
+            tok = pr.tokens[r];
+            if (tok >= 0 && tok < pr.cols) tok_x = widen_elem<Tag>(ld_scalar(row + tok));
+        }
+        const Part<Tag> part(row, pr.cols, rank, ranks);
+        SoftSum c;
+        int have = 0;
+        for (int at = 0;;) {
+            const Segment<Tag> sg = part.segment(at);
+            SoftSum d;
+            unsigned most = 0;
+            scan_segment<Tag, true, TOP, false>(d, row, sg, scale2, sh.big, nullptr, most);
+            c.join(d, scale2);
+            if constexpr (TOP) {
+                have = take_segment<Tag>(row, sg, k, have, most, sh);
+                __syncthreads();
+            }
+            at += sg.body;
+            if (at >= part.count) break;
+        }
+        c = block_softsum(c, scale2, red);
+        const unsigned long long* best = sh.best;
+        if (ranks > 1) {
+            cluster_wait();
+            if (t == 0) {
+                const unsigned at = cluster_addr(smem_u32(parts), 0);
+                st_cluster(at + 4 * rank, c.m);
+                st_cluster(at + 4 * (kMaxRanks + rank), c.s);
+                st_cluster(at + 4 * (2 * kMaxRanks + rank), c.t);
+            }
+            if constexpr (TOP) {
+                const unsigned at = cluster_addr(smem_u32(gathered), 0) + 8 * rank * k;
+                for (int i = t; i < k; i += blockDim.x) st_cluster(at + 8 * i, i < have ? sh.best[i] : 0ull);
+            }
+            cluster_arrive();
+            cluster_wait();
+            if (rank != 0) continue;
+            if (t < 32) {
+                SoftSum d;
+                if (t < ranks) {
+                    d.m = parts[t];
+                    d.s = parts[kMaxRanks + t];
+                    d.t = parts[2 * kMaxRanks + t];
+                }
+                c = warp_softsum(d, scale2);
+            }
+            if constexpr (TOP) {
+                rank_keys(gathered, ranks * k, k, sh.cand, sh.cand + ARGR_LOGITS_MAX_TOP, count);
+                best = sh.cand;
+            }
+        }
+        if (t == 0) {
+            const float ln_s = c.empty() ? neg_inf() : logf(c.s);
+            const float h = kLn2 * (log2f(c.s) - c.t / c.s);
+            const float entropy = c.empty() ? 0.0f : (h < 0.0f ? 0.0f : h);
+            if (pr.logprob) {
+                float lp = 0.0f;
+                if (tok >= pr.cols) lp = quiet_nan();
+                else if (tok >= 0) lp = c.empty() ? neg_inf() : (tok_x - c.m) / pr.temperature - ln_s;
+                pr.logprob[r] = lp;
+            }
+            if (pr.entropy) pr.entropy[r] = entropy;
+            if (pr.lse) pr.lse[r] = c.empty() ? neg_inf() : c.m / pr.temperature + ln_s;
+            if (pr.stats) pr.stats[r] = make_float4(c.empty() ? neg_inf() : c.m, ln_s, entropy, 0.0f);
+            row_m = c.m;
+            row_ln_s = ln_s;
+        }
+        if constexpr (TOP) {
+            __syncthreads();
+            for (int i = t; i < k; i += blockDim.x) {
+                const unsigned long long key = best[i];
+                const float v = order_value(static_cast<unsigned>(key >> 32));
+                if (pr.top_ids) pr.top_ids[r * k + i] = key_index(key);
+                if (pr.top_logprobs)
+                    pr.top_logprobs[r * k + i] =
+                        row_ln_s == neg_inf() ? neg_inf() : (v - row_m) / pr.temperature - row_ln_s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Distillation. With the tail, the elements that slots name are left out of the
+// pass (a bit per element in shared memory) and added once from the slots, so
+// that the tail's sum is a sum of its own.
+// ---------------------------------------------------------------------------
+template <class Tag, bool TAIL>
+__global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsProblem pr, float scale2, int ranks,
+                                                                  int seg_slots) {
+    using R = typename Tag::raw;
+    constexpr int E = kGroupElems<Tag>;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ float red[96];
+    __shared__ float parts[2 * kMaxRanks];
+    const int t = threadIdx.x;
+    const int rank = static_cast<int>(blockIdx.x % ranks);
+    unsigned* named = reinterpret_cast<unsigned*>(dyn);
+    grid_dependency_wait();
+    allow_dependents();
+    const int64_t row_slots = gridDim.x / ranks;
+    for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += row_slots) {
+        if (ranks > 1) cluster_arrive();
+        const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
+        const int64_t* ids = pr.ids + r * pr.slots;
+        const float* val = pr.teacher + r * pr.slots;
+        const Part<Tag> part(row, pr.cols, rank, ranks);
+        SoftSum c;  // without the tail: the row; with it: the indices that no slot names
+        for (int at = 0;;) {
+            const Segment<Tag> sg = part.segment(at);
+            if constexpr (TAIL) {
+                __syncthreads();
+                for (int i = t; i < (sg.slots() * E + 31) / 32; i += blockDim.x) named[i] = 0u;
+                __syncthreads();
+                for (int i = t; i < pr.slots; i += blockDim.x) {
+                    const int64_t id = ids[i];
+                    if (id < sg.head_lo || id >= sg.tail_hi) continue;
+                    const int j = static_cast<int>(id);
+                    const int bit = j < sg.body_lo    ? j - sg.head_lo
+                                    : j >= sg.tail_lo ? (sg.body + 1) * E + (j - sg.tail_lo)
+                                                      : E + (j - sg.body_lo);
+                    atomicOr(&named[bit >> 5], 1u << (bit & 31));
+                }
+                __syncthreads();
+            }
+            SoftSum d;
+            unsigned most = 0;
+            scan_segment<Tag, false, false, TAIL>(d, row, sg, scale2, nullptr, named, most);
+            d.t = 0.0f;
+            c.join(d, scale2);
+            at += sg.body;
+            if (at >= part.count) break;
+        }
+        c = block_softsum(c, scale2, red);
+        if (ranks > 1) {
+            cluster_wait();
+            if (t == 0) {
+                const unsigned at = cluster_addr(smem_u32(parts), 0);
+                st_cluster(at + 4 * rank, c.m);
+                st_cluster(at + 4 * (kMaxRanks + rank), c.s);
+            }
+            cluster_arrive();
+            cluster_wait();
+            if (rank != 0) continue;
+            if (t < 32) {
+                SoftSum d;
+                if (t < ranks) {
+                    d.m = parts[t];
+                    d.s = parts[kMaxRanks + t];
+                }
+                c = warp_softsum(d, scale2);
+            }
+        }
+        finish_distill<Tag, TAIL>(pr, r, row, ids, val, c, scale2, red);
+    }
+}
+
+}  // namespace argr

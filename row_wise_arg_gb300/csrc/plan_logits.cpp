@@ -8,6 +8,8 @@
 namespace argr {
 namespace {
 
+constexpr int64_t kMaxGridRows = 1 << 24;
+
 bool forward(int what) { return what == ARGR_LOGITS_LOGPROBS || what == ARGR_LOGITS_DISTILL || what == ARGR_LOGITS_DISTILL_STEP; }
 
 bool valid_problem(int what, int64_t rows, int64_t cols, int dtype, int k) {
@@ -24,13 +26,23 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
     if (dtype == ARGR_F64 || dtype == ARGR_I32 || dtype == ARGR_I64) return ARGR_EUNSUPPORTED;
     if (!valid_problem(what, rows, cols, dtype, k) || caps.sm_count < 1) return ARGR_EINVAL;
     if (rows == 0) return ARGR_OK;
+    out->flags = ARGR_PLAN_PDL;
     out->block = 512;
     out->cluster = 1;
     out->blocks_per_row = 1;
-    out->flags = ARGR_PLAN_PDL;
-    out->grid_rows = std::min<int64_t>(rows, 1 << 20);
     out->path = forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD;
-    if (out->path == ARGR_PATH_LOGITS_GRAD) out->blocks_per_row = std::min<int64_t>(4096, (cols + 8191) / 8192);
+    if (out->path == ARGR_PATH_LOGITS_GRAD) {
+        out->grid_rows = std::min<int64_t>(rows, 65535);
+        out->blocks_per_row = std::min<int64_t>(4096, (cols + 8191) / 8192);
+        return ARGR_OK;
+    }
+    const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
+    while (out->cluster < std::min(16, caps.max_cluster) && rows * out->cluster < 4 * caps.sm_count &&
+           groups / (2 * out->cluster) >= 128)
+        out->cluster *= 2;
+    const int64_t per_cta = groups / out->cluster;
+    while (out->block > 32 && out->block > per_cta) out->block /= 2;
+    out->grid_rows = std::min<int64_t>(rows, kMaxGridRows);
     return ARGR_OK;
 }
 
@@ -40,9 +52,14 @@ argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_
     if (p.path != (forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD)) return ARGR_EINVAL;
     if (p.block < 32 || p.block > 512 || p.block % 32) return ARGR_EINVAL;
     if (p.flags & ~ARGR_PLAN_PDL) return ARGR_EINVAL;
-    if (p.grid_rows < 1 || p.grid_rows > (1 << 20) || p.blocks_per_row < 1 || p.blocks_per_row > 4096) return ARGR_EINVAL;
-    if (p.cluster != 1) return ARGR_EINVAL;
-    if (p.path == ARGR_PATH_LOGITS && p.blocks_per_row != 1) return ARGR_EINVAL;
+    if (p.path == ARGR_PATH_LOGITS_GRAD) {
+        if (p.grid_rows < 1 || p.grid_rows > 65535 || p.blocks_per_row < 1 || p.blocks_per_row > 4096 || p.cluster != 1)
+            return ARGR_EINVAL;
+    } else {
+        if (p.grid_rows < 1 || p.grid_rows > kMaxGridRows || p.blocks_per_row != 1) return ARGR_EINVAL;
+        if (p.cluster < 1 || p.cluster > 16 || (p.cluster & (p.cluster - 1))) return ARGR_EINVAL;
+        if (p.cluster > caps.max_cluster) return ARGR_EUNSUPPORTED;
+    }
     return ARGR_OK;
 }
 
