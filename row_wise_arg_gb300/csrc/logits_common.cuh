@@ -122,8 +122,7 @@ __device__ __forceinline__ SoftSum block_softsum(SoftSum c, float scale2, float*
     return warp_softsum(r, scale2);
 }
 
-// Sum and maximum over the CTA, in every thread and in a fixed order. `smem`
-// holds 32 values.
+// Sum over the CTA, in every thread and in a fixed order. `smem` holds 32 values.
 __device__ __forceinline__ float block_sum(float v, float* smem) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -134,17 +133,6 @@ __device__ __forceinline__ float block_sum(float v, float* smem) {
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) r += smem[w];
     return r;
 }
-__device__ __forceinline__ float block_max(float v, float* smem) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = neg_inf();
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) r = fmaxf(r, smem[w]);
-    return r;
-}
-
 // ---------------------------------------------------------------------------
 // Order of the alternatives: larger values first, equal ones (both zeros are
 // equal) by index, NaNs after every number. order32() is larger for an earlier
@@ -197,68 +185,240 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 }
 
 // ---------------------------------------------------------------------------
-// The teacher's side of a row. A filled slot has 0 <= id < cols.
+// Groups: 64 bytes of a row, a thread's unit of work.
 // ---------------------------------------------------------------------------
+constexpr int kGroupBytes = 64;
+constexpr int kSegGroups = 8192;  // groups of a CTA's range that the forward passes handle at a time
+template <class Tag> constexpr int kGroupElems = kGroupBytes / static_cast<int>(sizeof(typename Tag::raw));
+
+template <class Tag>
+struct Group {
+    uint32_t w[16];
+    // 64 bytes at a 32-byte boundary, through the read-only path or, where this kernel may write them, the plain one.
+    template <bool READ_ONLY = true>
+    __device__ __forceinline__ void load(const typename Tag::raw* p) {
+        if constexpr (!READ_ONLY) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
+                               "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
+                             : "l"(reinterpret_cast<const char*>(p) + 32 * h)
+                             : "memory");
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
+                           "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
+                         : "l"(reinterpret_cast<const char*>(p) + 32 * h));
+    }
+    // Elements 2i and 2i + 1 of a word pair (binary32) or of word i (16 bits).
+    __device__ __forceinline__ void pair(int i, float& lo, float& hi) const {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+            lo = __uint_as_float(w[2 * i]);
+            hi = __uint_as_float(w[2 * i + 1]);
+        } else if constexpr (std::is_same<Tag, TagBF16>::value) {
+            lo = __uint_as_float(w[i] << 16);
+            hi = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            lo = f.x;
+            hi = f.y;
+        }
+    }
+    __device__ __forceinline__ void store(typename Tag::raw* p) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[8 * h]),
+                         "r"(w[8 * h + 1]), "r"(w[8 * h + 2]), "r"(w[8 * h + 3]), "r"(w[8 * h + 4]),
+                         "r"(w[8 * h + 5]), "r"(w[8 * h + 6]), "r"(w[8 * h + 7]),
+                         "l"(reinterpret_cast<char*>(p) + 32 * h)
+                         : "memory");
+    }
+    __device__ __forceinline__ void set_pair(int i, float lo, float hi) {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+            w[2 * i] = __float_as_uint(lo);
+            w[2 * i + 1] = __float_as_uint(hi);
+        } else if constexpr (std::is_same<Tag, TagBF16>::value) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+        } else {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+        }
+    }
+    // The largest element, NaN if there is no other.
+    __device__ __forceinline__ float largest() const {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+            float m = __uint_as_float(w[0]);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+            return m;
+        } else {
+            uint32_t m = w[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                if constexpr (std::is_same<Tag, TagBF16>::value) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+                else asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+            }
+            return fmaxf(Tag::widen(static_cast<uint16_t>(m & 0xffffu)), Tag::widen(static_cast<uint16_t>(m >> 16)));
+        }
+    }
+    // Put -inf in the place of the elements whose bits are set.
+    __device__ __forceinline__ void drop(unsigned bits) {
+        if constexpr (std::is_same<Tag, TagF32>::value) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (bits >> i & 1u) w[i] = 0xff800000u;
+        } else {
+            constexpr uint32_t ninf = std::is_same<Tag, TagBF16>::value ? 0xff80u : 0xfc00u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (bits >> (2 * i) & 1u) w[i] = (w[i] & 0xffff0000u) | ninf;
+                if (bits >> (2 * i + 1) & 1u) w[i] = (w[i] & 0xffffu) | ninf << 16;
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// A CTA's part of a row, and a segment of it. Slot i of a segment's groups is its
+// head (i = 0, may be empty), group i - 1 of its body, or its tail (i = body + 1,
+// may be empty); positions are elements of the row.
+// ---------------------------------------------------------------------------
+template <class Tag>
+struct Segment {
+    int head_lo, body_lo, body, tail_lo, tail_hi;  // [head_lo, body_lo) head, [tail_lo, tail_hi) tail
+    __device__ __forceinline__ int slots() const { return body + 2; }
+    __device__ __forceinline__ void range(int i, int& lo, int& n) const {
+        lo = i == 0 ? head_lo : body_lo + (i - 1) * kGroupElems<Tag>;
+        n = i == 0 ? body_lo - head_lo : i <= body ? kGroupElems<Tag> : tail_hi - tail_lo;
+    }
+};
+
+template <class Tag>
+struct Part {
+    int align;         // elements before the first 32-byte boundary
+    int first, count;  // body groups of this CTA
+    int cols;
+    bool is_first, is_last;
+
+    __device__ __forceinline__ Part(const typename Tag::raw* row, int n, int rank, int ranks) {
+        const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 31u);
+        align = static_cast<int>(((32u - off) & 31u) / sizeof(typename Tag::raw));
+        if (align > n) align = n;
+        const int groups = (n - align) / kGroupElems<Tag>;
+        first = static_cast<int>(static_cast<int64_t>(groups) * rank / ranks);
+        count = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / ranks) - first;
+        cols = n;
+        is_first = rank == 0;
+        is_last = rank == ranks - 1;
+    }
+    __device__ __forceinline__ Segment<Tag> segment(int at) const {
+        Segment<Tag> s;
+        s.body = count - at < kSegGroups ? count - at : kSegGroups;
+        s.body_lo = align + (first + at) * kGroupElems<Tag>;
+        s.head_lo = is_first && at == 0 ? 0 : s.body_lo;
+        s.tail_lo = s.body_lo + s.body * kGroupElems<Tag>;
+        s.tail_hi = is_last && at + s.body == count ? cols : s.tail_lo;
+        return s;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The teacher's side of a row, in shared memory.
+// ---------------------------------------------------------------------------
+struct Slots {
+    int id[ARGR_LOGITS_MAX_SLOTS];   // the index named, kNoId or kBadId
+    float v[ARGR_LOGITS_MAX_SLOTS];  // teacher / T without the tail, teacher with it
+    float x[ARGR_LOGITS_MAX_SLOTS];  // the row's element, where it was asked for
+    float shift, total, rest;
+    int any, bad;
+};
+constexpr int kNoId = -1;
+constexpr int kBadId = -2;  // past the row
+
 struct Teacher {
-    float shift;  // ln q = v - shift (v = teacher / T without the tail, teacher with it)
+    float shift;  // ln q = v - shift
     float total;  // sum of q over the filled slots
     float rest;   // what the tail holds
     bool any;     // a slot holds something
     bool bad;     // a slot names an index past the row
-    float inv_t;
-
-    __device__ __forceinline__ float lnq(float teacher) const { return teacher * inv_t - shift; }
 };
 
-__device__ __forceinline__ Teacher read_teacher(const LogitsProblem& pr, int64_t r, float* red) {
+// Fill a row's slots, with the row's elements for those of [lo, hi). A barrier
+// must follow (and come between earlier uses and this).
+template <class Tag>
+__device__ __forceinline__ void load_slots(const LogitsProblem& pr, int64_t r, const typename Tag::raw* row, int lo,
+                                           int hi, Slots& sl) {
     const int64_t* ids = pr.ids + r * pr.slots;
     const float* val = pr.teacher + r * pr.slots;
-    Teacher q;
-    q.inv_t = pr.tail ? 1.0f : 1.0f / pr.temperature;
-    q.shift = 0.0f;
-    bool any = false, bad = false;
-    float top = -FLT_MAX;
+    const float inv_t = pr.tail ? 1.0f : 1.0f / pr.temperature;
     for (int i = threadIdx.x; i < pr.slots; i += blockDim.x) {
         const int64_t id = ids[i];
-        any = any || (id >= 0 && (pr.tail || val[i] != neg_inf()));
-        bad = bad || id >= pr.cols;
-        if (id >= 0) top = fmaxf(top, val[i] * q.inv_t);
+        const int j = id < 0 ? kNoId : id >= pr.cols ? kBadId : static_cast<int>(id);
+        sl.id[i] = j;
+        sl.v[i] = val[i] * inv_t;
+        if (j >= lo && j < hi) sl.x[i] = widen_elem<Tag>(row[j]);
     }
-    q.any = __syncthreads_or(any);
-    q.bad = __syncthreads_or(bad);
-    if (!pr.tail) q.shift = block_max(top, red);
-    float sum = 0.0f;
-    for (int i = threadIdx.x; i < pr.slots; i += blockDim.x)
-        if (ids[i] >= 0) sum += expf(q.lnq(val[i]));
-    sum = block_sum(sum, red);
-    if (pr.tail) {
-        q.total = sum;
-        q.rest = q.any ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
-    } else {
-        q.shift = q.any ? q.shift + logf(sum) : 0.0f;
-        q.total = q.any ? 1.0f : 0.0f;
-        q.rest = 0.0f;
+}
+
+// The teacher's sums over filled slots, by warp 0, for every thread. Contains barriers,
+// the first of them after which the slots are complete.
+__device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, Slots& sl) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        bool any = false, bad = false;
+        float top = -FLT_MAX;
+        for (int i = lane; i < pr.slots; i += 32) {
+            const int id = sl.id[i];
+            any = any || (id != kNoId && (pr.tail || sl.v[i] != neg_inf()));
+            bad = bad || id == kBadId;
+            if (id != kNoId) top = fmaxf(top, sl.v[i]);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float shift = pr.tail ? 0.0f : top;
+        float sum = 0.0f;
+        for (int i = lane; i < pr.slots; i += 32)
+            if (sl.id[i] != kNoId) sum += expf(sl.v[i] - shift);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        any = __any_sync(0xffffffffu, any);
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+            sl.any = any;
+            sl.bad = bad;
+            sl.shift = pr.tail || !any ? 0.0f : shift + logf(sum);
+            sl.total = pr.tail ? sum : any ? 1.0f : 0.0f;
+            sl.rest = pr.tail && any ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
+        }
     }
+    __syncthreads();
+    Teacher q;
+    q.shift = sl.shift;
+    q.total = sl.total;
+    q.rest = sl.rest;
+    q.any = sl.any;
+    q.bad = sl.bad;
     return q;
 }
 
 // The loss of a row from its softmax statistics `c` (in warp 0; with the tail:
 // those of the indices that no slot names), and its entry of stats. All threads
-// of the CTA take part.
+// of the CTA take part; the slots hold every element that they name.
 template <class Tag, bool TAIL>
-__device__ __forceinline__ void finish_distill(const LogitsProblem& pr, int64_t r, const typename Tag::raw* row,
-                                               const int64_t* ids, const float* val, SoftSum c, float scale2,
-                                               float* red) {
+__device__ __forceinline__ void finish_distill(const LogitsProblem& pr, int64_t r, SoftSum c, float scale2,
+                                               float* red, Slots& sl) {
     __shared__ float m_ln_s[3];
     const int t = threadIdx.x;
-    const Teacher q = read_teacher(pr, r, red);
+    const Teacher q = teacher_of(pr, sl);
     SoftSum all = c;
     if constexpr (TAIL) {
         SoftSum d;
-        for (int i = t; i < pr.slots; i += blockDim.x) {
-            const int64_t id = ids[i];
-            if (id >= 0 && id < pr.cols) d.add(widen_elem<Tag>(row[id]), scale2);
-        }
+        for (int i = t; i < pr.slots; i += blockDim.x)
+            if (sl.id[i] >= 0) d.add(sl.x[i], scale2);
         d = block_softsum(d, scale2, red);
         if (t < 32) {
             all.join(d, scale2);
@@ -274,11 +434,10 @@ __device__ __forceinline__ void finish_distill(const LogitsProblem& pr, int64_t 
     const float m = m_ln_s[0], ln_s = m_ln_s[1], ln_rest = m_ln_s[2];
     float loss = 0.0f;
     for (int i = t; i < pr.slots; i += blockDim.x) {
-        const int64_t id = ids[i];
-        if (id < 0 || id >= pr.cols) continue;
-        const float lnq = q.lnq(val[i]);
+        if (sl.id[i] < 0) continue;
+        const float lnq = sl.v[i] - q.shift;
         const float p = expf(lnq);
-        const float lp = ln_s == neg_inf() ? neg_inf() : (widen_elem<Tag>(row[id]) - m) / pr.temperature - ln_s;
+        const float lp = ln_s == neg_inf() ? neg_inf() : (sl.x[i] - m) / pr.temperature - ln_s;
         if (!(p == 0.0f)) loss += p * (lnq - lp);
     }
     loss = block_sum(loss, red);

@@ -24,71 +24,8 @@
 namespace argr {
 
 constexpr int kFwdMaxBlock = 512;
-constexpr int kGroupBytes = 64;
-constexpr int kSegGroups = 8192;  // groups of a CTA's range that are handled at a time
 constexpr int kListGroups = 1024; // groups picked by a threshold, at most
 constexpr int kRankMax = 512;     // candidates ranked by counting, at most
-
-template <class Tag> constexpr int kGroupElems = kGroupBytes / static_cast<int>(sizeof(typename Tag::raw));
-
-template <class Tag>
-struct Group {
-    uint32_t w[16];
-    __device__ __forceinline__ void load(const typename Tag::raw* p) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
-                           "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
-                         : "l"(reinterpret_cast<const char*>(p) + 32 * h));
-    }
-    // Elements 2i and 2i + 1 of a word pair (binary32) or of word i (16 bits).
-    __device__ __forceinline__ void pair(int i, float& lo, float& hi) const {
-        if constexpr (std::is_same<Tag, TagF32>::value) {
-            lo = __uint_as_float(w[2 * i]);
-            hi = __uint_as_float(w[2 * i + 1]);
-        } else if constexpr (std::is_same<Tag, TagBF16>::value) {
-            lo = __uint_as_float(w[i] << 16);
-            hi = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            lo = f.x;
-            hi = f.y;
-        }
-    }
-    // The largest element, NaN if there is no other.
-    __device__ __forceinline__ float largest() const {
-        if constexpr (std::is_same<Tag, TagF32>::value) {
-            float m = __uint_as_float(w[0]);
-#pragma unroll
-            for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(w[i]));
-            return m;
-        } else {
-            uint32_t m = w[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) {
-                if constexpr (std::is_same<Tag, TagBF16>::value) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-                else asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-            }
-            return fmaxf(Tag::widen(static_cast<uint16_t>(m & 0xffffu)), Tag::widen(static_cast<uint16_t>(m >> 16)));
-        }
-    }
-    // Put -inf in the place of the elements whose bits are set.
-    __device__ __forceinline__ void drop(unsigned bits) {
-        if constexpr (std::is_same<Tag, TagF32>::value) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (bits >> i & 1u) w[i] = 0xff800000u;
-        } else {
-            constexpr uint32_t ninf = std::is_same<Tag, TagBF16>::value ? 0xff80u : 0xfc00u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (bits >> (2 * i) & 1u) w[i] = (w[i] & 0xffff0000u) | ninf;
-                if (bits >> (2 * i + 1) & 1u) w[i] = (w[i] & 0xffffu) | ninf << 16;
-            }
-        }
-    }
-};
 
 // Add a group whose largest element is `big`. Without ENT, t is left alone (and
 // elements of -inf need no bound: exp2 of -inf is 0).
@@ -124,50 +61,6 @@ __device__ __forceinline__ void add_group(SoftSum& c, const Group<Tag>& g, float
         c.t += a + b;
     }
 }
-
-// ---------------------------------------------------------------------------
-// A CTA's part of a row, and a segment of it. Slot i of a segment's groups is its
-// head (i = 0, may be empty), group i - 1 of its body, or its tail (i = body + 1,
-// may be empty); positions are elements of the row.
-// ---------------------------------------------------------------------------
-template <class Tag>
-struct Segment {
-    int head_lo, body_lo, body, tail_lo, tail_hi;  // [head_lo, body_lo) head, [tail_lo, tail_hi) tail
-    __device__ __forceinline__ int slots() const { return body + 2; }
-    __device__ __forceinline__ void range(int i, int& lo, int& n) const {
-        lo = i == 0 ? head_lo : body_lo + (i - 1) * kGroupElems<Tag>;
-        n = i == 0 ? body_lo - head_lo : i <= body ? kGroupElems<Tag> : tail_hi - tail_lo;
-    }
-};
-
-template <class Tag>
-struct Part {
-    int align;         // elements before the first 32-byte boundary
-    int first, count;  // body groups of this CTA
-    int cols;
-    bool is_first, is_last;
-
-    __device__ __forceinline__ Part(const typename Tag::raw* row, int n, int rank, int ranks) {
-        const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 31u);
-        align = static_cast<int>(((32u - off) & 31u) / sizeof(typename Tag::raw));
-        if (align > n) align = n;
-        const int groups = (n - align) / kGroupElems<Tag>;
-        first = static_cast<int>(static_cast<int64_t>(groups) * rank / ranks);
-        count = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / ranks) - first;
-        cols = n;
-        is_first = rank == 0;
-        is_last = rank == ranks - 1;
-    }
-    __device__ __forceinline__ Segment<Tag> segment(int at) const {
-        Segment<Tag> s;
-        s.body = count - at < kSegGroups ? count - at : kSegGroups;
-        s.body_lo = align + (first + at) * kGroupElems<Tag>;
-        s.head_lo = is_first && at == 0 ? 0 : s.body_lo;
-        s.tail_lo = s.body_lo + s.body * kGroupElems<Tag>;
-        s.tail_hi = is_last && at + s.body == count ? cols : s.tail_lo;
-        return s;
-    }
-};
 
 // One pass over a segment. TOP: each slot's largest element goes to big[slot]
 // (order32, 0 for an empty slot), the thread's to `most`. DROP: the elements whose
@@ -528,6 +421,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float red[96];
     __shared__ float parts[2 * kMaxRanks];
+    __shared__ Slots sl;
     const int t = threadIdx.x;
     const int rank = static_cast<int>(blockIdx.x % ranks);
     unsigned* named = reinterpret_cast<unsigned*>(dyn);
@@ -537,8 +431,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
     for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += row_slots) {
         if (ranks > 1) cluster_arrive();
         const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
-        const int64_t* ids = pr.ids + r * pr.slots;
-        const float* val = pr.teacher + r * pr.slots;
+        if (TAIL || rank == 0) load_slots<Tag>(pr, r, row, 0, rank == 0 ? pr.cols : 0, sl);
         const Part<Tag> part(row, pr.cols, rank, ranks);
         SoftSum c;  // without the tail: the row; with it: the indices that no slot names
         for (int at = 0;;) {
@@ -548,9 +441,8 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
                 for (int i = t; i < (sg.slots() * E + 31) / 32; i += blockDim.x) named[i] = 0u;
                 __syncthreads();
                 for (int i = t; i < pr.slots; i += blockDim.x) {
-                    const int64_t id = ids[i];
-                    if (id < sg.head_lo || id >= sg.tail_hi) continue;
-                    const int j = static_cast<int>(id);
+                    const int j = sl.id[i];
+                    if (j < sg.head_lo || j >= sg.tail_hi) continue;
                     const int bit = j < sg.body_lo    ? j - sg.head_lo
                                     : j >= sg.tail_lo ? (sg.body + 1) * E + (j - sg.tail_lo)
                                                       : E + (j - sg.body_lo);
@@ -586,7 +478,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
                 c = warp_softsum(d, scale2);
             }
         }
-        finish_distill<Tag, TAIL>(pr, r, row, ids, val, c, scale2, red);
+        finish_distill<Tag, TAIL>(pr, r, c, scale2, red, sl);
     }
 }
 

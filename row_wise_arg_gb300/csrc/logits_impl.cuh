@@ -65,7 +65,8 @@ inline dim3 grad_grid(const argr_plan& p) {
 }
 template <class Tag>
 cudaError_t launch_logprobs_grad_t(const argr_plan& p, const LogitsProblem& pr) {
-    return launch_ex(logprobs_grad_kernel<Tag>, grad_grid(p), dim3(p.block), 1, p, pr.stream, pr, scale2_of(pr));
+    auto kern = pr.grad_entropy ? logprobs_grad_kernel<Tag, true> : logprobs_grad_kernel<Tag, false>;
+    return launch_ex(kern, grad_grid(p), dim3(p.block), 1, p, pr.stream, pr, scale2_of(pr));
 }
 template <class Tag>
 cudaError_t launch_distill_grad_t(const argr_plan& p, const LogitsProblem& pr) {

@@ -32,8 +32,11 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
     out->blocks_per_row = 1;
     out->path = forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD;
     if (out->path == ARGR_PATH_LOGITS_GRAD) {
+        // chunks of about 64 KB (four groups per thread)
+        out->block = 256;
         out->grid_rows = std::min<int64_t>(rows, 65535);
-        out->blocks_per_row = std::min<int64_t>(4096, (cols + 8191) / 8192);
+        const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
+        out->blocks_per_row = std::min<int64_t>(4096, std::max<int64_t>(1, (groups + 1023) / 1024));
         return ARGR_OK;
     }
     const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
@@ -53,6 +56,7 @@ argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_
     if (p.block < 32 || p.block > 512 || p.block % 32) return ARGR_EINVAL;
     if (p.flags & ~ARGR_PLAN_PDL) return ARGR_EINVAL;
     if (p.path == ARGR_PATH_LOGITS_GRAD) {
+        if (p.block > 256) return ARGR_EINVAL;
         if (p.grid_rows < 1 || p.grid_rows > 65535 || p.blocks_per_row < 1 || p.blocks_per_row > 4096 || p.cluster != 1)
             return ARGR_EINVAL;
     } else {
