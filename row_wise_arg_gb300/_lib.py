@@ -19,7 +19,7 @@ ARGR_MAX, ARGR_MIN, ARGR_MAX_LAST, ARGR_MIN_LAST = 0, 1, 2, 3
 (ARGR_OK, ARGR_EINVAL, ARGR_ESCRATCH, ARGR_EUNSUPPORTED, ARGR_ECUDA, ARGR_ETIMEOUT) = range(6)
 ARGR_PATH_NONE, ARGR_PATH_ROWS, ARGR_PATH_SPLIT, ARGR_PATH_CLUSTER, ARGR_PATH_STREAM, ARGR_PATH_AXIS, \
     ARGR_PATH_CUM, ARGR_PATH_CUM_SPLIT, ARGR_PATH_CUM_STREAM = range(9)
-ARGR_PATH_LOGITS, ARGR_PATH_LOGITS_GRAD = 9, 10
+ARGR_PATH_LOGITS, ARGR_PATH_LOGITS_GRAD, ARGR_PATH_LOGITS_STEP, ARGR_PATH_LOGITS_STREAM = 9, 10, 11, 12
 ARGR_PLAN_PDL = 1
 ARGR_PLAN_BULK = 2
 ARGR_PLAN_TEST_EXPIRE = 4
@@ -35,7 +35,9 @@ OP_CODES = {"max": ARGR_MAX, "min": ARGR_MIN, "max_last": ARGR_MAX_LAST, "min_la
 PATH_NAMES = {ARGR_PATH_NONE: "none", ARGR_PATH_ROWS: "rows", ARGR_PATH_SPLIT: "split",
               ARGR_PATH_CLUSTER: "cluster", ARGR_PATH_STREAM: "stream", ARGR_PATH_AXIS: "axis",
               ARGR_PATH_CUM: "cum", ARGR_PATH_CUM_SPLIT: "cum_split", ARGR_PATH_CUM_STREAM: "cum_stream",
-              ARGR_PATH_LOGITS: "logits", ARGR_PATH_LOGITS_GRAD: "logits_grad"}
+              ARGR_PATH_LOGITS: "logits", ARGR_PATH_LOGITS_GRAD: "logits_grad",
+              ARGR_PATH_LOGITS_STEP: "logits_step",
+              ARGR_PATH_LOGITS_STREAM: "logits_stream"}
 LOGITS_CODES = {"logprobs": 0, "logprobs_backward": 1, "distill": 2, "distill_backward": 3, "distill_step": 4}
 LOGITS_MAX_TOP = 128
 LOGITS_MAX_SLOTS = 1024

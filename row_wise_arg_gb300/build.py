@@ -38,7 +38,8 @@ SOURCES = ["api.cpp", "plan.cpp", "plan_cum.cpp",
            "cum_f32.cu", "cum_f16.cu", "cum_bf16.cu", "cum_f64.cu", "cum_i32.cu", "cum_i64.cu", "noalloc.cu",
            "logits_api.cpp", "plan_logits.cpp", "logits_f32.cu", "logits_f16.cu", "logits_bf16.cu"]
 HEADERS = ["device_common.cuh", "kernels_impl.cuh", "internal.h", "tma.cuh", "cum_impl.cuh", "logits.h", "logits_common.cuh",
-           "logits_forward.cuh", "logits_grad.cuh", "logits_impl.cuh"]
+           "logits_forward.cuh", "logits_grad.cuh", "logits_step.cuh",
+           "logits_stream.cuh", "logits_impl.cuh"]
 COMPARE_SOURCES = ["compare/cub_argreduce.cu"]
 
 

@@ -38,6 +38,13 @@ struct LogitsProblem {
     cudaStream_t stream;
 };
 
+// Bytes of a row that a CTA of the step's kernel holds, at most: two CTAs per SM.
+constexpr int64_t kStepMaxChunk = 108 * 1024;
+
+// Shared memory of a CTA of the persistent forward kernel, for the planner: k
+// alternatives (distill == false) or slots, `warps` in all.
+size_t logits_stream_smem(bool distill, int64_t cols, int dtype, int k, int warps, int finishers);
+
 // Planner (plan_logits.cpp): pure host code.
 argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, int k, const argr_caps& caps,
                              argr_plan* out);
@@ -47,6 +54,7 @@ argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_
 #define ARGR_DECLARE_LOGITS(sfx)                                                         \
     cudaError_t launch_logprobs_##sfx(const argr_plan& p, const LogitsProblem& pr);      \
     cudaError_t launch_distill_##sfx(const argr_plan& p, const LogitsProblem& pr);       \
+    cudaError_t launch_distill_step_##sfx(const argr_plan& p, const LogitsProblem& pr);  \
     cudaError_t launch_logprobs_grad_##sfx(const argr_plan& p, const LogitsProblem& pr); \
     cudaError_t launch_distill_grad_##sfx(const argr_plan& p, const LogitsProblem& pr);
 ARGR_DECLARE_LOGITS(f32)

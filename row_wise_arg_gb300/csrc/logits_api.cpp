@@ -198,7 +198,6 @@ argr_status argreduce_distill_step(const void* x, argr_dtype dtype, int64_t rows
     if ((s = check_grad(x, dtype, rows, cols, row_stride, grad, grad_stride)) != ARGR_OK) return s;
     argr_plan p, g;
     if ((s = pick_plan(ARGR_LOGITS_DISTILL_STEP, plan, rows, cols, dtype, slots, &p)) != ARGR_OK) return s;
-    if ((s = pick_plan(ARGR_LOGITS_DISTILL_GRAD, nullptr, rows, cols, dtype, slots, &g)) != ARGR_OK) return s;
     LogitsProblem pr = rows_problem(x, dtype, rows, cols, row_stride, temperature, stats, stream);
     pr.ids = ids;
     pr.teacher = teacher;
@@ -208,6 +207,9 @@ argr_status argreduce_distill_step(const void* x, argr_dtype dtype, int64_t rows
     pr.grad_logprob = grad_loss;
     pr.grad = grad;
     pr.grad_stride = grad_stride;
+    if (p.path == ARGR_PATH_LOGITS_STEP) return ARGR_LOGITS_DISPATCH(launch_distill_step, p, pr);
+    // a row too long for the shared memory of a cluster: the two passes
+    if ((s = pick_plan(ARGR_LOGITS_DISTILL_GRAD, nullptr, rows, cols, dtype, slots, &g)) != ARGR_OK) return s;
     if ((s = ARGR_LOGITS_DISPATCH(launch_distill, p, pr)) != ARGR_OK) return s;
     return ARGR_LOGITS_DISPATCH(launch_distill_grad, g, pr);
 }

@@ -144,6 +144,7 @@ __device__ __forceinline__ unsigned order32(float v) {
     const unsigned u = b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
     return v != v ? 1u : u;
 }
+constexpr unsigned kOrderNegInf = 0x007fffffu;  // order32 of -inf, the least number
 __device__ __forceinline__ float order_value(unsigned u) {
     const unsigned b = u ^ ((u & 0x80000000u) ? 0x80000000u : 0xffffffffu);
     return u == 1u ? quiet_nan() : __uint_as_float(b);
@@ -197,22 +198,18 @@ struct Group {
     // 64 bytes at a 32-byte boundary, through the read-only path or, where this kernel may write them, the plain one.
     template <bool READ_ONLY = true>
     __device__ __forceinline__ void load(const typename Tag::raw* p) {
-        if constexpr (!READ_ONLY) {
+#define ARGR_LOAD32(OP)                                                                            \
+    asm volatile(OP " {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"                                     \
+                 : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),     \
+                   "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])  \
+                 : "l"(reinterpret_cast<const char*>(p) + 32 * h)                                  \
+                 : "memory")
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                             : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
-                               "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
-                             : "l"(reinterpret_cast<const char*>(p) + 32 * h)
-                             : "memory");
-            return;
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (READ_ONLY) ARGR_LOAD32("ld.global.nc.L1::no_allocate.v8.b32");
+            else ARGR_LOAD32("ld.global.L1::no_allocate.v8.b32");
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                         : "=r"(w[8 * h]), "=r"(w[8 * h + 1]), "=r"(w[8 * h + 2]), "=r"(w[8 * h + 3]),
-                           "=r"(w[8 * h + 4]), "=r"(w[8 * h + 5]), "=r"(w[8 * h + 6]), "=r"(w[8 * h + 7])
-                         : "l"(reinterpret_cast<const char*>(p) + 32 * h));
+#undef ARGR_LOAD32
     }
     // Elements 2i and 2i + 1 of a word pair (binary32) or of word i (16 bits).
     __device__ __forceinline__ void pair(int i, float& lo, float& hi) const {
@@ -314,6 +311,9 @@ struct Part {
         is_first = rank == 0;
         is_last = rank == ranks - 1;
     }
+    // The elements of this part, ragged ends included.
+    __device__ __forceinline__ int begin() const { return is_first ? 0 : align + first * kGroupElems<Tag>; }
+    __device__ __forceinline__ int end() const { return is_last ? cols : align + (first + count) * kGroupElems<Tag>; }
     __device__ __forceinline__ Segment<Tag> segment(int at) const {
         Segment<Tag> s;
         s.body = count - at < kSegGroups ? count - at : kSegGroups;
@@ -328,16 +328,6 @@ struct Part {
 // ---------------------------------------------------------------------------
 // The teacher's side of a row, in shared memory.
 // ---------------------------------------------------------------------------
-struct Slots {
-    int id[ARGR_LOGITS_MAX_SLOTS];   // the index named, kNoId or kBadId
-    float v[ARGR_LOGITS_MAX_SLOTS];  // teacher / T without the tail, teacher with it
-    float x[ARGR_LOGITS_MAX_SLOTS];  // the row's element, where it was asked for
-    float shift, total, rest;
-    int any, bad;
-};
-constexpr int kNoId = -1;
-constexpr int kBadId = -2;  // past the row
-
 struct Teacher {
     float shift;  // ln q = v - shift
     float total;  // sum of q over the filled slots
@@ -346,11 +336,30 @@ struct Teacher {
     bool bad;     // a slot names an index past the row
 };
 
+struct Slots {
+    int* id;   // the index named, kNoId or kBadId
+    float* v;  // teacher / T without the tail, teacher with it
+    float* x;  // the row's element, where it was asked for
+    Teacher* sums;
+
+    // In `bytes(n)` bytes of shared memory at p (16-byte aligned).
+    __device__ __forceinline__ Slots(unsigned char* p, int n)
+        : id(reinterpret_cast<int*>(p + sizeof(Teacher) + 12)),
+          v(reinterpret_cast<float*>(id + n)),
+          x(v + n),
+          sums(reinterpret_cast<Teacher*>(p)) {}
+    static __host__ __device__ size_t bytes(int n) {
+        return (sizeof(Teacher) + 12 + 12 * static_cast<size_t>(n) + 15) / 16 * 16;
+    }
+};
+constexpr int kNoId = -1;
+constexpr int kBadId = -2;  // past the row
+
 // Fill a row's slots, with the row's elements for those of [lo, hi). A barrier
 // must follow (and come between earlier uses and this).
 template <class Tag>
 __device__ __forceinline__ void load_slots(const LogitsProblem& pr, int64_t r, const typename Tag::raw* row, int lo,
-                                           int hi, Slots& sl) {
+                                           int hi, const Slots& sl) {
     const int64_t* ids = pr.ids + r * pr.slots;
     const float* val = pr.teacher + r * pr.slots;
     const float inv_t = pr.tail ? 1.0f : 1.0f / pr.temperature;
@@ -363,54 +372,98 @@ __device__ __forceinline__ void load_slots(const LogitsProblem& pr, int64_t r, c
     }
 }
 
-// The teacher's sums over filled slots, by warp 0, for every thread. Contains barriers,
-// the first of them after which the slots are complete.
-__device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, Slots& sl) {
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        bool any = false, bad = false;
-        float top = -FLT_MAX;
-        for (int i = lane; i < pr.slots; i += 32) {
-            const int id = sl.id[i];
-            any = any || (id != kNoId && (pr.tail || sl.v[i] != neg_inf()));
-            bad = bad || id == kBadId;
-            if (id != kNoId) top = fmaxf(top, sl.v[i]);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float shift = pr.tail ? 0.0f : top;
-        float sum = 0.0f;
-        for (int i = lane; i < pr.slots; i += 32)
-            if (sl.id[i] != kNoId) sum += expf(sl.v[i] - shift);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        any = __any_sync(0xffffffffu, any);
-        bad = __any_sync(0xffffffffu, bad);
-        if (lane == 0) {
-            sl.any = any;
-            sl.bad = bad;
-            sl.shift = pr.tail || !any ? 0.0f : shift + logf(sum);
-            sl.total = pr.tail ? sum : any ? 1.0f : 0.0f;
-            sl.rest = pr.tail && any ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
-        }
+// The teacher's sums over filled slots, by one warp, in all its lanes; the slots
+// are complete for it.
+__device__ __forceinline__ Teacher warp_teacher(const LogitsProblem& pr, const Slots& sl) {
+    const int lane = threadIdx.x & 31;
+    bool any = false, bad = false;
+    float top = -FLT_MAX;
+    for (int i = lane; i < pr.slots; i += 32) {
+        const int id = sl.id[i];
+        any = any || (id != kNoId && (pr.tail || sl.v[i] != neg_inf()));
+        bad = bad || id == kBadId;
+        if (id != kNoId) top = fmaxf(top, sl.v[i]);
     }
-    __syncthreads();
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float shift = pr.tail ? 0.0f : top;
+    float sum = 0.0f;
+    for (int i = lane; i < pr.slots; i += 32)
+        if (sl.id[i] != kNoId) sum += expf(sl.v[i] - shift);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     Teacher q;
-    q.shift = sl.shift;
-    q.total = sl.total;
-    q.rest = sl.rest;
-    q.any = sl.any;
-    q.bad = sl.bad;
+    q.any = __any_sync(0xffffffffu, any);
+    q.bad = __any_sync(0xffffffffu, bad);
+    q.shift = pr.tail || !q.any ? 0.0f : shift + logf(sum);
+    q.total = pr.tail ? sum : q.any ? 1.0f : 0.0f;
+    q.rest = pr.tail && q.any ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
     return q;
 }
 
+// The same by warp 0, for every thread of the CTA. Contains barriers, the first of
+// them after which the slots are complete.
+__device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, const Slots& sl) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const Teacher q = warp_teacher(pr, sl);
+        if (threadIdx.x == 0) *sl.sums = q;
+    }
+    __syncthreads();
+    return *sl.sums;
+}
+
+// What a slot adds to the loss of a row with largest element m.
+__device__ __forceinline__ float slot_loss(const LogitsProblem& pr, const Teacher& q, const Slots& sl, int i, float m,
+                                           float ln_s) {
+    if (sl.id[i] < 0) return 0.0f;
+    const float lnq = sl.v[i] - q.shift;
+    const float p = expf(lnq);
+    const float lp = ln_s == neg_inf() ? neg_inf() : (sl.x[i] - m) / pr.temperature - ln_s;
+    return p == 0.0f ? 0.0f : p * (lnq - lp);
+}
+__device__ __forceinline__ float whole_loss(const Teacher& q, float loss, float ln_s, float ln_rest) {
+    if (q.rest > 0.0f && ln_rest != neg_inf()) loss += q.rest * (logf(q.rest) - (ln_rest - ln_s));
+    return (ln_s != ln_s && q.any) || q.bad ? quiet_nan() : loss;
+}
+
+// The loss of a row, in thread 0, from its largest element, ln s and ln s_rest.
+// All threads of the CTA take part; the slots hold every element that they name.
+__device__ __forceinline__ float row_loss(const LogitsProblem& pr, const Teacher& q, const Slots& sl, float m,
+                                          float ln_s, float ln_rest, float* red) {
+    float loss = 0.0f;
+    for (int i = threadIdx.x; i < pr.slots; i += blockDim.x) loss += slot_loss(pr, q, sl, i, m, ln_s);
+    return whole_loss(q, block_sum(loss, red), ln_s, ln_rest);
+}
+
+// The weights of a row's gradient: named elements g (total p - q), others dense p;
+// `none`: every element is `dense`.
+struct GradWeights {
+    float g, total, dense, m, ls2;
+    bool none;
+
+    __device__ __forceinline__ GradWeights(const LogitsProblem& pr, const Teacher& q, float grad_loss, float row_m,
+                                           float ln_s, float ln_rest) {
+        const float rest = ln_rest > neg_inf() ? q.rest : 0.0f;
+        g = grad_loss / pr.temperature;
+        if (q.bad || (ln_s != ln_s && q.any)) g = quiet_nan();
+        none = ln_s == neg_inf() || !q.any;  // nothing is taught, or nothing can be
+        total = q.total + rest;
+        dense = g * (rest > 0.0f ? total - rest * expf(ln_s - ln_rest) : total);
+        if (none) dense = q.bad ? g : 0.0f;
+        m = none ? 0.0f : row_m;
+        ls2 = none ? 0.0f : ln_s * kLog2E;
+    }
+    __device__ __forceinline__ float named(float x, float lnq, float scale2) const {
+        return g * (total * ex2((x - m) * scale2 - ls2) - expf(lnq));
+    }
+};
+
 // The loss of a row from its softmax statistics `c` (in warp 0; with the tail:
-// those of the indices that no slot names), and its entry of stats. All threads
-// of the CTA take part; the slots hold every element that they name.
+// those of the indices that no slot names), and its entry of stats.
 template <class Tag, bool TAIL>
 __device__ __forceinline__ void finish_distill(const LogitsProblem& pr, int64_t r, SoftSum c, float scale2,
-                                               float* red, Slots& sl) {
+                                               float* red, const Slots& sl) {
     __shared__ float m_ln_s[3];
     const int t = threadIdx.x;
     const Teacher q = teacher_of(pr, sl);
@@ -426,26 +479,16 @@ __device__ __forceinline__ void finish_distill(const LogitsProblem& pr, int64_t 
         }
     }
     if (t == 0) {
-        m_ln_s[0] = all.m;
+        m_ln_s[0] = all.empty() ? neg_inf() : all.m;
         m_ln_s[1] = all.empty() ? neg_inf() : logf(all.s);
         m_ln_s[2] = c.empty() ? neg_inf() : logf(c.s);
     }
     __syncthreads();
     const float m = m_ln_s[0], ln_s = m_ln_s[1], ln_rest = m_ln_s[2];
-    float loss = 0.0f;
-    for (int i = t; i < pr.slots; i += blockDim.x) {
-        if (sl.id[i] < 0) continue;
-        const float lnq = sl.v[i] - q.shift;
-        const float p = expf(lnq);
-        const float lp = ln_s == neg_inf() ? neg_inf() : (sl.x[i] - m) / pr.temperature - ln_s;
-        if (!(p == 0.0f)) loss += p * (lnq - lp);
-    }
-    loss = block_sum(loss, red);
+    const float loss = row_loss(pr, q, sl, m, ln_s, ln_rest, red);
     if (t == 0) {
-        if (q.rest > 0.0f && ln_rest != neg_inf()) loss += q.rest * (logf(q.rest) - (ln_rest - ln_s));
-        if ((ln_s != ln_s && q.any) || q.bad) loss = quiet_nan();
         if (pr.loss) pr.loss[r] = loss;
-        if (pr.stats) pr.stats[r] = make_float4(ln_s == neg_inf() ? neg_inf() : m, ln_s, ln_rest, 0.0f);
+        if (pr.stats) pr.stats[r] = make_float4(m, ln_s, ln_rest, 0.0f);
     }
     __syncthreads();
 }

@@ -62,12 +62,25 @@ __device__ __forceinline__ void add_group(SoftSum& c, const Group<Tag>& g, float
     }
 }
 
+// L2 prefetch of a CTA's part: the first kAheadBytes before anything else (also
+// before the wait for the previous grid), then, while the part is read, the bytes kAheadBytes ahead of
+// the loads. DRAM latency is then hidden without registers for loads in flight.
+constexpr int kAheadBytes = 128 * 1024;
+template <class Tag>
+__device__ __forceinline__ void prefetch_part(const LogitsProblem& pr, int64_t r, int rank, int ranks) {
+    using R = typename Tag::raw;
+    const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
+    const Part<Tag> part(row, pr.cols, rank, ranks);
+    prefetch_l2_range(row + part.begin(), row + part.end(), kAheadBytes);
+}
+
 // One pass over a segment. TOP: each slot's largest element goes to big[slot]
 // (order32, 0 for an empty slot), the thread's to `most`. DROP: the elements whose
 // bits are set in named[] (kGroupElems bits per slot) are left out.
 template <class Tag, bool ENT, bool TOP, bool DROP>
 __device__ __forceinline__ void scan_segment(SoftSum& c, const typename Tag::raw* row, const Segment<Tag>& sg,
-                                             float scale2, unsigned* big, const void* named, unsigned& most) {
+                                             float scale2, unsigned* big, const void* named, unsigned& most,
+                                             const typename Tag::raw* part_end) {
     using Bits = std::conditional_t<kGroupElems<Tag> == 32, uint32_t, uint16_t>;
     const Bits* bits = static_cast<const Bits*>(named);
     const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5;
@@ -112,12 +125,22 @@ __device__ __forceinline__ void scan_segment(SoftSum& c, const typename Tag::raw
         }
         add_group<Tag, ENT>(c, v, m, scale2);
     };
+    const auto ahead = [&](int at) {  // one thread, for the CTA's next pass over nt groups
+        if (t != 0) return;
+        const char* p = reinterpret_cast<const char*>(body) + static_cast<int64_t>(at) * kGroupBytes + kAheadBytes;
+        const int64_t left = (reinterpret_cast<const char*>(part_end) - p) & ~static_cast<int64_t>(15);
+        if (left > 0)
+            prefetch_l2_bulk(reinterpret_cast<uintptr_t>(p),
+                             static_cast<unsigned>(left < nt * kGroupBytes ? left : nt * kGroupBytes));
+    };
     while (g < sg.body) {
+        ahead(g);
         int next = g + nt;
         if (next < sg.body) b.load(body + static_cast<int64_t>(next) * kGroupElems<Tag>);
         use(a, g);
         g = next;
         if (g >= sg.body) break;
+        ahead(g);
         next = g + nt;
         if (next < sg.body) a.load(body + static_cast<int64_t>(next) * kGroupElems<Tag>);
         use(b, g);
@@ -318,8 +341,9 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
         sh.list = reinterpret_cast<unsigned short*>(sh.big + seg_slots);
         sh.count = count;
     }
-    grid_dependency_wait();
     allow_dependents();
+    prefetch_part<Tag>(pr, blockIdx.x / ranks, rank, ranks);
+    grid_dependency_wait();
     const int64_t slots = gridDim.x / ranks;
     for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += slots) {
         if (ranks > 1) cluster_arrive();  // CTA 0 is running, and done with the row before
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
             const Segment<Tag> sg = part.segment(at);
             SoftSum d;
             unsigned most = 0;
-            scan_segment<Tag, true, TOP, false>(d, row, sg, scale2, sh.big, nullptr, most);
+            scan_segment<Tag, true, TOP, false>(d, row, sg, scale2, sh.big, nullptr, most, row + part.end());
             c.join(d, scale2);
             if constexpr (TOP) {
                 have = take_segment<Tag>(row, sg, k, have, most, sh);
@@ -421,12 +445,13 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float red[96];
     __shared__ float parts[2 * kMaxRanks];
-    __shared__ Slots sl;
     const int t = threadIdx.x;
     const int rank = static_cast<int>(blockIdx.x % ranks);
-    unsigned* named = reinterpret_cast<unsigned*>(dyn);
-    grid_dependency_wait();
+    const Slots sl(dyn, pr.slots);
+    unsigned* named = reinterpret_cast<unsigned*>(dyn + Slots::bytes(pr.slots));
     allow_dependents();
+    prefetch_part<Tag>(pr, blockIdx.x / ranks, rank, ranks);
+    grid_dependency_wait();
     const int64_t row_slots = gridDim.x / ranks;
     for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += row_slots) {
         if (ranks > 1) cluster_arrive();
@@ -452,7 +477,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
             }
             SoftSum d;
             unsigned most = 0;
-            scan_segment<Tag, false, false, TAIL>(d, row, sg, scale2, nullptr, named, most);
+            scan_segment<Tag, false, false, TAIL>(d, row, sg, scale2, nullptr, named, most, row + part.end());
             d.t = 0.0f;
             c.join(d, scale2);
             at += sg.body;

@@ -15,27 +15,74 @@ namespace argr {
 
 constexpr int kGradMaxBlock = 256;
 
+// Elements [begin, end) of a row whose gradient lies otherwise than x within 32
+// bytes: words of W bytes, W the most that both allow, consecutive threads on
+// consecutive words, kWords loads in flight.
+constexpr int kWords = 4;
+template <class Tag, int W, class F>
+__device__ __forceinline__ void grad_words(const typename Tag::raw* row, typename Tag::raw* out, int begin, int end,
+                                           float m, float ls2, float scale2, F f) {
+    using R = typename Tag::raw;
+    using Word = std::conditional_t<W == 8, uint2, std::conditional_t<W == 4, uint32_t, uint16_t>>;
+    constexpr int N = W / static_cast<int>(sizeof(R));
+    const int t = threadIdx.x, nt = blockDim.x;
+    const auto one = [&](int j) { out[j] = narrow_elem<Tag>(f((widen_elem<Tag>(row[j]) - m) * scale2 - ls2)); };
+    int head = static_cast<int>(((W - (reinterpret_cast<uintptr_t>(row + begin) & (W - 1))) & (W - 1)) / sizeof(R));
+    if (head > end - begin) head = end - begin;
+    const int words = (end - begin - head) / N, done = begin + head + words * N;
+    const R* src = row + begin + head;
+    R* dst = out + begin + head;
+    for (int w0 = 0; w0 < words;) {
+        Word v[kWords];
+        const int left = words - w0;
+#pragma unroll
+        for (int u = 0; u < kWords; ++u)
+            if (t + u * nt < left) v[u] = reinterpret_cast<const Word*>(src)[static_cast<int64_t>(w0) + t + u * nt];
+#pragma unroll
+        for (int u = 0; u < kWords; ++u) {
+            if (t + u * nt >= left) continue;
+            R* e = reinterpret_cast<R*>(&v[u]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) e[i] = narrow_elem<Tag>(f((widen_elem<Tag>(e[i]) - m) * scale2 - ls2));
+            reinterpret_cast<Word*>(dst)[static_cast<int64_t>(w0) + t + u * nt] = v[u];
+        }
+        if (left <= kWords * nt) break;
+        w0 += kWords * nt;
+    }
+    if (t < head) one(begin + t);
+    if (t < end - done) one(done + t);
+}
+
 // A CTA's chunk of a row: f(y) gives the gradient of an element with log2 p = y.
-// x and out may be the same memory. entry(lo, n): called before the elements
-// [lo, lo + n) are written by this thread, then after(lo, n).
+// x and out may be the same memory. before(lo, n) is called before the elements
+// [lo, lo + n) are written by this thread, then after(lo, n); where x and out
+// are not the same memory, they may be called by any thread, after a barrier, for the whole
+// chunk instead.
 template <class Tag, class F, class B, class A>
 __device__ __forceinline__ void grad_chunk(const typename Tag::raw* row, typename Tag::raw* out, int cols, int b,
                                            int nb, float m, float ls2, float scale2, F f, B before, A after) {
-    using R = typename Tag::raw;
     constexpr int E = kGroupElems<Tag>;
     const int t = threadIdx.x, nt = blockDim.x;
     const Part<Tag> part(row, cols, b, nb);
     const int lo = part.align + part.first * E;
-    const int begin = part.is_first ? 0 : lo, end = part.is_last ? cols : lo + part.count * E;
+    const int begin = part.begin(), end = part.end();
+    const unsigned apart = static_cast<unsigned>((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 31u);
+    if (apart != 0) {
+        if ((apart & 7u) == 0) grad_words<Tag, 8>(row, out, begin, end, m, ls2, scale2, f);
+        else if (sizeof(typename Tag::raw) == 4 || (apart & 3u) == 0) grad_words<Tag, 4>(row, out, begin, end, m, ls2, scale2, f);
+        else if constexpr (sizeof(typename Tag::raw) == 2) grad_words<Tag, 2>(row, out, begin, end, m, ls2, scale2, f);
+        __syncthreads();
+        if (t == 0) {
+            before(begin, end - begin);
+            after(begin, end - begin);
+        }
+        return;
+    }
     const auto one = [&](int j) {
         before(j, 1);
         out[j] = narrow_elem<Tag>(f((widen_elem<Tag>(row[j]) - m) * scale2 - ls2));
         after(j, 1);
     };
-    if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 31u) != 0) {
-        for (unsigned i = t; i < static_cast<unsigned>(end - begin); i += nt) one(begin + static_cast<int>(i));
-        return;
-    }
     const f32x2 minus = pack2(-m, -m), scale = pack2(scale2, scale2), shift = pack2(-ls2, -ls2);
     const auto group = [&](Group<Tag>& v, int g) {
 #pragma unroll
@@ -105,7 +152,8 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) logprobs_grad_kernel(const L
 template <class Tag>
 __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const LogitsProblem pr, float scale2) {
     using R = typename Tag::raw;
-    __shared__ Slots sl;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    const Slots sl(dyn, pr.slots);
     grid_dependency_wait();
     allow_dependents();
     const int t = threadIdx.x;
@@ -113,31 +161,22 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const Lo
         const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
         R* out = static_cast<R*>(pr.grad) + r * pr.grad_stride;
         const Part<Tag> part(row, pr.cols, blockIdx.x, gridDim.x);
-        const int lo = part.is_first ? 0 : part.align + part.first * kGroupElems<Tag>;
-        const int hi = part.is_last ? pr.cols : part.align + (part.first + part.count) * kGroupElems<Tag>;
+        const int lo = part.begin(), hi = part.end();
         load_slots<Tag>(pr, r, row, lo, hi, sl);
         const float4 st = pr.stats[r];
         const Teacher q = teacher_of(pr, sl);  // its barriers order the reads above before the stores below
-        const float rest = st.z > neg_inf() ? q.rest : 0.0f;
-        float g = pr.grad_logprob[r] / pr.temperature;
-        if (q.bad || (st.y != st.y && q.any)) g = quiet_nan();
-        const bool none = st.x == neg_inf() || !q.any;  // nothing is taught, or nothing can be
-        const float total = q.total + rest;
-        float dense = g * (rest > 0.0f ? total - rest * expf(st.y - st.z) : total);
-        if (none) dense = q.bad ? g : 0.0f;
-        const float m = none ? 0.0f : st.x, ls2 = none ? 0.0f : st.y * kLog2E;
-        const auto nothing = [](int, int) {};
-        if (none) {
-            const R fill = narrow_elem<Tag>(dense);
+        const GradWeights w(pr, q, pr.grad_logprob[r], st.x, st.y, st.z);
+        if (w.none) {
+            const R fill = narrow_elem<Tag>(w.dense);
             for (unsigned i = t; i < static_cast<unsigned>(hi - lo); i += blockDim.x) out[lo + i] = fill;
         } else {
-            grad_chunk<Tag>(row, out, pr.cols, blockIdx.x, gridDim.x, m, ls2, scale2,
-                            [&](float y) { return dense * ex2(y); }, nothing, nothing);
+            const auto nothing = [](int, int) {};
+            grad_chunk<Tag>(row, out, pr.cols, blockIdx.x, gridDim.x, w.m, w.ls2, scale2,
+                            [&](float y) { return w.dense * ex2(y); }, nothing, nothing);
             __syncthreads();
             for (int i = t; i < pr.slots; i += blockDim.x) {
                 const int j = sl.id[i];
-                if (j >= lo && j < hi)
-                    out[j] = narrow_elem<Tag>(g * (total * ex2((sl.x[i] - m) * scale2 - ls2) - expf(sl.v[i] - q.shift)));
+                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(w.named(sl.x[i], sl.v[i] - q.shift, scale2));
             }
         }
         __syncthreads();

@@ -3,6 +3,8 @@
 
 #include "logits_forward.cuh"
 #include "logits_grad.cuh"
+#include "logits_step.cuh"
+#include "logits_stream.cuh"
 
 namespace argr {
 
@@ -37,8 +39,22 @@ int segment_slots(const argr_plan& p, int cols) {
     return static_cast<int>((groups < kSegGroups ? groups : kSegGroups) + 2 + 3) / 4 * 4;
 }
 
+// The persistent kernel of one mode: p.group finishers per CTA.
+template <class Tag, int MODE>
+cudaError_t launch_stream(const argr_plan& p, const LogitsProblem& pr) {
+    auto kern = logits_stream_kernel<Tag, MODE>;
+    static KernelLaunchCache cache;
+    const size_t smem = StreamLayout(MODE, p.block / 32 - p.group, p.group, kWideElems<Tag>, pr.cols, pr.slots).total;
+    const cudaError_t e = ensure_smem_limit(kern, smem, cache);
+    if (e != cudaSuccess) return e;
+    return launch_ex_smem(kern, dim3(static_cast<unsigned>(p.grid_rows)), dim3(p.block), 1, smem, p, pr.stream, pr,
+                          scale2_of(pr), p.group);
+}
+
 template <class Tag>
 cudaError_t launch_logprobs_t(const argr_plan& p, const LogitsProblem& pr) {
+    if (p.path == ARGR_PATH_LOGITS_STREAM)
+        return pr.top_k ? launch_stream<Tag, kStreamTop>(p, pr) : launch_stream<Tag, kStreamSums>(p, pr);
     const int slots = segment_slots<Tag>(p, pr.cols);
     if (pr.top_k == 0) {
         static KernelLaunchCache cache;
@@ -51,14 +67,27 @@ cudaError_t launch_logprobs_t(const argr_plan& p, const LogitsProblem& pr) {
 }
 template <class Tag>
 cudaError_t launch_distill_t(const argr_plan& p, const LogitsProblem& pr) {
+    if (p.path == ARGR_PATH_LOGITS_STREAM)
+        return pr.tail ? launch_stream<Tag, kStreamLossTail>(p, pr) : launch_stream<Tag, kStreamLoss>(p, pr);
     const int slots = segment_slots<Tag>(p, pr.cols);
+    const size_t smem = Slots::bytes(pr.slots);
     if (!pr.tail) {
         static KernelLaunchCache cache;
-        return launch_forward(distill_kernel<Tag, false>, cache, p, pr, 0, slots);
+        return launch_forward(distill_kernel<Tag, false>, cache, p, pr, smem, slots);
     }
     static KernelLaunchCache cache;
-    return launch_forward(distill_kernel<Tag, true>, cache, p, pr, static_cast<size_t>(slots) * kGroupElems<Tag> / 8 + 16,
-                          slots);
+    return launch_forward(distill_kernel<Tag, true>, cache, p, pr,
+                          smem + static_cast<size_t>(slots) * kGroupElems<Tag> / 8 + 16, slots);
+}
+// The step's kernel holds ceil(groups / C) groups of a row per CTA.
+template <class Tag>
+cudaError_t launch_distill_step_t(const argr_plan& p, const LogitsProblem& pr) {
+    const int groups = (pr.cols / kGroupElems<Tag> + p.cluster - 1) / p.cluster;
+    const int units = groups * (kGroupBytes / 16);
+    const size_t smem = 16 * static_cast<size_t>(units) + Slots::bytes(pr.slots) + (pr.tail ? (units + 15) / 16 * 16 : 0);
+    static KernelLaunchCache caches[2];
+    return pr.tail ? launch_forward(distill_step_kernel<Tag, true>, caches[1], p, pr, smem, units)
+                   : launch_forward(distill_step_kernel<Tag, false>, caches[0], p, pr, smem, units);
 }
 inline dim3 grad_grid(const argr_plan& p) {
     return dim3(static_cast<unsigned>(p.blocks_per_row), static_cast<unsigned>(p.grid_rows < 65535 ? p.grid_rows : 65535));
@@ -70,7 +99,8 @@ cudaError_t launch_logprobs_grad_t(const argr_plan& p, const LogitsProblem& pr) 
 }
 template <class Tag>
 cudaError_t launch_distill_grad_t(const argr_plan& p, const LogitsProblem& pr) {
-    return launch_ex(distill_grad_kernel<Tag>, grad_grid(p), dim3(p.block), 1, p, pr.stream, pr, scale2_of(pr));
+    return launch_ex_smem(distill_grad_kernel<Tag>, grad_grid(p), dim3(p.block), 1, Slots::bytes(pr.slots), p, pr.stream,
+                          pr, scale2_of(pr));
 }
 
 #define ARGR_DEFINE_LOGITS(sfx, Tag)                                                                                 \
@@ -80,6 +110,9 @@ cudaError_t launch_distill_grad_t(const argr_plan& p, const LogitsProblem& pr) {
     }                                                                                                                \
     cudaError_t launch_distill_##sfx(const argr_plan& p, const LogitsProblem& pr) {                                  \
         return launch_distill_t<Tag>(p, pr);                                                                         \
+    }                                                                                                                \
+    cudaError_t launch_distill_step_##sfx(const argr_plan& p, const LogitsProblem& pr) {                             \
+        return launch_distill_step_t<Tag>(p, pr);                                                                    \
     }                                                                                                                \
     cudaError_t launch_logprobs_grad_##sfx(const argr_plan& p, const LogitsProblem& pr) {                            \
         return launch_logprobs_grad_t<Tag>(p, pr);                                                                   \

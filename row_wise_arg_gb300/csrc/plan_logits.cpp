@@ -9,6 +9,7 @@ namespace argr {
 namespace {
 
 constexpr int64_t kMaxGridRows = 1 << 24;
+constexpr size_t kStreamSmem = 110 * 1024;  // two CTAs per SM
 
 bool forward(int what) { return what == ARGR_LOGITS_LOGPROBS || what == ARGR_LOGITS_DISTILL || what == ARGR_LOGITS_DISTILL_STEP; }
 
@@ -18,7 +19,28 @@ bool valid_problem(int what, int64_t rows, int64_t cols, int dtype, int k) {
            (dtype == ARGR_F32 || dtype == ARGR_F16 || dtype == ARGR_BF16);
 }
 
+// Finishing warps that keep up with the streaming ones. Measured (two CTAs per SM): a
+// row streams at 22 bytes per ns; a finish takes about 5 us, 0.1 us per slot of a
+// distillation, or 0.3 us per alternative and 4 ns per 128-byte group of the row.
+// [2048, 202048] bf16, top 20: 171, 156, 159 us with 1, 2, 3 of them; top 64: 236,
+// 190, 180 us; [4096, 65536] bf16, 32 slots: 116, 94 us with 1, 2.
+int stream_finishers(bool distill, int64_t row_bytes, int k) {
+    const double row_us = row_bytes / 22.0e3;
+    const double finish_us = 5.0 + (distill ? 0.1 * k : k > 0 ? 0.3 * k + 0.004 * (row_bytes / 128) : 0.0);
+    return finish_us <= row_us ? 1 : finish_us <= 2 * row_us ? 2 : 3;
+}
+
 }  // namespace
+
+// The most that any mode of the kernel lays out (logits_stream.cuh, StreamLayout).
+size_t logits_stream_smem(bool distill, int64_t cols, int dtype, int k, int warps, int finishers) {
+    const int64_t elems = dtype == ARGR_F32 ? 32 : 64;
+    const size_t slots = static_cast<size_t>(cols / elems + 6);
+    size_t buffer = 16 * static_cast<size_t>(warps) + 16;
+    if (distill) buffer += slots * elems / 8 + 64 + 12 * static_cast<size_t>(k);
+    else if (k > 0) buffer += 4 * slots + slots / 8 + 64 + 128 * static_cast<size_t>(warps);
+    return (finishers + 1) * buffer + (!distill && k > 0 ? finishers * (8 * (1024 + 192) + 2 * 640) : 0);
+}
 
 argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, int k, const argr_caps& caps,
                              argr_plan* out) {
@@ -40,19 +62,57 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
         return ARGR_OK;
     }
     const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
+    out->grid_rows = std::min<int64_t>(rows, kMaxGridRows);
+    if (what == ARGR_LOGITS_DISTILL_STEP) {
+        // Chunks of at most 52 KB (four CTAs of 256 threads per SM), or what a cluster of 16 allows.
+        const int most = std::min(16, caps.max_cluster);
+        int64_t c = std::max<int64_t>(1, (groups * 64 + 52 * 1024 - 1) / (52 * 1024));
+        while (c < most && rows * c < 4 * caps.sm_count && groups / (2 * c) >= 128) c *= 2;
+        c = std::min<int64_t>(c, most);
+        if ((groups + c - 1) / c * 64 <= kStepMaxChunk) {
+            out->path = ARGR_PATH_LOGITS_STEP;
+            out->cluster = static_cast<int>(c);
+            out->block = 256;
+            while (out->block > 32 && out->block * 4 > (groups + c - 1) / c * 4) out->block /= 2;
+            return ARGR_OK;
+        }
+    }
+    // Long rows, and enough of them to keep two persistent CTAs per SM busy: the
+    // streaming kernel. Rows below the limits finish too often for it ([8192, 32000]
+    // bf16: 120 us against 100 us with a CTA of 128 threads per row; [4096, 65536] bf16: 98
+    // against 104 us, with 20 alternatives 136 against 133 us); so does a last round that few CTAs
+    // take part in ([512, 100003] f16, 32 slots: 27.4 against 24.5 us).
+    const int es = dtype == ARGR_F32 ? 4 : 2;
+    const bool distill = what != ARGR_LOGITS_LOGPROBS;
+    const int64_t ctas = 2 * static_cast<int64_t>(caps.sm_count), row_bytes = cols * es;
+    const int64_t rounds = (rows + ctas - 1) / ctas;
+    if (row_bytes >= (distill || k == 0 ? 96 : 160) * 1024 && rows * 100 >= rounds * ctas * 85) {
+        for (int f = stream_finishers(distill, row_bytes, k); f >= 1; --f) {
+            if (logits_stream_smem(distill, cols, dtype, k, 16, f) > kStreamSmem) continue;
+            out->path = ARGR_PATH_LOGITS_STREAM;
+            out->grid_rows = ctas;
+            out->group = f;
+            return ARGR_OK;
+        }
+    }
+    // Clusters until there are four CTAs per SM. With that many rows, eight groups
+    // per thread: small CTAs, whose phases overlap ([4096, 32000] f16, top 5: 127, 81, 70,
+    // 88 us with 512, 256, 128, 64 threads); with few, a group per thread.
     while (out->cluster < std::min(16, caps.max_cluster) && rows * out->cluster < 4 * caps.sm_count &&
            groups / (2 * out->cluster) >= 128)
         out->cluster *= 2;
     const int64_t per_cta = groups / out->cluster;
-    while (out->block > 32 && out->block > per_cta) out->block /= 2;
-    out->grid_rows = std::min<int64_t>(rows, kMaxGridRows);
+    const int64_t threads = rows * out->cluster >= 3 * caps.sm_count ? (per_cta + 7) / 8 : per_cta;
+    while (out->block > 32 && out->block / 2 >= threads) out->block /= 2;
     return ARGR_OK;
 }
 
 argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_t cols, int dtype, int k,
                               const argr_caps& caps) {
     if (!valid_problem(what, rows, cols, dtype, k) || caps.sm_count < 1) return ARGR_EINVAL;
-    if (p.path != (forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD)) return ARGR_EINVAL;
+    const bool step = what == ARGR_LOGITS_DISTILL_STEP && p.path == ARGR_PATH_LOGITS_STEP;
+    const bool stream = forward(what) && p.path == ARGR_PATH_LOGITS_STREAM;
+    if (!step && !stream && p.path != (forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD)) return ARGR_EINVAL;
     if (p.block < 32 || p.block > 512 || p.block % 32) return ARGR_EINVAL;
     if (p.flags & ~ARGR_PLAN_PDL) return ARGR_EINVAL;
     if (p.path == ARGR_PATH_LOGITS_GRAD) {
@@ -61,7 +121,15 @@ argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_
             return ARGR_EINVAL;
     } else {
         if (p.grid_rows < 1 || p.grid_rows > kMaxGridRows || p.blocks_per_row != 1) return ARGR_EINVAL;
-        if (p.cluster < 1 || p.cluster > 16 || (p.cluster & (p.cluster - 1))) return ARGR_EINVAL;
+        if (p.cluster < 1 || p.cluster > 16) return ARGR_EINVAL;
+        if (stream &&
+            (p.cluster != 1 || p.group < 1 || p.group > 3 || p.block < 32 * (p.group + 1) ||
+             logits_stream_smem(what != ARGR_LOGITS_LOGPROBS, cols, dtype, k, p.block / 32, p.group) > kStreamSmem))
+            return ARGR_EINVAL;
+        if (step) {
+            const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
+            if (p.block > 256 || (groups + p.cluster - 1) / p.cluster * 64 > kStepMaxChunk) return ARGR_EINVAL;
+        }
         if (p.cluster > caps.max_cluster) return ARGR_EUNSUPPORTED;
     }
     return ARGR_OK;

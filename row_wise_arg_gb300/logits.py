@@ -21,8 +21,12 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _lib
+from . import _lib, _stream_ptr, dtype_code
 from ._lib import ARGR_OK, ArgreduceError
+
+_LIB = _lib.load()  # looked up once: these calls are short
+_F32, _I64 = torch.float32, torch.int64
+_empty = torch.empty
 
 
 class TokenLogprobs(NamedTuple):
@@ -41,7 +45,6 @@ class DistillLoss(NamedTuple):
 
 def _rows(x, dtype):
     """(rows, cols, row stride, type code) of logits."""
-    from . import dtype_code
     if not x.is_cuda:
         raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
     code = dtype_code(x, dtype)
@@ -67,7 +70,7 @@ def _rows(x, dtype):
     return rows, cols, x.stride(0) if rows > 1 else cols, code
 
 
-def _arg(t, what, dtype, shape, like):
+def _arg(t, what, dtype, shape, device):
     """Data pointer of an argument that must be a contiguous tensor of this type and shape on the logits' device."""
     if t is None:
         return None
@@ -75,14 +78,9 @@ def _arg(t, what, dtype, shape, like):
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous tensor on {like.device}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor on {device}")
     return t.data_ptr()
-
-
-def _stream(x, stream):
-    from . import _stream_ptr
-    return _stream_ptr(stream, x.get_device()) or None
 
 
 def _plan(plan):
@@ -97,7 +95,7 @@ def _check(st, what):
 def _grad_out(x, grad):
     """The gradient's tensor and its row stride."""
     if grad is None:
-        grad = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        grad = _empty(x.shape, dtype=x.dtype, device=x.device)
         return grad, x.shape[-1]
     if grad.shape != x.shape or grad.dtype is not x.dtype or grad.device != x.device:
         raise ValueError("grad must have the shape, type and device of logits")
@@ -107,24 +105,26 @@ def _grad_out(x, grad):
 
 def _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream):
     rows, cols, stride, code = _rows(x, dtype)
-    lead = x.shape[:-1]
-    tok = _arg(tokens, "tokens", torch.int64, lead, x)
+    lead, dev = x.shape[:-1], x.device
+    tok = _arg(tokens, "tokens", _I64, lead, dev)
     if not 0 <= top_k <= min(cols, _lib.LOGITS_MAX_TOP):
         raise ValueError(f"top_k must be in [0, {min(cols, _lib.LOGITS_MAX_TOP)}], got {top_k}")
-    dev = x.device
-    logprob, entropy, lse = torch.empty((3,) + lead, dtype=torch.float32, device=dev).unbind(0)
-    stats = torch.empty(lead + (4,), dtype=torch.float32, device=dev)
-    ids = top = None
+    entropy = _empty(lead, dtype=_F32, device=dev)
+    lse = _empty(lead, dtype=_F32, device=dev)
+    stats = _empty((*lead, 4), dtype=_F32, device=dev)
+    logprob = ids = top = None
+    if tok is not None:
+        logprob = _empty(lead, dtype=_F32, device=dev)
     if top_k:
-        ids = torch.empty(lead + (top_k,), dtype=torch.int64, device=dev)
-        top = torch.empty(lead + (top_k,), dtype=torch.float32, device=dev)
-    st = _lib.load().argreduce_logprobs(
+        ids = _empty((*lead, top_k), dtype=_I64, device=dev)
+        top = _empty((*lead, top_k), dtype=_F32, device=dev)
+    st = _LIB.argreduce_logprobs(
         x.data_ptr(), code, rows, cols, stride, temperature, tok, top_k,
-        logprob.data_ptr() if tok is not None else None, entropy.data_ptr(), lse.data_ptr(),
+        logprob.data_ptr() if logprob is not None else None, entropy.data_ptr(), lse.data_ptr(),
         ids.data_ptr() if top_k else None, top.data_ptr() if top_k else None, stats.data_ptr(), _plan(plan),
-        _stream(x, stream))
+        _stream_ptr(stream, x.get_device()) or None)
     _check(st, "argreduce_logprobs")
-    return logprob if tok is not None else None, entropy, lse, ids, top, stats
+    return logprob, entropy, lse, ids, top, stats
 
 
 class _TokenLogprobsFunction(torch.autograd.Function):
@@ -167,17 +167,16 @@ def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entro
     same logits and temperature. ``grad``: a tensor for the result, which may be
     ``logits`` itself (then overwritten)."""
     rows, cols, stride, code = _rows(logits, dtype)
-    lead = logits.shape[:-1]
-    f32 = torch.float32
-    tok = _arg(tokens, "tokens", torch.int64, lead, logits)
+    lead, dev = logits.shape[:-1], logits.device
+    tok = _arg(tokens, "tokens", _I64, lead, dev)
     if tok is None and grad_logprob is not None:
         raise ValueError("grad_logprob needs tokens")
-    args = (tok, _arg(stats, "stats", f32, lead + (4,), logits), _arg(grad_logprob, "grad_logprob", f32, lead, logits),
-            _arg(grad_entropy, "grad_entropy", f32, lead, logits), _arg(grad_lse, "grad_lse", f32, lead, logits))
+    args = (tok, _arg(stats, "stats", _F32, (*lead, 4), dev), _arg(grad_logprob, "grad_logprob", _F32, lead, dev),
+            _arg(grad_entropy, "grad_entropy", _F32, lead, dev), _arg(grad_lse, "grad_lse", _F32, lead, dev))
     grad, grad_stride = _grad_out(logits, grad)
-    _check(_lib.load().argreduce_logprobs_backward(logits.data_ptr(), code, rows, cols, stride, temperature, *args,
+    _check(_LIB.argreduce_logprobs_backward(logits.data_ptr(), code, rows, cols, stride, temperature, *args,
                                                    grad.data_ptr(), grad_stride, _plan(plan),
-                                                   _stream(logits, stream)), "argreduce_logprobs_backward")
+                                                   _stream_ptr(stream, logits.get_device()) or None), "argreduce_logprobs_backward")
     return grad
 
 
@@ -189,16 +188,16 @@ def _slots(x, ids, teacher):
     slots = ids.shape[-1]
     if slots > _lib.LOGITS_MAX_SLOTS:
         raise ValueError(f"at most {_lib.LOGITS_MAX_SLOTS} slots, got {slots}")
-    return (_arg(ids, "ids", torch.int64, ids.shape, x), _arg(teacher, "teacher", torch.float32, ids.shape, x), slots)
+    return _arg(ids, "ids", _I64, ids.shape, x.device), _arg(teacher, "teacher", _F32, ids.shape, x.device), slots
 
 
 def _forward_distill(x, ids, teacher, temperature, tail, dtype, plan, stream):
     rows, cols, stride, code = _rows(x, dtype)
     i, t, slots = _slots(x, ids, teacher)
-    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    stats = torch.empty(x.shape[:-1] + (4,), dtype=torch.float32, device=x.device)
-    _check(_lib.load().argreduce_distill(x.data_ptr(), code, rows, cols, stride, temperature, i, t, slots, bool(tail),
-                                         loss.data_ptr(), stats.data_ptr(), _plan(plan), _stream(x, stream)),
+    loss = _empty(x.shape[:-1], dtype=_F32, device=x.device)
+    stats = _empty((*x.shape[:-1], 4), dtype=_F32, device=x.device)
+    _check(_LIB.argreduce_distill(x.data_ptr(), code, rows, cols, stride, temperature, i, t, slots, bool(tail),
+                                         loss.data_ptr(), stats.data_ptr(), _plan(plan), _stream_ptr(stream, x.get_device()) or None),
            "argreduce_distill")
     return loss, stats
 
@@ -241,12 +240,12 @@ def distill_topk_backward(logits, ids, teacher, stats, grad_loss, *, temperature
     rows, cols, stride, code = _rows(logits, dtype)
     lead = logits.shape[:-1]
     i, t, slots = _slots(logits, ids, teacher)
-    st = _arg(stats, "stats", torch.float32, lead + (4,), logits)
-    g = _arg(grad_loss, "grad_loss", torch.float32, lead, logits)
+    st = _arg(stats, "stats", _F32, (*lead, 4), logits.device)
+    g = _arg(grad_loss, "grad_loss", _F32, lead, logits.device)
     grad, grad_stride = _grad_out(logits, grad)
-    _check(_lib.load().argreduce_distill_backward(logits.data_ptr(), code, rows, cols, stride, temperature, i, t,
+    _check(_LIB.argreduce_distill_backward(logits.data_ptr(), code, rows, cols, stride, temperature, i, t,
                                                   slots, bool(tail), st, g, grad.data_ptr(), grad_stride,
-                                                  _plan(plan), _stream(logits, stream)), "argreduce_distill_backward")
+                                                  _plan(plan), _stream_ptr(stream, logits.get_device()) or None), "argreduce_distill_backward")
     return grad
 
 
@@ -258,12 +257,12 @@ def distill_topk_step(logits, ids, teacher, grad_loss, *, temperature: float = 1
     rows, cols, stride, code = _rows(logits, dtype)
     lead = logits.shape[:-1]
     i, t, slots = _slots(logits, ids, teacher)
-    g = _arg(grad_loss, "grad_loss", torch.float32, lead, logits)
+    g = _arg(grad_loss, "grad_loss", _F32, lead, logits.device)
     grad, grad_stride = _grad_out(logits, grad)
-    loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
-    stats = torch.empty(lead + (4,), dtype=torch.float32, device=logits.device)
-    _check(_lib.load().argreduce_distill_step(logits.data_ptr(), code, rows, cols, stride, temperature, i, t, slots,
+    loss = _empty(lead, dtype=_F32, device=logits.device)
+    stats = _empty((*lead, 4), dtype=_F32, device=logits.device)
+    _check(_LIB.argreduce_distill_step(logits.data_ptr(), code, rows, cols, stride, temperature, i, t, slots,
                                               bool(tail), g, loss.data_ptr(), stats.data_ptr(), grad.data_ptr(),
-                                              grad_stride, _plan(plan), _stream(logits, stream)),
+                                              grad_stride, _plan(plan), _stream_ptr(stream, logits.get_device()) or None),
            "argreduce_distill_step")
     return loss, grad

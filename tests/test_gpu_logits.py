@@ -535,3 +535,132 @@ def test_teacher_to_student():
         assert abs(loss.item() - want.item()) < 1e-4
     assert losses[-1] < 0.5 * losses[0]
     assert torch.equal(A.argmax(student.detach()), t.top_ids[:, 0])
+
+
+# ---------------------------------------------------------------------------
+# Every kernel, whatever the planner would choose.
+# ---------------------------------------------------------------------------
+from row_wise_arg_gb300 import _lib  # noqa: E402
+
+
+def forward_plan(cluster=1, block=256, grid=1 << 20, rows=1):
+    p = _lib.argr_plan()
+    p.path, p.block, p.cluster, p.blocks_per_row = _lib.ARGR_PATH_LOGITS, block, cluster, 1
+    p.grid_rows, p.flags = min(grid, rows), _lib.ARGR_PLAN_PDL
+    return p
+
+
+def stream_plan(finishers=1, block=256, grid=4):
+    p = _lib.argr_plan()
+    p.path, p.block, p.cluster, p.blocks_per_row = _lib.ARGR_PATH_LOGITS_STREAM, block, 1, 1
+    p.group, p.grid_rows, p.flags = finishers, grid, _lib.ARGR_PLAN_PDL
+    return p
+
+
+def step_plan(cluster=1, block=256, grid=4):
+    p = forward_plan(cluster, block, grid, grid)
+    p.path = _lib.ARGR_PATH_LOGITS_STEP
+    return p
+
+
+def grad_plan(chunks=1, block=256, grid=4):
+    p = _lib.argr_plan()
+    p.path, p.block, p.cluster, p.blocks_per_row = _lib.ARGR_PATH_LOGITS_GRAD, block, 1, chunks
+    p.grid_rows = grid
+    return p
+
+
+FORWARD = [("cluster", dict(cluster=c, block=b, grid=g)) for c, b, g in
+           ((1, 32, 1), (1, 512, 3), (2, 64, 2), (3, 96, 9), (5, 128, 1), (8, 256, 9), (16, 512, 2), (16, 32, 9))] + \
+          [("stream", dict(finishers=f, block=b, grid=g)) for f, b, g in
+           ((1, 64, 1), (1, 512, 2), (2, 96, 1), (2, 256, 3), (3, 128, 1), (3, 512, 9), (1, 96, 9))]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind,how", FORWARD, ids=lambda v: v if isinstance(v, str) else "-".join(map(str, v.values())))
+def test_forced_forward_plans(dtype, kind, how):
+    rng = np.random.default_rng(17)
+    for rows, cols, pad, offset in ((9, 1, 0, 0), (9, 70, 1, 1), (9, 5003, 0, 0), (3, 40001, 3, 5), (2, 65536, 0, 0)):
+        plan = forward_plan(rows=rows, **how) if kind == "cluster" else stream_plan(**how)
+        x = rng.normal(0, 3, (rows, cols)).astype(np.float32)
+        tokens = rng.integers(-1, cols, rows)
+        for k in (0, 1, 20, 128):
+            check_logprobs(x, dtype, tokens, min(k, cols), 0.9, plan=plan, pad=pad, offset=offset)
+        for slots, tail in ((7, False), (7, True), (130, True)):
+            ids, val = slots_for(rng, rows, cols, slots, tail, 0.2)
+            xd, x64 = on_gpu(x, dtype, pad, offset)
+            r = A.distill_topk(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), tail=tail, plan=plan)
+            same = A.distill_topk(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), tail=tail,
+                                  plan=forward_plan(rows=rows))
+            # the two kernels against each other (the chosen one is checked against 64 bits everywhere else)
+            want, _ = ref.distill(x64, ids, val, 1.0, tail)
+            big = 40.0 + np.abs(want)
+            close(r.loss, want, ref.sum_error(cols) * big * 3, "loss")
+            close(r.stats[:, :2], same.stats[:, :2].double().cpu().numpy(), 2 * ref.sum_error(cols) * 30, "stats")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", HARD)
+def test_forced_plans_on_hard_rows(dtype, name):
+    for cols in (40, 1031, 40003):
+        x = np.repeat(hard_rows(cols, LOW[dtype])[name], 3, 0)
+        x[1] = np.random.default_rng(cols).normal(0, 3, cols)
+        tokens = np.array([cols // 2, 0, -1])
+        for plan in (forward_plan(4, 64, 3, 3), stream_plan(1, 128, 1), stream_plan(2, 512, 2)):
+            for k in (1, 40, 128):
+                check_logprobs(x, dtype, tokens, min(k, cols), plan=plan)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_forced_gradient_plans(dtype):
+    rng = np.random.default_rng(19)
+    for rows, cols, kw in ((5, 1, {}), (5, 70, {"pad": 1, "offset": 1}), (5, 5003, {"out_pad": 1}), (2, 40001, {}),
+                           (3, 32768, {"out_pad": 8}), (3, 4096, {"in_place": True}), (3, 4099, {"in_place": True})):
+        x = rng.normal(0, 3, (rows, cols)).astype(np.float32)
+        tokens = rng.integers(-1, cols, rows)
+        ids, val = slots_for(rng, rows, cols, 9, True, 0.1)
+        for chunks, block, grid in ((1, 32, 1), (3, 256, 5), (40, 64, 2)):
+            check_logprobs_grad(x, dtype, tokens, plan=grad_plan(chunks, block, grid), **kw)
+            for cluster, sblock, sgrid in ((1, 256, 2), (3, 64, 5), (16, 32, 1)):
+                if -(-(cols * ES[dtype] // 64) // cluster) * 64 > 108 * 1024:
+                    continue
+                check_distill(x, dtype, ids, val, 1.3, True, grad_plan=grad_plan(chunks, block, grid),
+                              step_plan=step_plan(cluster, sblock, sgrid), **kw)
+            check_distill(x, dtype, ids, val, 1.0, True, step_plan=forward_plan(2, 128, 3, rows), **kw)
+
+
+def test_many_rows_through_the_persistent_kernel():
+    """As many rows as two CTAs per SM, as the planner runs them."""
+    rng = np.random.default_rng(23)
+    for dtype, rows, cols in (("bf16", 300, 82003), ("f32", 304, 41000), ("f16", 290, 90001)):
+        assert A.argreduce_logits_plan("logprobs", rows, cols, dtype, 20, CAPS).path == _lib.ARGR_PATH_LOGITS_STREAM
+        x = rng.normal(0, 3, (rows, cols)).astype(np.float32)
+        x[5] = -np.inf
+        x[7, 100:] = -np.inf
+        x[9] = 1.0
+        tokens = rng.integers(0, cols, rows)
+        for k in (0, 128):
+            check_logprobs(x, dtype, tokens, k)
+        for tail in (False, True):
+            ids, val = slots_for(rng, rows, cols, 40, tail, 0.1)
+            ids[11] = -1
+            check_distill(x, dtype, ids, val, 1.0, tail)
+
+
+def test_plan_refusals_on_the_device():
+    x = torch.zeros(4, 100, device="cuda")
+    tok = torch.zeros(4, dtype=torch.int64, device="cuda")
+    bad = [forward_plan(17), forward_plan(0), forward_plan(1, 48), forward_plan(1, 1024), stream_plan(0), stream_plan(4),
+           stream_plan(3, 96), stream_plan(1, 32), stream_plan(1, 256, 0), grad_plan(), step_plan()]
+    for p in bad:
+        with pytest.raises(A.ArgreduceError):
+            A.token_logprobs(x, tok, 3, plan=p)
+    s = A.token_logprobs(x, tok).stats
+    for p in (grad_plan(0), grad_plan(1, 512), forward_plan(), stream_plan()):
+        with pytest.raises(A.ArgreduceError):
+            A.token_logprobs_backward(x, tok, s, torch.ones(4, device="cuda"), plan=p)
+    wide = torch.zeros(1, 1 << 20, device="cuda")
+    one = torch.zeros(1, 1, dtype=torch.int64, device="cuda")
+    for p in (step_plan(4), stream_plan(1, 512)):
+        with pytest.raises(A.ArgreduceError):
+            A.distill_topk_step(wide, one, one.float(), torch.ones(1, device="cuda"), plan=p)
