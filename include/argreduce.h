@@ -122,7 +122,7 @@ typedef struct {
  * every thread. The share must be at most 128 KiB. */
 #define ARGR_PLAN_BULK 2
 /* Plan flag for tests of failure handling (STREAM, CLUSTER with a row slot
- * per row, CUM_SPLIT and CUM_STREAM paths only). STREAM: one bulk copy's
+ * per row, CUM_SPLIT, CUM_STREAM and LOGITS_STEP paths only). STREAM: one bulk copy's
  * barrier is made to expect more bytes than arrive, so the kernel's bounded
  * wait (2 ms under this flag) expires; the kernel records the expiry, skips
  * its work and returns. CLUSTER (push merge only: grid_rows == rows, at
@@ -131,8 +131,9 @@ typedef struct {
  * writing the row. CUM_SPLIT and
  * CUM_STREAM: the first chunk (tile) of each row never publishes its record,
  * so every wait for it expires after 2 ms. Either way argreduce_read_error()
- * then reports ARGR_ETIMEOUT and outputs are undefined. Never set in the
- * planner's plans. */
+ * then reports ARGR_ETIMEOUT and outputs are undefined. LOGITS_STEP: the last
+ * stage of every CTA's part expects 16 bytes more than are copied, as STREAM
+ * does. Never set in the planner's plans. */
 #define ARGR_PLAN_TEST_EXPIRE 4
 /* Plan flag (CUM_SPLIT path): each CTA copies its whole chunk (at most 80 KiB)
  * into shared memory with bulk (TMA) copies and scans it there, so the input

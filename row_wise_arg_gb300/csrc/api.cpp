@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "logits.h"
 
 namespace argr {
 namespace {
@@ -364,7 +365,9 @@ argr_status argreduce_read_error(void* scratch, argr_stream stream) {
     // expired), and the one in the caller's scratch.
     unsigned any = 0;
     cudaError_t (*readers[])(unsigned*) = {read_and_clear_error_f32, read_and_clear_error_f16,
-                                           read_and_clear_error_bf16, read_and_clear_error_f64};
+                                           read_and_clear_error_bf16, read_and_clear_error_f64,
+                                           read_and_clear_logits_error_f32, read_and_clear_logits_error_f16,
+                                           read_and_clear_logits_error_bf16};
     for (auto rd : readers) {
         unsigned v = 0;
         if (rd(&v) != cudaSuccess) {

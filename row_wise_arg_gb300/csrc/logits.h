@@ -54,6 +54,7 @@ argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_
 #define ARGR_DECLARE_LOGITS(sfx)                                                         \
     cudaError_t launch_logprobs_##sfx(const argr_plan& p, const LogitsProblem& pr);      \
     cudaError_t launch_distill_##sfx(const argr_plan& p, const LogitsProblem& pr);       \
+    cudaError_t read_and_clear_logits_error_##sfx(unsigned* out);                        \
     cudaError_t launch_distill_step_##sfx(const argr_plan& p, const LogitsProblem& pr);  \
     cudaError_t launch_logprobs_grad_##sfx(const argr_plan& p, const LogitsProblem& pr); \
     cudaError_t launch_distill_grad_##sfx(const argr_plan& p, const LogitsProblem& pr);

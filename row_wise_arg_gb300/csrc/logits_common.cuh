@@ -195,7 +195,8 @@ template <class Tag> constexpr int kGroupElems = kGroupBytes / static_cast<int>(
 template <class Tag>
 struct Group {
     uint32_t w[16];
-    // 64 bytes at a 32-byte boundary, through the read-only path or, where this kernel may write them, the plain one.
+    // 64 bytes at a 32-byte boundary, through the read-only path or, where this
+    // kernel may write them, the plain one.
     template <bool READ_ONLY = true>
     __device__ __forceinline__ void load(const typename Tag::raw* p) {
 #define ARGR_LOAD32(OP)                                                                            \
@@ -304,9 +305,11 @@ struct Part {
         const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 31u);
         align = static_cast<int>(((32u - off) & 31u) / sizeof(typename Tag::raw));
         if (align > n) align = n;
-        const int groups = (n - align) / kGroupElems<Tag>;
-        first = static_cast<int>(static_cast<int64_t>(groups) * rank / ranks);
-        count = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / ranks) - first;
+        // 32-bit division: a 64-bit one costs a thread as much as 30 elements
+        const unsigned groups = static_cast<unsigned>(n - align) / kGroupElems<Tag>;
+        const unsigned each = groups / static_cast<unsigned>(ranks), more = groups - each * ranks;
+        first = static_cast<int>(each * rank + min(static_cast<unsigned>(rank), more));
+        count = static_cast<int>(each + (static_cast<unsigned>(rank) < more));
         cols = n;
         is_first = rank == 0;
         is_last = rank == ranks - 1;
@@ -402,15 +405,21 @@ __device__ __forceinline__ Teacher warp_teacher(const LogitsProblem& pr, const S
 }
 
 // The same by warp 0, for every thread of the CTA. Contains barriers, the first of
-// them after which the slots are complete.
-__device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, const Slots& sl) {
+// them after which the slots are complete; `also`, given the sums, runs in warp 0
+// before the second.
+template <class F>
+__device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, const Slots& sl, F also) {
     __syncthreads();
     if (threadIdx.x < 32) {
         const Teacher q = warp_teacher(pr, sl);
         if (threadIdx.x == 0) *sl.sums = q;
+        also(q);
     }
     __syncthreads();
     return *sl.sums;
+}
+__device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, const Slots& sl) {
+    return teacher_of(pr, sl, [](const Teacher&) {});
 }
 
 // What a slot adds to the loss of a row with largest element m.
@@ -442,6 +451,7 @@ struct GradWeights {
     float g, total, dense, m, ls2;
     bool none;
 
+    GradWeights() = default;
     __device__ __forceinline__ GradWeights(const LogitsProblem& pr, const Teacher& q, float grad_loss, float row_m,
                                            float ln_s, float ln_rest) {
         const float rest = ln_rest > neg_inf() ? q.rest : 0.0f;

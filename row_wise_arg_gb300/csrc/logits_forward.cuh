@@ -437,11 +437,30 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
 // pass (a bit per element in shared memory) and added once from the slots, so
 // that the tail's sum is a sum of its own.
 // ---------------------------------------------------------------------------
+// The bits of a segment's elements that slots name (the slots are complete after
+// the first barrier).
+template <class Tag>
+__device__ __forceinline__ void name_segment(const Segment<Tag>& sg, const Slots& sl, int slots, unsigned* named) {
+    constexpr int E = kGroupElems<Tag>;
+    const int t = threadIdx.x, nt = blockDim.x;
+    __syncthreads();
+    for (int i = t; i < (sg.slots() * E + 31) / 32; i += nt) named[i] = 0u;
+    __syncthreads();
+    for (int i = t; i < slots; i += nt) {
+        const int j = sl.id[i];
+        if (j < sg.head_lo || j >= sg.tail_hi) continue;
+        const int bit = j < sg.body_lo    ? j - sg.head_lo
+                        : j >= sg.tail_lo ? (sg.body + 1) * E + (j - sg.tail_lo)
+                                          : E + (j - sg.body_lo);
+        atomicOr(&named[bit >> 5], 1u << (bit & 31));
+    }
+    __syncthreads();
+}
+
 template <class Tag, bool TAIL>
 __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsProblem pr, float scale2, int ranks,
                                                                   int seg_slots) {
     using R = typename Tag::raw;
-    constexpr int E = kGroupElems<Tag>;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float red[96];
     __shared__ float parts[2 * kMaxRanks];
@@ -462,18 +481,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
         for (int at = 0;;) {
             const Segment<Tag> sg = part.segment(at);
             if constexpr (TAIL) {
-                __syncthreads();
-                for (int i = t; i < (sg.slots() * E + 31) / 32; i += blockDim.x) named[i] = 0u;
-                __syncthreads();
-                for (int i = t; i < pr.slots; i += blockDim.x) {
-                    const int j = sl.id[i];
-                    if (j < sg.head_lo || j >= sg.tail_hi) continue;
-                    const int bit = j < sg.body_lo    ? j - sg.head_lo
-                                    : j >= sg.tail_lo ? (sg.body + 1) * E + (j - sg.tail_lo)
-                                                      : E + (j - sg.body_lo);
-                    atomicOr(&named[bit >> 5], 1u << (bit & 31));
-                }
-                __syncthreads();
+                name_segment<Tag>(sg, sl, pr.slots, named);
             }
             SoftSum d;
             unsigned most = 0;

@@ -153,6 +153,7 @@ template <class Tag>
 __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const LogitsProblem pr, float scale2) {
     using R = typename Tag::raw;
     extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ GradWeights weights;
     const Slots sl(dyn, pr.slots);
     grid_dependency_wait();
     allow_dependents();
@@ -163,9 +164,12 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const Lo
         const Part<Tag> part(row, pr.cols, blockIdx.x, gridDim.x);
         const int lo = part.begin(), hi = part.end();
         load_slots<Tag>(pr, r, row, lo, hi, sl);
-        const float4 st = pr.stats[r];
-        const Teacher q = teacher_of(pr, sl);  // its barriers order the reads above before the stores below
-        const GradWeights w(pr, q, pr.grad_logprob[r], st.x, st.y, st.z);
+        // its barriers order the reads above before the stores below
+        const Teacher q = teacher_of(pr, sl, [&](const Teacher& sums) {
+            const float4 st = pr.stats[r];
+            if (t == 0) weights = GradWeights(pr, sums, pr.grad_logprob[r], st.x, st.y, st.z);
+        });
+        const GradWeights w = weights;
         if (w.none) {
             const R fill = narrow_elem<Tag>(w.dense);
             for (unsigned i = t; i < static_cast<unsigned>(hi - lo); i += blockDim.x) out[lo + i] = fill;

@@ -14,9 +14,9 @@ namespace argr {
 inline float scale2_of(const LogitsProblem& pr) { return kLog2E / pr.temperature; }
 
 // Launch a forward kernel: `ranks` CTAs per row, `smem` bytes of dynamic shared memory.
-template <class K>
+template <class K, typename... More>
 cudaError_t launch_forward(K kern, KernelLaunchCache& cache, const argr_plan& p, const LogitsProblem& pr, size_t smem,
-                           int seg_slots) {
+                           More... more) {
     cudaError_t e = ensure_smem_limit(kern, smem + 2048, cache);  // with the static part
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(p.grid_rows * p.cluster));
@@ -29,7 +29,7 @@ cudaError_t launch_forward(K kern, KernelLaunchCache& cache, const argr_plan& p,
         if (!ok) return cudaErrorInvalidClusterSize;
     }
     return launch_ex_smem(kern, grid, dim3(p.block), p.cluster, smem, p, pr.stream, pr, scale2_of(pr), p.cluster,
-                          seg_slots);
+                          more...);
 }
 
 // Slots of the longest segment of a CTA's part of a row (a multiple of 4).
@@ -83,11 +83,13 @@ cudaError_t launch_distill_t(const argr_plan& p, const LogitsProblem& pr) {
 template <class Tag>
 cudaError_t launch_distill_step_t(const argr_plan& p, const LogitsProblem& pr) {
     const int groups = (pr.cols / kGroupElems<Tag> + p.cluster - 1) / p.cluster;
-    const int units = groups * (kGroupBytes / 16);
-    const size_t smem = 16 * static_cast<size_t>(units) + Slots::bytes(pr.slots) + (pr.tail ? (units + 15) / 16 * 16 : 0);
+    const int units = groups * (kGroupBytes / 16), batch = 4 * p.block;
+    const size_t smem = 16 * static_cast<size_t>(units) + Slots::bytes(pr.slots) +
+                        (pr.tail ? static_cast<size_t>((units + batch - 1) / batch) * batch : 0);
     static KernelLaunchCache caches[2];
-    return pr.tail ? launch_forward(distill_step_kernel<Tag, true>, caches[1], p, pr, smem, units)
-                   : launch_forward(distill_step_kernel<Tag, false>, caches[0], p, pr, smem, units);
+    const int flags = static_cast<int>(p.flags);
+    return pr.tail ? launch_forward(distill_step_kernel<Tag, true>, caches[1], p, pr, smem, units, flags)
+                   : launch_forward(distill_step_kernel<Tag, false>, caches[0], p, pr, smem, units, flags);
 }
 inline dim3 grad_grid(const argr_plan& p) {
     return dim3(static_cast<unsigned>(p.blocks_per_row), static_cast<unsigned>(p.grid_rows < 65535 ? p.grid_rows : 65535));
@@ -105,6 +107,9 @@ cudaError_t launch_distill_grad_t(const argr_plan& p, const LogitsProblem& pr) {
 
 #define ARGR_DEFINE_LOGITS(sfx, Tag)                                                                                 \
     namespace argr {                                                                                                 \
+    cudaError_t read_and_clear_logits_error_##sfx(unsigned* out) {                                                   \
+        return read_and_clear_error_t(out);                                                                             \
+    }                                                                                                                \
     cudaError_t launch_logprobs_##sfx(const argr_plan& p, const LogitsProblem& pr) {                                 \
         return launch_logprobs_t<Tag>(p, pr);                                                                        \
     }                                                                                                                \

@@ -95,14 +95,14 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
             return ARGR_OK;
         }
     }
-    // Clusters until there are four CTAs per SM. With that many rows, eight groups
-    // per thread: small CTAs, whose phases overlap ([4096, 32000] f16, top 5: 127, 81, 70,
-    // 88 us with 512, 256, 128, 64 threads); with few, a group per thread.
-    while (out->cluster < std::min(16, caps.max_cluster) && rows * out->cluster < 4 * caps.sm_count &&
+    // Clusters until there are three CTAs per SM, a group per thread. Where the rows
+    // alone are that many, eight groups per thread: small CTAs, whose phases overlap
+    // ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads).
+    while (out->cluster < std::min(16, caps.max_cluster) && rows * out->cluster < 3 * caps.sm_count &&
            groups / (2 * out->cluster) >= 128)
         out->cluster *= 2;
     const int64_t per_cta = groups / out->cluster;
-    const int64_t threads = rows * out->cluster >= 3 * caps.sm_count ? (per_cta + 7) / 8 : per_cta;
+    const int64_t threads = out->cluster == 1 && rows >= 3 * caps.sm_count ? (per_cta + 7) / 8 : per_cta;
     while (out->block > 32 && out->block / 2 >= threads) out->block /= 2;
     return ARGR_OK;
 }
@@ -114,7 +114,7 @@ argr_status check_logits_plan(int what, const argr_plan& p, int64_t rows, int64_
     const bool stream = forward(what) && p.path == ARGR_PATH_LOGITS_STREAM;
     if (!step && !stream && p.path != (forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD)) return ARGR_EINVAL;
     if (p.block < 32 || p.block > 512 || p.block % 32) return ARGR_EINVAL;
-    if (p.flags & ~ARGR_PLAN_PDL) return ARGR_EINVAL;
+    if (p.flags & ~(ARGR_PLAN_PDL | (step ? ARGR_PLAN_TEST_EXPIRE : 0))) return ARGR_EINVAL;
     if (p.path == ARGR_PATH_LOGITS_GRAD) {
         if (p.block > 256) return ARGR_EINVAL;
         if (p.grid_rows < 1 || p.grid_rows > 65535 || p.blocks_per_row < 1 || p.blocks_per_row > 4096 || p.cluster != 1)

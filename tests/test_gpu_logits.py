@@ -626,7 +626,7 @@ def test_forced_gradient_plans(dtype):
                     continue
                 check_distill(x, dtype, ids, val, 1.3, True, grad_plan=grad_plan(chunks, block, grid),
                               step_plan=step_plan(cluster, sblock, sgrid), **kw)
-            check_distill(x, dtype, ids, val, 1.0, True, step_plan=forward_plan(2, 128, 3, rows), **kw)
+            check_distill(x, dtype, ids, val, 1.0, False, step_plan=forward_plan(2, 128, 3, rows), **kw)
 
 
 def test_many_rows_through_the_persistent_kernel():
@@ -661,6 +661,26 @@ def test_plan_refusals_on_the_device():
             A.token_logprobs_backward(x, tok, s, torch.ones(4, device="cuda"), plan=p)
     wide = torch.zeros(1, 1 << 20, device="cuda")
     one = torch.zeros(1, 1, dtype=torch.int64, device="cuda")
-    for p in (step_plan(4), stream_plan(1, 512)):
+    with pytest.raises(A.ArgreduceError):  # more than the shared memory of two CTAs per SM
+        A.distill_topk(wide, one, one.float(), plan=stream_plan(3, 512))
+    for p in (step_plan(17), step_plan(16, 512), step_plan(4), stream_plan(1, 512)):
         with pytest.raises(A.ArgreduceError):
             A.distill_topk_step(wide, one, one.float(), torch.ones(1, device="cuda"), plan=p)
+
+
+def test_step_whose_copies_never_land():
+    """A bounded wait that runs out is reported and leaves the library usable."""
+    g = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn(3, 30000, device="cuda", generator=g)
+    ids, val = torch.arange(4, device="cuda").repeat(3, 1), torch.full((3, 4), -2.0, device="cuda")
+    w = torch.ones(3, device="cuda")
+    want = A.distill_topk_step(x, ids, val, w, tail=True)
+    assert A.argreduce_read_error(0, 0) == _lib.ARGR_OK
+    for cluster, grid in ((4, 3), (2, 1)):
+        p = step_plan(cluster, 128, grid)
+        p.flags |= _lib.ARGR_PLAN_TEST_EXPIRE
+        A.distill_topk_step(x, ids, val, w, tail=True, plan=p)
+        assert A.argreduce_read_error(0, 0) == _lib.ARGR_ETIMEOUT
+        assert A.argreduce_read_error(0, 0) == _lib.ARGR_OK
+    got = A.distill_topk_step(x, ids, val, w, tail=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
