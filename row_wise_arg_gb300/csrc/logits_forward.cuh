@@ -307,6 +307,9 @@ __device__ __forceinline__ void st_cluster(unsigned addr, float v) {
 __device__ __forceinline__ void st_cluster(unsigned addr, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+// Before the first write into another CTA: that it runs, and has consumed what
+// was written for the row before. Orders nothing, so it waits for no memory operation.
+__device__ __forceinline__ void cluster_ready() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
     grid_dependency_wait();
     const int64_t slots = gridDim.x / ranks;
     for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += slots) {
-        if (ranks > 1) cluster_arrive();  // CTA 0 is running, and done with the row before
+        if (ranks > 1) cluster_ready();
         const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
         int64_t tok = -1;
         float tok_x = 0.0f;
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) distill_kernel(const LogitsPr
     grid_dependency_wait();
     const int64_t row_slots = gridDim.x / ranks;
     for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += row_slots) {
-        if (ranks > 1) cluster_arrive();
+        if (ranks > 1) cluster_ready();
         const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
         if (TAIL || rank == 0) load_slots<Tag>(pr, r, row, 0, rank == 0 ? pr.cols : 0, sl);
         const Part<Tag> part(row, pr.cols, rank, ranks);

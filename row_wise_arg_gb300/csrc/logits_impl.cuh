@@ -83,9 +83,8 @@ cudaError_t launch_distill_t(const argr_plan& p, const LogitsProblem& pr) {
 template <class Tag>
 cudaError_t launch_distill_step_t(const argr_plan& p, const LogitsProblem& pr) {
     const int groups = (pr.cols / kGroupElems<Tag> + p.cluster - 1) / p.cluster;
-    const int units = groups * (kGroupBytes / 16), batch = 4 * p.block;
-    const size_t smem = 16 * static_cast<size_t>(units) + Slots::bytes(pr.slots) +
-                        (pr.tail ? static_cast<size_t>((units + batch - 1) / batch) * batch : 0);
+    const int units = groups * (kGroupBytes / 16);
+    const size_t smem = 16 * static_cast<size_t>(units) + Slots::bytes(pr.slots);
     static KernelLaunchCache caches[2];
     const int flags = static_cast<int>(p.flags);
     return pr.tail ? launch_forward(distill_step_kernel<Tag, true>, caches[1], p, pr, smem, units, flags)

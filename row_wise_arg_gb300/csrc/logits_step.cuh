@@ -52,19 +52,17 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
     constexpr int E = kGroupElems<Tag>;
     constexpr int P = 16 / static_cast<int>(sizeof(R));  // elements of a unit
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ float2 parts[kMaxRanks * kStepMaxBlock / 32];  // (m, s) of every warp of the cluster
-    __shared__ float2 own[kMaxRanks];                         // and of each CTA's elements that slots name
-    __shared__ __align__(8) unsigned long long bars[kStepStages];
+    // of every warp of the cluster: (m, s), and the same of the elements that slots name
+    __shared__ __align__(16) uint4 parts[kMaxRanks * kStepMaxBlock / 32];
+    __shared__ __align__(8) unsigned long long bars[kStepStages + 1];  // the stages', and the exchange's
     __shared__ unsigned ends[2];  // the named elements of the ragged ends, a bit each
     const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5, warps = nt >> 5;
     const int rank = static_cast<int>(blockIdx.x % ranks);
     uint4* data = reinterpret_cast<uint4*>(dyn);
     const Slots sl(dyn + 16 * static_cast<size_t>(max_units), pr.slots);
-    // for the elements that slots name, 32 bits per batch and thread (unit j of the batch: bits j P on)
-    unsigned* named = reinterpret_cast<unsigned*>(dyn + 16 * static_cast<size_t>(max_units) + Slots::bytes(pr.slots));
     const unsigned bar = smem_u32(bars);
     if (t == 0) {
-        for (int s = 0; s < kStepStages; ++s) mbar_init(bar + 8 * s, 1);
+        for (int s = 0; s <= kStepStages; ++s) mbar_init(bar + 8 * s, 1);
         mbar_init_fence();
     }
     allow_dependents();
@@ -74,7 +72,7 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
     unsigned parity = 0;
     bool dead = false;  // a wait ran out
     for (int64_t r = blockIdx.x / ranks; r < pr.rows; r += row_slots, parity ^= 1) {
-        if (ranks > 1) cluster_arrive();
+        if (ranks > 1) cluster_ready();  // (the first time: the barriers are initialised)
         const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
         R* out = static_cast<R*>(pr.grad) + r * pr.grad_stride;
         const Part<Tag> part(row, pr.cols, rank, ranks);
@@ -101,12 +99,10 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
         asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(grad_loss) : "l"(pr.grad_logprob + r));
         load_slots<Tag>(pr, r, row, rank == 0 ? 0 : lo, rank == 0 ? pr.cols : hi, sl);
         if constexpr (TAIL) {
-            for (int b = 0; b < batches; ++b) named[b * nt + t] = 0u;
             if (t < 2) ends[t] = 0u;
         }
         __syncthreads();
-        // the teacher's sums in the first warp; with the tail, the sums of this part's named elements in the
-        // second, and their bits by the others (or by one warp, one after the other)
+        // the teacher's sums in the first warp; with the tail, the sums of this part's named elements in the second
         if (warp == 0) {
             const Teacher q = warp_teacher(pr, sl);
             if (lane == 0) *sl.sums = q;
@@ -119,18 +115,18 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
                     if (sl.id[i] >= lo && sl.id[i] < hi) d.add(sl.x[i], scale2);
                 d = warp_softsum(d, scale2);
             }
-            const int from = warps > 2 ? 2 : 0;
-            if (warp >= from) {
-                for (int i = t - 32 * from; i < pr.slots; i += nt - 32 * from) {
-                    const int j = sl.id[i];
-                    if (j >= body && j < tail) {
-                        const unsigned u = static_cast<unsigned>(j - body) / P, b = u / (4 * nt), in = u - b * 4 * nt;
-                        const unsigned at = in / nt;
-                        atomicOr(&named[b * nt + in - at * nt], 1u << (at * P + static_cast<unsigned>(j - body) % P));
-                    } else if (j >= lo && j < hi) {
-                        atomicOr(&ends[j >= tail], 1u << (j >= tail ? j - tail : j - lo));
-                    }
-                }
+        }
+        bool landed = true;
+        const unsigned long long limit = (flags & ARGR_PLAN_TEST_EXPIRE) ? 2ull * 1000 * 1000 : kWaitLimitNs;
+        if constexpr (TAIL) {
+            // -inf in the place of the elements that slots name: nothing to the sums, 0 to the dense gradient
+            for (int s = 0; s < kStepStages; ++s)
+                if (!dead) landed = mbar_wait_bounded(bar + 8 * s, parity, limit) && landed;
+            R* mine = reinterpret_cast<R*>(data);
+            for (int i = t; i < pr.slots; i += nt) {
+                const int j = sl.id[i];
+                if (j >= body && j < tail) mine[j - body] = narrow_elem<Tag>(neg_inf());
+                else if (j >= lo && j < hi) atomicOr(&ends[j >= tail], 1u << (j >= tail ? j - tail : j - lo));
             }
         }
         __syncthreads();
@@ -138,59 +134,52 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
         SoftSum c;
         if (has_head && !drop_head) c.add(x_head, scale2);
         if (has_tail && !drop_tail) c.add(x_tail, scale2);
-        bool landed = true;
-        const unsigned long long limit = (flags & ARGR_PLAN_TEST_EXPIRE) ? 2ull * 1000 * 1000 : kWaitLimitNs;
         for (int s = 0; s < kStepStages; ++s) {
-            if (!dead) landed = mbar_wait_bounded(bar + 8 * s, parity, limit) && landed;
+            if (!TAIL && !dead) landed = mbar_wait_bounded(bar + 8 * s, parity, limit) && landed;
             for (int b = batches * s / kStepStages; b < batches * (s + 1) / kStepStages; ++b) {
                 Group<Tag> v;
                 const int first = t + 4 * b * nt;
                 if (b < full) load_batch<Tag, true>(v, data, first, units);
                 else load_batch<Tag, false>(v, data, first, units);
-                if constexpr (TAIL) {
-                    const unsigned bits = named[b * nt + t];
-                    if (bits) v.drop(bits);
-                }
                 add_group<Tag, false>(c, v, v.largest(), scale2);
             }
         }
         // every warp's sums to every CTA, which joins them in each of its warps
         c.t = 0.0f;
         c = warp_softsum(c, scale2);
+        const uint4 mine = make_uint4(__float_as_uint(c.m), __float_as_uint(c.s), __float_as_uint(d.m), __float_as_uint(d.s));
         if (ranks > 1) {
-            cluster_wait();  // every CTA is running, and done with the row before
-            if (lane < ranks) {
-                const unsigned to = cluster_addr(smem_u32(parts), lane) + 8 * (rank * warps + warp);
-                st_cluster(to, c.m);
-                st_cluster(to + 4, c.s);
-                if (warp == d_warp) {
-                    const unsigned also = cluster_addr(smem_u32(own), lane) + 8 * rank;
-                    st_cluster(also, d.m);
-                    st_cluster(also + 4, d.s);
-                }
-            }
-            cluster_arrive();
             cluster_wait();
+            if (t == 0) mbar_arrive_expect_tx(bar + 8 * kStepStages, 16u * static_cast<unsigned>(ranks * warps));
+            if (lane < ranks)
+                st_async_v4(cluster_addr(smem_u32(&parts[rank * warps + warp]), lane), mine,
+                            cluster_addr(bar + 8 * kStepStages, lane));
+            const unsigned long long t0 = global_timer_ns();
+            bool here = mbar_try_wait_cluster(bar + 8 * kStepStages, parity);
+            while (!here && global_timer_ns() - t0 <= kWaitLimitNs) here = mbar_try_wait_cluster(bar + 8 * kStepStages, parity);
+            landed = landed && here;
         } else {
-            if (lane == 0) parts[warp] = make_float2(c.m, c.s);
-            if (lane == 0 && warp == d_warp) own[0] = make_float2(d.m, d.s);
+            if (lane == 0) parts[warp] = mine;
             __syncthreads();
         }
         c = SoftSum();
+        d = SoftSum();
         for (int i = lane; i < ranks * warps; i += 32) {
+            const uint4 v = parts[i];
             SoftSum o;
-            o.m = parts[i].x;
-            o.s = parts[i].y;
+            o.m = __uint_as_float(v.x);
+            o.s = __uint_as_float(v.y);
             c.join(o, scale2);
+            if constexpr (TAIL) {
+                o.m = __uint_as_float(v.z);
+                o.s = __uint_as_float(v.w);
+                o.t = 0.0f;
+                d.join(o, scale2);
+            }
         }
         c = warp_softsum(c, scale2);
         SoftSum all = c;
         if constexpr (TAIL) {
-            d = SoftSum();
-            if (lane < ranks) {
-                d.m = own[lane].x;
-                d.s = own[lane].y;
-            }
             all.join(warp_softsum(d, scale2), scale2);
             c.rebase(all.m, scale2);
         }
