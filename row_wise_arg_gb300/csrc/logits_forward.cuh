@@ -156,7 +156,7 @@ struct TopShared {
     unsigned short* list;       // kListGroups slots picked
     unsigned long long* cand;   // room candidates
     unsigned long long* best;   // 2 * ARGR_LOGITS_MAX_TOP keys: the best so far, in order, and a spare
-    int* count;                 // 2 counters
+    int* count;                 // 3 counters
     int room;
 };
 
@@ -231,10 +231,14 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
         if (last > at) at = last;
     }
     if (at == 0) at = 1;
-    int cut = slots;  // of the slots whose largest element equals `at`, those up to here
-    for (bool exact = false;; exact = true) {
-        if (exact) {
-            // the k first slots by (largest element, position)
+    // Mode 0 looks into every slot that reaches `at`. Mode 1, where fewer than k slots
+    // exceed it and very many equal it (a masked row, whose -inf fill the places that its
+    // few numbers leave): into those that exceed it, and takes the first elements that equal it in
+    // order. Mode 2, where still too many reach it: into the k first by (largest element,
+    // position), found exactly.
+    int mode = 0, cut = slots;  // cut: of the slots whose largest element equals `at`, those up to here
+    for (;;) {
+        if (mode == 2) {
             at = 0;
             for (int b = 31; b >= 0; --b) {
                 const unsigned trial = at | 1u << b;
@@ -256,19 +260,33 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
         if (t == 0) {
             sh.count[0] = 0;
             sh.count[1] = have;
+            sh.count[2] = 0;
         }
         for (int i = t; i < have; i += nt) sh.cand[i] = sh.best[i];
         __syncthreads();
+        int equal = 0;
         for (int i = t; i < slots; i += nt) {
             const unsigned o = sh.big[i];
-            if (o > at || (o == at && i <= cut)) {
+            equal += o == at;
+            if (o > at || (o == at && i <= cut && mode != 1)) {
                 const int p = atomicAdd(&sh.count[0], 1);
                 if (p < kListGroups) sh.list[p] = static_cast<unsigned short>(i);
             }
         }
+        if (mode == 0 && equal) atomicAdd(&sh.count[2], equal);
         __syncthreads();
         const int picked = sh.count[0];
-        if (picked > kListGroups && !exact) continue;
+        if (mode == 0) {
+            const int over = picked - sh.count[2];  // slots that exceed it
+            if (over < k && picked > 2 * k + 32) {
+                mode = 1;
+                continue;
+            }
+        }
+        if (picked > kListGroups && mode != 2) {
+            mode = 2;
+            continue;
+        }
         // the picked slots' elements, 32 / E slots per warp at a time
         for (int p0 = (t >> 5) * (32 / E); p0 < picked; p0 += (nt >> 5) * (32 / E)) {
             const int p = p0 + lane / E;
@@ -279,7 +297,8 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
                 const int j = lane % E;
                 if (j < n) {
                     key = order_key(widen_elem<Tag>(ld_scalar(row + lo + j)), lo + j);
-                    if (static_cast<unsigned>(key >> 32) < at) key = 0;
+                    const unsigned o = static_cast<unsigned>(key >> 32);
+                    if (o < at || (o == at && mode == 1)) key = 0;
                 }
             }
             const unsigned got = __ballot_sync(0xffffffffu, key != 0);
@@ -290,8 +309,37 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
             if (key != 0 && q < sh.room) sh.cand[q] = key;
         }
         __syncthreads();
-        if (sh.count[1] <= sh.room || exact) break;
+        if (sh.count[1] > sh.room && mode != 2) {
+            mode = 2;
+            continue;
+        }
+        if (mode == 1 && sh.count[1] < k && t < 32) {
+            // the first warp fills up to k, in order: such elements lie close (a warp that still reads
+            // the count above sees at most k, which fits)
+            int n = sh.count[1];
+            const int end = sg.tail_hi;
+            for (int j0 = sg.head_lo; j0 < end && n < k;) {
+                constexpr int U = 4;
+                float x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    x[u] = end - j0 > 32 * u + lane ? widen_elem<Tag>(ld_scalar(row + j0 + 32 * u + lane)) : 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = end - j0 > 32 * u + lane && order32(x[u]) == at;
+                    const unsigned got = __ballot_sync(0xffffffffu, in);
+                    const int q = n + __popc(got & ((1u << lane) - 1u));
+                    if (in && q < k) sh.cand[q] = order_key(x[u], j0 + 32 * u + lane);
+                    n += __popc(got);
+                }
+                if (end - j0 <= 32 * U) break;
+                j0 += 32 * U;
+            }
+            if (lane == 0) sh.count[1] = n < k ? n : k;
+        }
+        break;
     }
+    __syncthreads();
     const int n = sh.count[1] < sh.room ? sh.count[1] : sh.room;
     __syncthreads();
     rank_keys(sh.cand, n, k, sh.best, sh.best + ARGR_LOGITS_MAX_TOP, sh.count);
@@ -329,7 +377,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
     __shared__ float red[96];
     __shared__ float parts[3 * kMaxRanks];
     __shared__ float row_m, row_ln_s;
-    __shared__ int count[2];
+    __shared__ int count[3];
     const int t = threadIdx.x;
     const int rank = static_cast<int>(blockIdx.x % ranks);
     const int k = pr.top_k;

@@ -10,6 +10,7 @@ namespace {
 
 constexpr int64_t kMaxGridRows = 1 << 24;
 constexpr size_t kStreamSmem = 110 * 1024;  // two CTAs per SM
+constexpr int64_t kStepPart = 41 * 1024;    // bytes of a row per CTA of the step's kernel
 
 bool forward(int what) { return what == ARGR_LOGITS_LOGPROBS || what == ARGR_LOGITS_DISTILL || what == ARGR_LOGITS_DISTILL_STEP; }
 
@@ -64,16 +65,21 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
     const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
     out->grid_rows = std::min<int64_t>(rows, kMaxGridRows);
     if (what == ARGR_LOGITS_DISTILL_STEP) {
-        // Chunks of at most 52 KB (four CTAs of 256 threads per SM), or what a cluster of 16 allows.
+        // Parts of about 40 KB, five or more CTAs of 128 threads per SM, whose phases
+        // overlap; more parts while the rows are few. Clusters of an odd size find fewer places
+        // (SMs come in pairs): [1024, 202048] bf16, 64 slots: 175, 195, 168, 183, 156, 169, 197 us with
+        // 6, 7, 8, 9, 10, 12, 16 CTAs; [2048, 65536]: 113, 121, 103 with 2, 3, 4. Of 8 CTAs with
+        // 256, 192, 128, 96 threads: 180, 176, 168, 177 us.
         const int most = std::min(16, caps.max_cluster);
-        int64_t c = std::max<int64_t>(1, (groups * 64 + 52 * 1024 - 1) / (52 * 1024));
-        while (c < most && rows * c < 4 * caps.sm_count && groups / (2 * c) >= 128) c *= 2;
+        int64_t c = std::max<int64_t>(1, (groups * 64 + kStepPart - 1) / kStepPart);
+        if (c > 1) c += c % 2;
+        while (2 * c <= most && rows * c < 4 * caps.sm_count && groups / (2 * c) >= 128) c *= 2;
         c = std::min<int64_t>(c, most);
         if ((groups + c - 1) / c * 64 <= kStepMaxChunk) {
             out->path = ARGR_PATH_LOGITS_STEP;
             out->cluster = static_cast<int>(c);
-            out->block = 256;
-            while (out->block > 32 && out->block * 4 > (groups + c - 1) / c * 4) out->block /= 2;
+            out->block = 128;
+            while (out->block > 32 && out->block > groups / c) out->block /= 2;
             return ARGR_OK;
         }
     }
@@ -96,14 +102,18 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
         }
     }
     // Clusters until there are three CTAs per SM, a group per thread. Where the rows
-    // alone are that many, eight groups per thread: small CTAs, whose phases overlap
-    // ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads).
+    // alone are that many, about eight groups per thread: small CTAs, whose phases overlap
+    // ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads;
+    // [512, 100003] f16, 32 slots: 29, 25, 34 us with 512, 256, 128).
     while (out->cluster < std::min(16, caps.max_cluster) && rows * out->cluster < 3 * caps.sm_count &&
            groups / (2 * out->cluster) >= 128)
         out->cluster *= 2;
     const int64_t per_cta = groups / out->cluster;
-    const int64_t threads = out->cluster == 1 && rows >= 3 * caps.sm_count ? (per_cta + 7) / 8 : per_cta;
-    while (out->block > 32 && out->block / 2 >= threads) out->block /= 2;
+    if (out->cluster == 1 && rows >= 3 * caps.sm_count) {
+        while (out->block > 32 && out->block * 8 > per_cta + per_cta / 8) out->block /= 2;
+    } else {
+        while (out->block > 32 && out->block / 2 >= per_cta) out->block /= 2;
+    }
     return ARGR_OK;
 }
 

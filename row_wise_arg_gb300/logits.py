@@ -35,12 +35,12 @@ class TokenLogprobs(NamedTuple):
     lse: torch.Tensor                #: [...] log sum exp(logits / temperature)
     top_ids: Optional[torch.Tensor]  #: [..., top_k] int64, the largest logits first, ties to the lowest index
     top_logprobs: Optional[torch.Tensor]  #: [..., top_k] their log p
-    stats: torch.Tensor              #: [..., 4] what the backward pass needs: row maximum, log sum, entropy, 0
+    stats: Optional[torch.Tensor]    #: [..., 4] what the backward pass needs: row maximum, log sum, entropy, 0; None unless asked for
 
 
 class DistillLoss(NamedTuple):
     loss: torch.Tensor   #: [...]
-    stats: torch.Tensor  #: [..., 4] what the backward pass needs: row maximum, log sum, log sum of the tail, 0
+    stats: Optional[torch.Tensor]  #: [..., 4] what the backward pass needs: row maximum, log sum, log sum of the tail, 0
 
 
 def _rows(x, dtype):
@@ -103,7 +103,7 @@ def _grad_out(x, grad):
     return grad, stride
 
 
-def _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream):
+def _forward_logprobs(x, tokens, top_k, temperature, with_stats, dtype, plan, stream):
     rows, cols, stride, code = _rows(x, dtype)
     lead, dev = x.shape[:-1], x.device
     tok = _arg(tokens, "tokens", _I64, lead, dev)
@@ -111,8 +111,9 @@ def _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream):
         raise ValueError(f"top_k must be in [0, {min(cols, _lib.LOGITS_MAX_TOP)}], got {top_k}")
     entropy = _empty(lead, dtype=_F32, device=dev)
     lse = _empty(lead, dtype=_F32, device=dev)
-    stats = _empty((*lead, 4), dtype=_F32, device=dev)
-    logprob = ids = top = None
+    logprob = ids = top = stats = None
+    if with_stats:
+        stats = _empty((*lead, 4), dtype=_F32, device=dev)
     if tok is not None:
         logprob = _empty(lead, dtype=_F32, device=dev)
     if top_k:
@@ -121,7 +122,8 @@ def _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream):
     st = _LIB.argreduce_logprobs(
         x.data_ptr(), code, rows, cols, stride, temperature, tok, top_k,
         logprob.data_ptr() if logprob is not None else None, entropy.data_ptr(), lse.data_ptr(),
-        ids.data_ptr() if top_k else None, top.data_ptr() if top_k else None, stats.data_ptr(), _plan(plan),
+        ids.data_ptr() if top_k else None, top.data_ptr() if top_k else None,
+        stats.data_ptr() if with_stats else None, _plan(plan),
         _stream_ptr(stream, x.get_device()) or None)
     _check(st, "argreduce_logprobs")
     return logprob, entropy, lse, ids, top, stats
@@ -130,7 +132,7 @@ def _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream):
 class _TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, tokens, top_k, temperature, dtype, plan, stream):
-        out = _forward_logprobs(x, tokens, top_k, temperature, dtype, plan, stream)
+        out = _forward_logprobs(x, tokens, top_k, temperature, True, dtype, plan, stream)
         ctx.save_for_backward(x, tokens, out[5])
         ctx.temperature, ctx.dtype, ctx.stream = temperature, dtype, stream
         ctx.mark_non_differentiable(*(t for t in out[3:] if t is not None))
@@ -148,23 +150,24 @@ class _TokenLogprobsFunction(torch.autograd.Function):
                                         stream=ctx.stream),) + (None,) * 6
 
 
-def token_logprobs(logits, tokens=None, top_k: int = 0, *, temperature: float = 1.0, dtype: Optional[str] = None,
-                   plan=None, stream=None) -> TokenLogprobs:
+def token_logprobs(logits, tokens=None, top_k: int = 0, *, temperature: float = 1.0, with_stats: bool = False,
+                   dtype: Optional[str] = None, plan=None, stream=None) -> TokenLogprobs:
     """For each row of logits: log p of its token (``tokens``, int64 of the
     leading shape; negative: none), the entropy, the log of the sum of
     exponentials, and the ``top_k`` (at most 128) likeliest tokens with their
-    log p. Runs on ``stream`` (default: torch's current stream) without
+    log p. ``with_stats``: also what ``token_logprobs_backward`` needs (always there
+    where the logits require a gradient). Runs on ``stream`` (default: torch's current stream) without
     synchronising."""
     if torch.is_grad_enabled() and logits.requires_grad:
         return TokenLogprobs(*_TokenLogprobsFunction.apply(logits, tokens, top_k, temperature, dtype, plan, stream))
-    return TokenLogprobs(*_forward_logprobs(logits, tokens, top_k, temperature, dtype, plan, stream))
+    return TokenLogprobs(*_forward_logprobs(logits, tokens, top_k, temperature, with_stats, dtype, plan, stream))
 
 
 def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entropy=None, grad_lse=None, *,
                             temperature: float = 1.0, grad=None, dtype: Optional[str] = None, plan=None, stream=None):
     """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy +
-    grad_lse * lse) to the logits; ``stats`` from ``token_logprobs`` of the
-    same logits and temperature. ``grad``: a tensor for the result, which may be
+    grad_lse * lse) to the logits; ``stats`` from ``token_logprobs(...,
+    with_stats=True)`` of the same logits and temperature. ``grad``: a tensor for the result, which may be
     ``logits`` itself (then overwritten)."""
     rows, cols, stride, code = _rows(logits, dtype)
     lead, dev = logits.shape[:-1], logits.device
@@ -191,21 +194,21 @@ def _slots(x, ids, teacher):
     return _arg(ids, "ids", _I64, ids.shape, x.device), _arg(teacher, "teacher", _F32, ids.shape, x.device), slots
 
 
-def _forward_distill(x, ids, teacher, temperature, tail, dtype, plan, stream):
+def _forward_distill(x, ids, teacher, temperature, tail, with_stats, dtype, plan, stream):
     rows, cols, stride, code = _rows(x, dtype)
     i, t, slots = _slots(x, ids, teacher)
     loss = _empty(x.shape[:-1], dtype=_F32, device=x.device)
-    stats = _empty((*x.shape[:-1], 4), dtype=_F32, device=x.device)
+    stats = _empty((*x.shape[:-1], 4), dtype=_F32, device=x.device) if with_stats else None
     _check(_LIB.argreduce_distill(x.data_ptr(), code, rows, cols, stride, temperature, i, t, slots, bool(tail),
-                                         loss.data_ptr(), stats.data_ptr(), _plan(plan), _stream_ptr(stream, x.get_device()) or None),
-           "argreduce_distill")
+                                         loss.data_ptr(), stats.data_ptr() if with_stats else None, _plan(plan),
+                                  _stream_ptr(stream, x.get_device()) or None), "argreduce_distill")
     return loss, stats
 
 
 class _DistillFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, ids, teacher, temperature, tail, dtype, plan, stream):
-        loss, stats = _forward_distill(x, ids, teacher, temperature, tail, dtype, plan, stream)
+        loss, stats = _forward_distill(x, ids, teacher, temperature, tail, True, dtype, plan, stream)
         ctx.save_for_backward(x, ids, teacher, stats)
         ctx.given = dict(temperature=temperature, tail=tail, dtype=dtype, stream=stream)
         ctx.mark_non_differentiable(stats)
@@ -218,24 +221,24 @@ class _DistillFunction(torch.autograd.Function):
         return (distill_topk_backward(x, ids, teacher, stats, grad_loss.contiguous(), **ctx.given),) + (None,) * 7
 
 
-def distill_topk(logits, ids, teacher, *, temperature: float = 1.0, tail: bool = False, dtype: Optional[str] = None,
-                 plan=None, stream=None) -> DistillLoss:
+def distill_topk(logits, ids, teacher, *, temperature: float = 1.0, tail: bool = False, with_stats: bool = False,
+                 dtype: Optional[str] = None, plan=None, stream=None) -> DistillLoss:
     """Loss of a student's logits against a teacher's top ones, for each row:
     ``ids`` [..., slots] int64 names distinct tokens (negative: an empty slot),
     ``teacher`` [..., slots] float32 holds the teacher's logits for them, whose
     softmax (at ``temperature``) over the slots is taught, or, with ``tail``,
     the teacher's log probabilities, taught together with what they leave of 1
     as one more outcome. Sums over rows, and a factor of temperature ** 2 where
-    one is wanted, are the caller's."""
+    one is wanted, are the caller's. ``with_stats`` as in ``token_logprobs``."""
     if torch.is_grad_enabled() and logits.requires_grad:
         return DistillLoss(*_DistillFunction.apply(logits, ids, teacher, temperature, tail, dtype, plan, stream))
-    return DistillLoss(*_forward_distill(logits, ids, teacher, temperature, tail, dtype, plan, stream))
+    return DistillLoss(*_forward_distill(logits, ids, teacher, temperature, tail, with_stats, dtype, plan, stream))
 
 
 def distill_topk_backward(logits, ids, teacher, stats, grad_loss, *, temperature: float = 1.0, tail: bool = False,
                           grad=None, dtype: Optional[str] = None, plan=None, stream=None):
     """The gradient of sum(grad_loss * loss) to the logits; ``stats`` from
-    ``distill_topk`` with the same arguments. ``grad`` as in
+    ``distill_topk(..., with_stats=True)`` with the same arguments. ``grad`` as in
     ``token_logprobs_backward``."""
     rows, cols, stride, code = _rows(logits, dtype)
     lead = logits.shape[:-1]

@@ -75,7 +75,7 @@ def check_logprobs_grad(x, dtype, tokens, temp=1.0, plan=None, pad=0, offset=0, 
     g, h, c = (rng.normal(size=rows).astype(np.float32) for _ in range(3))
     xd, x64 = on_gpu(x, dtype, pad, offset)
     tok = torch.from_numpy(tokens).cuda()
-    r = A.token_logprobs(xd, tok, temperature=temp)
+    r = A.token_logprobs(xd, tok, temperature=temp, with_stats=True)
     out = None
     if in_place:
         out = xd
@@ -122,7 +122,7 @@ def check_distill(x, dtype, ids, val, temp=1.0, tail=False, plan=None, grad_plan
     i, v, gd = torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), torch.from_numpy(g).cuda()
     want, wgrad = ref.distill(x64, ids, val, temp, tail, g.astype(np.float64))
     kw = dict(temperature=temp, tail=tail)
-    r = A.distill_topk(xd, i, v, plan=plan, **kw)
+    r = A.distill_topk(xd, i, v, plan=plan, with_stats=True, **kw)
     slots = max(1, ids.shape[1])
     # |loss| is at most what its terms add up to: q |ln q| <= ln slots + 1, q |ln p| <= the largest |ln p| of a slot
     lp = ref.log_probs(x64, temp)
@@ -336,7 +336,7 @@ def test_leading_dimensions_and_broadcast_rows():
     rng = np.random.default_rng(9)
     x = torch.from_numpy(rng.normal(0, 2, (2, 3, 517)).astype(np.float32)).cuda()
     tokens = torch.randint(0, 500, (2, 3), device="cuda")
-    r = A.token_logprobs(x[..., :500], tokens, 4)
+    r = A.token_logprobs(x[..., :500], tokens, 4, with_stats=True)
     assert r.logprob.shape == (2, 3) and r.top_ids.shape == (2, 3, 4) and r.stats.shape == (2, 3, 4)
     flat = A.token_logprobs(x.reshape(6, 517)[:, :500].contiguous(), tokens.view(-1), 4)
     # the rows' addresses decide how their sums are grouped: equal to rounding, by the same bounds as everywhere
@@ -362,7 +362,7 @@ def test_binding_refusals():
         with pytest.raises(TypeError):
             bad()
     big = torch.zeros(4, 1025, dtype=torch.int64, device="cuda")
-    s = A.token_logprobs(x, tok).stats
+    s = A.token_logprobs(x, tok, with_stats=True).stats
     for bad in (lambda: A.token_logprobs(x, tok[:3]), lambda: A.token_logprobs(x, tok, 101),
                 lambda: A.token_logprobs(x, tok, -1), lambda: A.token_logprobs(x, tok, 129),
                 lambda: A.token_logprobs(x.t(), tok), lambda: A.token_logprobs(x, tok.cpu()),
@@ -431,7 +431,7 @@ def test_gradients_against_differences():
     tok = torch.tensor([7], device="cuda")
     r = A.token_logprobs(m, tok.expand(74).contiguous())
     f = (r.logprob + 0.5 * r.entropy - 0.25 * r.lse).cpu().numpy().reshape(37, 2)
-    s = A.token_logprobs(one, tok).stats
+    s = A.token_logprobs(one, tok, with_stats=True).stats
     grad = A.token_logprobs_backward(one, tok, s, *(torch.full((1,), w, device="cuda") for w in (1.0, 0.5, -0.25)))
     assert np.abs((f[:, 0] - f[:, 1]) / (2 * step) - grad.cpu().numpy()[0]).max() < 2e-3
 
@@ -440,16 +440,16 @@ def test_streams_graphs_and_repeats():
     g = torch.Generator("cuda").manual_seed(4)
     x = (torch.randn(9, 40001, device="cuda", generator=g) * 3).bfloat16()
     tok = torch.randint(0, 40001, (9,), device="cuda", generator=g)
-    first = A.token_logprobs(x, tok, 20)
+    first = A.token_logprobs(x, tok, 20, with_stats=True)
     ids, val = first.top_ids, first.top_logprobs
     w = torch.rand(9, device="cuda", generator=g)
     step = A.distill_topk_step(x, ids, val, w, tail=True)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        again = A.token_logprobs(x, tok, 20)
+        again = A.token_logprobs(x, tok, 20, with_stats=True)
         step2 = A.distill_topk_step(x, ids, val, w, tail=True)
-    other = A.token_logprobs(x, tok, 20, stream=side)
+    other = A.token_logprobs(x, tok, 20, stream=side, with_stats=True)
     side.synchronize()
     for a, b, c in zip(first, again, other):
         assert torch.equal(a, b) and torch.equal(a, c)
@@ -457,12 +457,12 @@ def test_streams_graphs_and_repeats():
         assert torch.equal(a, b)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        r = A.token_logprobs(x, tok, 20)
+        r = A.token_logprobs(x, tok, 20, with_stats=True)
         s = A.distill_topk_step(x, r.top_ids, r.top_logprobs, w, tail=True)
     for k in range(3):
         x.copy_((torch.randn(9, 40001, device="cuda", generator=g) * 3).bfloat16())
         graph.replay()
-        eager = A.token_logprobs(x, tok, 20)
+        eager = A.token_logprobs(x, tok, 20, with_stats=True)
         estep = A.distill_topk_step(x, eager.top_ids, eager.top_logprobs, w, tail=True)
         torch.cuda.synchronize()
         for a, b in zip(tuple(r) + tuple(s), tuple(eager) + tuple(estep)):
@@ -502,7 +502,7 @@ def test_longest_row():
     at = [cols - 1, 5, 2 ** 30 + 7, 2 ** 31 - 5]
     for n, j in enumerate(at):
         x[0, j] = 20.0 - n
-    r = A.token_logprobs(x, torch.tensor([cols - 1], device="cuda"), 6)
+    r = A.token_logprobs(x, torch.tensor([cols - 1], device="cuda"), 6, with_stats=True)
     s = float(np.exp([20.0, 19.0, 18.0, 17.0]).sum() + (cols - 4))
     assert r.top_ids[0].tolist() == at + [0, 1]
     assert abs(r.lse.item() - np.log(s)) < 1e-4
@@ -589,9 +589,10 @@ def test_forced_forward_plans(dtype, kind, how):
         for slots, tail in ((7, False), (7, True), (130, True)):
             ids, val = slots_for(rng, rows, cols, slots, tail, 0.2)
             xd, x64 = on_gpu(x, dtype, pad, offset)
-            r = A.distill_topk(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), tail=tail, plan=plan)
+            r = A.distill_topk(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), tail=tail, plan=plan,
+                               with_stats=True)
             same = A.distill_topk(xd, torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), tail=tail,
-                                  plan=forward_plan(rows=rows))
+                                  plan=forward_plan(rows=rows), with_stats=True)
             # the two kernels against each other (the chosen one is checked against 64 bits everywhere else)
             want, _ = ref.distill(x64, ids, val, 1.0, tail)
             big = 40.0 + np.abs(want)
@@ -655,7 +656,7 @@ def test_plan_refusals_on_the_device():
     for p in bad:
         with pytest.raises(A.ArgreduceError):
             A.token_logprobs(x, tok, 3, plan=p)
-    s = A.token_logprobs(x, tok).stats
+    s = A.token_logprobs(x, tok, with_stats=True).stats
     for p in (grad_plan(0), grad_plan(1, 512), forward_plan(), stream_plan()):
         with pytest.raises(A.ArgreduceError):
             A.token_logprobs_backward(x, tok, s, torch.ones(4, device="cuda"), plan=p)
