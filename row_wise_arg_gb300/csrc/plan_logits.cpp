@@ -101,11 +101,12 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
             return ARGR_OK;
         }
     }
-    // Clusters until there are three CTAs per SM, a group per thread. Where the rows
-    // alone are that many, about eight groups per thread: small CTAs, whose phases overlap
-    // ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads;
+    // Clusters until there are three CTAs for two SMs, a group per thread ([32, 202048]
+    // bf16, top 20: 32, 23, 24 us with 16, 8, 4 CTAs; [64, 202048], 64 slots: 25, 16 us with 16, 8).
+    // Where the rows alone are three per SM, about eight groups per thread: small CTAs, whose phases
+    // overlap ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads;
     // [512, 100003] f16, 32 slots: 29, 25, 34 us with 512, 256, 128).
-    while (out->cluster < std::min(16, caps.max_cluster) && rows * out->cluster < 3 * caps.sm_count &&
+    while (out->cluster < std::min(16, caps.max_cluster) && 2 * rows * out->cluster < 3 * caps.sm_count &&
            groups / (2 * out->cluster) >= 128)
         out->cluster *= 2;
     const int64_t per_cta = groups / out->cluster;

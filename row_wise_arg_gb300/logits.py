@@ -43,44 +43,47 @@ class DistillLoss(NamedTuple):
     stats: Optional[torch.Tensor]  #: [..., 4] what the backward pass needs: row maximum, log sum, log sum of the tail, 0
 
 
+_CODES = {torch.float32: _lib.ARGR_F32, torch.float16: _lib.ARGR_F16, torch.bfloat16: _lib.ARGR_BF16}
+
+
 def _rows(x, dtype):
     """(rows, cols, row stride, type code) of logits."""
     if not x.is_cuda:
         raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
-    code = dtype_code(x, dtype)
-    if code > _lib.ARGR_BF16:
+    code = _CODES.get(x.dtype) if dtype is None else dtype_code(x, dtype)
+    if code is None or code > _lib.ARGR_BF16:
         raise TypeError("logits must be float32, float16 or bfloat16")
-    n = x.dim()
+    shape, stride = x.shape, x.stride()
+    n = len(shape)
     if n == 0:
         raise ValueError("logits must have at least one dimension")
-    shape = x.shape
     cols = shape[-1]
     if cols == 0:
         raise ValueError("logits must have a vocabulary of at least one")
-    if cols > 1 and x.stride(-1) != 1:
+    if stride[-1] != 1 and cols > 1:
         raise ValueError("the last dimension of logits must be contiguous")
+    if n == 2:
+        return shape[0], cols, stride[0] if shape[0] > 1 else cols, code
     if n == 1:
         return 1, cols, cols, code
-    if n > 2:
-        try:
-            x = x.view(-1, cols)
-        except RuntimeError:
-            raise ValueError("the leading dimensions of logits must be evenly spaced (make it contiguous)") from None
-    rows = x.shape[0]
-    return rows, cols, x.stride(0) if rows > 1 else cols, code
+    try:
+        x = x.view(-1, cols)
+    except RuntimeError:
+        raise ValueError("the leading dimensions of logits must be evenly spaced (make it contiguous)") from None
+    return x.shape[0], cols, x.stride(0) if x.shape[0] > 1 else cols, code
 
 
 def _arg(t, what, dtype, shape, device):
     """Data pointer of an argument that must be a contiguous tensor of this type and shape on the logits' device."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous tensor on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous tensor on {device}")
 
 
 def _plan(plan):
@@ -111,21 +114,22 @@ def _forward_logprobs(x, tokens, top_k, temperature, with_stats, dtype, plan, st
         raise ValueError(f"top_k must be in [0, {min(cols, _lib.LOGITS_MAX_TOP)}], got {top_k}")
     entropy = _empty(lead, dtype=_F32, device=dev)
     lse = _empty(lead, dtype=_F32, device=dev)
-    logprob = ids = top = stats = None
+    logprob = ids = top = stats = p_logprob = p_ids = p_top = p_stats = None
     if with_stats:
         stats = _empty((*lead, 4), dtype=_F32, device=dev)
+        p_stats = stats.data_ptr()
     if tok is not None:
         logprob = _empty(lead, dtype=_F32, device=dev)
+        p_logprob = logprob.data_ptr()
     if top_k:
         ids = _empty((*lead, top_k), dtype=_I64, device=dev)
         top = _empty((*lead, top_k), dtype=_F32, device=dev)
-    st = _LIB.argreduce_logprobs(
-        x.data_ptr(), code, rows, cols, stride, temperature, tok, top_k,
-        logprob.data_ptr() if logprob is not None else None, entropy.data_ptr(), lse.data_ptr(),
-        ids.data_ptr() if top_k else None, top.data_ptr() if top_k else None,
-        stats.data_ptr() if with_stats else None, _plan(plan),
-        _stream_ptr(stream, x.get_device()) or None)
-    _check(st, "argreduce_logprobs")
+        p_ids, p_top = ids.data_ptr(), top.data_ptr()
+    st = _LIB.argreduce_logprobs(x.data_ptr(), code, rows, cols, stride, temperature, tok, top_k, p_logprob,
+                                 entropy.data_ptr(), lse.data_ptr(), p_ids, p_top, p_stats, _plan(plan),
+                                 _stream_ptr(stream, dev.index) or None)
+    if st != ARGR_OK:
+        raise ArgreduceError(st, "argreduce_logprobs")
     return logprob, entropy, lse, ids, top, stats
 
 
