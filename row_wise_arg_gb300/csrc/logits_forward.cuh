@@ -176,7 +176,7 @@ __device__ __forceinline__ int block_count(int v, int* slot) {
 __device__ __forceinline__ void rank_keys(const unsigned long long* src, int n, int k, unsigned long long* out,
                                           unsigned long long* spare, int* count) {
     const int t = threadIdx.x, nt = blockDim.x;
-    if (n > kRankMax && n > k) {
+    if (n > k && (n > kRankMax || n > 4 * nt)) {
         // the k-th largest key, bit by bit; then only the keys that reach it
         unsigned long long at = 0;
         for (int b = 63; b >= 0; --b) {
@@ -208,6 +208,30 @@ __device__ __forceinline__ void rank_keys(const unsigned long long* src, int n, 
     __syncthreads();
 }
 
+// The k largest of `lists` lists (at most 32) of k distinct keys each, every list in
+// order and filled up with 0. A list's key at place ceil(k / lists) has that many keys of
+// its list before or at it, so at least k keys reach the least of these: only they are
+// ranked.
+__device__ __forceinline__ void merge_keys(const unsigned long long* src, int lists, int k, unsigned long long* cand,
+                                           unsigned long long* out, unsigned long long* spare, int* count) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long least = lane < lists ? src[lane * k + (k + lists - 1) / lists - 1] : ~0ull;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const unsigned long long d = __shfl_xor_sync(0xffffffffu, least, o);
+        if (d < least) least = d;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *count = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < lists * k; i += blockDim.x)
+        if (src[i] >= least && src[i] != 0) cand[atomicAdd(count, 1)] = src[i];
+    __syncthreads();
+    const int n = *count;
+    __syncthreads();
+    rank_keys(cand, n, k, out, spare, count);
+}
+
 // Take a scanned segment into the best keys so far; returns their number. `most`
 // is the thread's largest element of the segment (order32).
 template <class Tag>
@@ -216,23 +240,25 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
     constexpr int E = kGroupElems<Tag>;
     const int t = threadIdx.x, nt = blockDim.x, lane = t & 31;
     const int slots = sg.slots();
-    // A value that at least k elements reach (or 1: every element does).
-    unsigned at = 0;
-    for (int b = 31; b >= 0; --b) {
-        const unsigned trial = at | 1u << b;
-        const int n = __syncthreads_count(most >= trial);
-        if (n >= k) {
-            at = trial;
-            if (n <= k + k / 4 + 2) break;
+    // A value that at least k elements reach (or 1: every element does): near the
+    // k-th largest of the threads' values, or (exact) that one.
+    const auto threshold = [&](bool exact) {
+        unsigned v = 0;
+        for (int b = 31; b >= 0; --b) {
+            const unsigned trial = v | 1u << b;
+            const int n = __syncthreads_count(most >= trial);
+            if (n >= k) {
+                v = trial;
+                if (!exact && n <= k + k / 4 + 2) break;
+            }
         }
-    }
-    if (have == k) {
-        const unsigned last = static_cast<unsigned>(sh.best[k - 1] >> 32);
-        if (last > at) at = last;
-    }
-    if (at == 0) at = 1;
-    // Mode 0 looks into every slot that reaches `at`. Mode 1, where fewer than k slots
-    // exceed it and very many equal it (a masked row, whose -inf fill the places that its
+        if (have == k) v = max(v, static_cast<unsigned>(sh.best[k - 1] >> 32));
+        return v > 1 && v < kOrderNegInf ? kOrderNegInf : max(v, 1u);  // (nothing lies between a NaN and -inf)
+    };
+    unsigned at = threshold(false);
+    bool exact = false;
+    // Mode 0 looks into every slot that reaches `at`, or exceeds it where many equal
+    // it and k exceed it. Mode 1, where fewer than k slots exceed it and many equal it (a masked row, whose -inf fill the places that its
     // few numbers leave): into those that exceed it, and takes the first elements that equal it in
     // order. Mode 2, where still too many reach it: into the k first by (largest element,
     // position), found exactly.
@@ -278,62 +304,77 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
         const int picked = sh.count[0];
         if (mode == 0) {
             const int over = picked - sh.count[2];  // slots that exceed it
-            if (over < k && picked > 2 * k + 32) {
-                mode = 1;
+            if (over < picked && (picked > 2 * k + 32 || picked * E > sh.room)) {
+                if (over < k) mode = 1;
+                else ++at;
                 continue;
             }
         }
+        const auto too_many = [&]() {  // first a better threshold, then the exact way
+            if (exact) {
+                mode = 2;
+            } else {
+                at = threshold(true);
+                exact = true;
+                mode = 0;
+            }
+        };
         if (picked > kListGroups && mode != 2) {
-            mode = 2;
+            too_many();
             continue;
         }
-        // the picked slots' elements, 32 / E slots per warp at a time
-        for (int p0 = (t >> 5) * (32 / E); p0 < picked; p0 += (nt >> 5) * (32 / E)) {
-            const int p = p0 + lane / E;
-            unsigned long long key = 0;
-            if (p < picked) {
-                int lo, n;
-                sg.range(sh.list[p], lo, n);
-                const int j = lane % E;
-                if (j < n) {
-                    key = order_key(widen_elem<Tag>(ld_scalar(row + lo + j)), lo + j);
+        // the picked slots' elements, U times 32 / E slots per warp at a time
+        constexpr int U = 4, S = 32 / E;
+        for (int p0 = (t >> 5) * (U * S); p0 < picked; p0 += (nt >> 5) * (U * S)) {
+            float x[U];
+            int at_j[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = p0 + u * S + lane / E;
+                int lo = 0, n = 0;
+                if (p < picked) sg.range(sh.list[p], lo, n);
+                at_j[u] = lane % E < n ? lo + lane % E : -1;
+                x[u] = at_j[u] >= 0 ? widen_elem<Tag>(ld_scalar(row + at_j[u])) : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                unsigned long long key = 0;
+                if (at_j[u] >= 0) {
+                    key = order_key(x[u], at_j[u]);
                     const unsigned o = static_cast<unsigned>(key >> 32);
                     if (o < at || (o == at && mode == 1)) key = 0;
                 }
+                const unsigned got = __ballot_sync(0xffffffffu, key != 0);
+                if (got == 0) continue;  // (of the whole warp)
+                int base = 0;
+                if (lane == 0) base = atomicAdd(&sh.count[1], __popc(got));
+                base = __shfl_sync(0xffffffffu, base, 0);
+                const int q = base + __popc(got & ((1u << lane) - 1u));
+                if (key != 0 && q < sh.room) sh.cand[q] = key;
             }
-            const unsigned got = __ballot_sync(0xffffffffu, key != 0);
-            int base = 0;
-            if (lane == 0 && got) base = atomicAdd(&sh.count[1], __popc(got));
-            base = __shfl_sync(0xffffffffu, base, 0);
-            const int q = base + __popc(got & ((1u << lane) - 1u));
-            if (key != 0 && q < sh.room) sh.cand[q] = key;
         }
         __syncthreads();
         if (sh.count[1] > sh.room && mode != 2) {
-            mode = 2;
+            too_many();
             continue;
         }
         if (mode == 1 && sh.count[1] < k && t < 32) {
-            // the first warp fills up to k, in order: such elements lie close (a warp that still reads
-            // the count above sees at most k, which fits)
+            // the first warp fills up to k, in order, from the slots that reach `at` (a warp that still
+            // reads the count above sees at most k, which fits)
             int n = sh.count[1];
-            const int end = sg.tail_hi;
-            for (int j0 = sg.head_lo; j0 < end && n < k;) {
-                constexpr int U = 4;
-                float x[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    x[u] = end - j0 > 32 * u + lane ? widen_elem<Tag>(ld_scalar(row + j0 + 32 * u + lane)) : 0.0f;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const bool in = end - j0 > 32 * u + lane && order32(x[u]) == at;
+            for (int s0 = 0; s0 < slots && n < k; s0 += 32) {
+                unsigned hit = __ballot_sync(0xffffffffu, s0 + lane < slots && sh.big[s0 + lane] >= at);
+                while (hit && n < k) {
+                    int lo, size;
+                    sg.range(s0 + __ffs(hit) - 1, lo, size);
+                    hit &= hit - 1;
+                    const float x = lane < size ? widen_elem<Tag>(ld_scalar(row + lo + lane)) : 0.0f;
+                    const bool in = lane < size && order32(x) == at;
                     const unsigned got = __ballot_sync(0xffffffffu, in);
                     const int q = n + __popc(got & ((1u << lane) - 1u));
-                    if (in && q < k) sh.cand[q] = order_key(x[u], j0 + 32 * u + lane);
+                    if (in && q < k) sh.cand[q] = order_key(x, lo + lane);
                     n += __popc(got);
                 }
-                if (end - j0 <= 32 * U) break;
-                j0 += 32 * U;
             }
             if (lane == 0) sh.count[1] = n < k ? n : k;
         }
@@ -422,7 +463,6 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
             if (at >= part.count) break;
         }
         c = block_softsum(c, scale2, red);
-        const unsigned long long* best = sh.best;
         if (ranks > 1) {
             cluster_wait();
             if (t == 0) {
@@ -448,8 +488,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
                 c = warp_softsum(d, scale2);
             }
             if constexpr (TOP) {
-                rank_keys(gathered, ranks * k, k, sh.cand, sh.cand + ARGR_LOGITS_MAX_TOP, count);
-                best = sh.cand;
+                merge_keys(gathered, ranks, k, sh.cand, sh.best, sh.best + ARGR_LOGITS_MAX_TOP, count);
             }
         }
         if (t == 0) {
@@ -471,7 +510,7 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
         if constexpr (TOP) {
             __syncthreads();
             for (int i = t; i < k; i += blockDim.x) {
-                const unsigned long long key = best[i];
+                const unsigned long long key = sh.best[i];
                 const float v = order_value(static_cast<unsigned>(key >> 32));
                 if (pr.top_ids) pr.top_ids[r * k + i] = key_index(key);
                 if (pr.top_logprobs)

@@ -55,11 +55,14 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
     out->blocks_per_row = 1;
     out->path = forward(what) ? ARGR_PATH_LOGITS : ARGR_PATH_LOGITS_GRAD;
     if (out->path == ARGR_PATH_LOGITS_GRAD) {
-        // chunks of about 64 KB (four groups per thread)
+        // chunks of about 64 KB (four groups per thread); down to one group per thread
+        // while that leaves fewer than four CTAs per SM
         out->block = 256;
         out->grid_rows = std::min<int64_t>(rows, 65535);
         const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
-        out->blocks_per_row = std::min<int64_t>(4096, std::max<int64_t>(1, (groups + 1023) / 1024));
+        int64_t chunks = std::max<int64_t>(1, (groups + 1023) / 1024);
+        chunks = std::max(chunks, std::min((groups + 255) / 256, (4 * static_cast<int64_t>(caps.sm_count) + rows - 1) / rows));
+        out->blocks_per_row = std::min<int64_t>(4096, chunks);
         return ARGR_OK;
     }
     const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32);
@@ -101,20 +104,25 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
             return ARGR_OK;
         }
     }
-    // Clusters until there are three CTAs for two SMs, a group per thread ([32, 202048]
+    // Clusters until there are about three CTAs for two SMs, a group per thread, and
+    // 256 threads where more than two CTAs per SM would make a second wave ([32, 202048]
     // bf16, top 20: 32, 23, 24 us with 16, 8, 4 CTAs; [64, 202048], 64 slots: 25, 16 us with 16, 8).
     // Where the rows alone are three per SM, about eight groups per thread: small CTAs, whose phases
     // overlap ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads;
     // [512, 100003] f16, 32 slots: 29, 25, 34 us with 512, 256, 128).
-    while (out->cluster < std::min(16, caps.max_cluster) && 2 * rows * out->cluster < 3 * caps.sm_count &&
+    while (out->cluster < std::min(16, caps.max_cluster) && 5 * rows * out->cluster < 7 * caps.sm_count &&
            groups / (2 * out->cluster) >= 128)
         out->cluster *= 2;
     const int64_t per_cta = groups / out->cluster;
     if (out->cluster == 1 && rows >= 3 * caps.sm_count) {
         while (out->block > 32 && out->block * 8 > per_cta + per_cta / 8) out->block /= 2;
     } else {
+        if (rows * out->cluster > ctas) out->block = 256;
         while (out->block > 32 && out->block / 2 >= per_cta) out->block /= 2;
     }
+    // the threshold for alternatives needs more threads than alternatives to be near them
+    if (!distill)
+        while (out->block < 512 && out->block < 2 * k) out->block *= 2;
     return ARGR_OK;
 }
 
