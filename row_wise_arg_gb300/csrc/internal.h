@@ -68,8 +68,6 @@ struct Problem {
 };
 
 int elem_size(int dtype);
-// Properties of the current device (api.cpp), cached per device.
-argr_status current_caps(argr_caps* out);
 
 // Planner (plan.cpp): pure host code. `base_aligned`: x is 16-byte aligned.
 argr_status make_plan(int64_t rows, int64_t cols, int dtype, int op, const argr_caps& caps, bool base_aligned,

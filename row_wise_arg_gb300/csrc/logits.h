@@ -7,6 +7,9 @@
 
 namespace argr {
 
+// Properties of the current device (api.cpp), cached per device.
+argr_status current_caps(argr_caps* out);
+
 struct LogitsProblem {
     const void* x;
     int dtype;

@@ -685,3 +685,15 @@ def test_step_whose_copies_never_land():
         assert A.argreduce_read_error(0, 0) == _lib.ARGR_OK
     got = A.distill_topk_step(x, ids, val, w, tail=True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "distill.py")
+    spec = importlib.util.spec_from_file_location("example_distill", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, agree, rewards = example.main(rows=64, vocab=5003, steps=25, say=lambda s: None)
+    assert losses[-1] < 0.5 * losses[0] and agree > 0.9
+    assert sum(rewards[-5:]) > sum(rewards[:5]) + 0.5
