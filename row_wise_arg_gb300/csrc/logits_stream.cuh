@@ -350,6 +350,28 @@ __device__ __forceinline__ int warp_places(int mine, int* n) {
     return first;
 }
 
+// The k largest of n <= 32 R keys (0: none) to their places in `out`, by counting; every lane holds R.
+template <int R>
+__device__ __forceinline__ void rank_lane_keys(const unsigned long long* keys, int n, int k, unsigned long long* out) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long mine[R];
+    int rank[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        mine[u] = lane + 32 * u < n ? keys[lane + 32 * u] : 0ull;
+        rank[u] = 0;
+    }
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long other = keys[j];
+#pragma unroll
+        for (int u = 0; u < R; ++u) rank[u] += other > mine[u];
+    }
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+        if (mine[u] != 0 && rank[u] < k) out[rank[u]] = mine[u];
+}
+
 // The row's k first alternatives, in order, as keys in cand[kStreamCands, + k),
 // from the largest elements of its slots (big), of its tiles of 32 groups (tile)
 // and of the streaming threads (most). The finisher shares its scheduler with
@@ -474,23 +496,12 @@ __device__ __forceinline__ void warp_top(const WideRow<Tag>& row, int k, const u
         warp_prune(cand, n, k, spare);
         n = k;
     }
-    // in order, by counting: up to six keys per lane (0: none)
-    unsigned long long mine[kRankKeys / 32];
-    int rank[kRankKeys / 32];
-#pragma unroll
-    for (int u = 0; u < kRankKeys / 32; ++u) {
-        mine[u] = lane + 32 * u < n ? cand[lane + 32 * u] : 0ull;
-        rank[u] = 0;
-    }
-    for (int j = 0; j < n; ++j) {
-        const unsigned long long other = cand[j];
-#pragma unroll
-        for (int u = 0; u < kRankKeys / 32; ++u)
-            if (u == 0 || 32 * u < n) rank[u] += other > mine[u];
-    }
-#pragma unroll
-    for (int u = 0; u < kRankKeys / 32; ++u)
-        if (mine[u] != 0 && rank[u] < k) spare[rank[u]] = mine[u];
+    // in order, by counting
+    const int per_lane = (n + 31) / 32;
+    if (per_lane <= 1) rank_lane_keys<1>(cand, n, k, spare);
+    else if (per_lane == 2) rank_lane_keys<2>(cand, n, k, spare);
+    else if (per_lane == 3) rank_lane_keys<3>(cand, n, k, spare);
+    else rank_lane_keys<kRankKeys / 32>(cand, n, k, spare);
     __syncwarp();
 }
 
