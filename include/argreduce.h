@@ -96,7 +96,7 @@ typedef enum {
     ARGR_PATH_LOGITS_GRAD = 10, /* vocabulary rows, gradients: a row in `blocks_per_row` chunks, a
                               CTA of `block` threads each */
     ARGR_PATH_LOGITS_STEP = 11, /* argreduce_distill_step: as ARGR_PATH_LOGITS, the row held in the shared
-                              memory of its CTAs (at most 108 KB each) */
+                              memory of its CTAs (about 40 KB each, at most 108) */
     ARGR_PATH_LOGITS_STREAM = 12, /* vocabulary rows, forward: `grid_rows` persistent CTAs of `block` threads,
                               `group` (1 to 3) of their warps finish rows while the others read on */
     ARGR_PATH_STREAM = 4   /* every warp streams a contiguous range of rows through its own

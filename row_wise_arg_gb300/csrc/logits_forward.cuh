@@ -17,6 +17,13 @@
 // picks the groups, usually hardly more than k of them; their elements are read
 // again (from L2) and the few that reach the threshold are ranked by counting. Where ties
 // make more groups reach it, the k first groups are found exactly.
+//
+// Bound by latency for few rows: [32, 202048] bf16, clusters of 8 CTAs of 512 threads, in a
+// graph: 5.5 us (13 MB, 2.4 TB/s), 19.8 us with the top 20 (the threshold's barriers, the second read
+// and the exchange over the cluster). For many rows by instruction issue and the barriers
+// between a CTA's phases: [8192, 32000] bf16 96 us, 5.5 TB/s; [4096, 32000] f16, top 5, 77 us,
+// 3.4 TB/s; [512, 100003] f16, 32 slots and a tail, 24.7 us, 4.2 TB/s (one wave: all CTAs read at
+// first and all finish at last).
 #pragma once
 
 #include "logits_common.cuh"

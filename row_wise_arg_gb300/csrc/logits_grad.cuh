@@ -3,10 +3,16 @@
 //
 // Where the gradient's row lies as x's does within 32 bytes (always when both are
 // whole tensors, or one is the other) a thread handles 64-byte groups, two in flight;
-// otherwise element by element. The few single entries (the token, the slots'
+// otherwise words of the size that both allow. The few single entries (the token, the slots'
 // indices) are written a second time after the dense pass, by the same thread
 // or behind a barrier. grad may be x itself: every element is read by the thread that writes it,
 // and the single entries are read before the dense pass writes any.
+//
+//   log probabilities: dx_j = ((g_lse - g_lp) p_j - g_H p_j (log p_j + H) + [j = token] g_lp) / T
+//   distillation:      dx_j = g (w p_j - q_j) / T at a slot's index, g w' p_j / T elsewhere
+//
+// Bound by the memory: [2048, 202048] bf16 239 us, 6.9 TB/s read and written; [1024, 262144]
+// bf16, 64 slots, 157 us, 6.9 TB/s; [1024, 100000] f32 121 us, 6.8 TB/s (a copy: 6.8).
 #pragma once
 
 #include "logits_common.cuh"

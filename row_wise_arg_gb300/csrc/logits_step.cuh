@@ -5,14 +5,25 @@
 // First pass: softmax sums of the part, a stage as it lands, exchanged across the cluster.
 // Second pass: the gradient, from shared memory. So x is read once and the
 // gradient written once, where a forward and a backward kernel read x twice; the
-// exponential is taken twice. Four CTAs per SM, at different points of this, keep
-// both directions of the memory busy.
+// exponential is taken twice. Parts of about 40 KB, so that five CTAs or more per SM, at
+// different points of this, keep both directions of the memory busy.
+//
+//   p_j = exp2((x_j - m) scale2 - log2 s), (m, s) joined over the cluster;
+//   dx_j = w p_j, and at the elements that slots name (Q + tail) p_j - q_j. With a
+//   tail bucket the named elements are left out of the sums (-inf in their place in shared
+//   memory) and summed by themselves.
 //
 // A CTA's time is a chain: copies, sums, exchange, gradient; what is not memory
-// in it (about 12 of 23 thousand cycles for 50 KB) bounds the kernel. Hence: every warp
-// sends its own sums to every CTA and joins all of them itself (one cluster barrier,
-// no CTA-wide reduction before or after it), and nothing is loaded where it is
-// used.
+// in it (about half) bounds the kernel. Hence: every warp sends its own sums to every
+// CTA and joins all of them itself (one cluster barrier, no CTA-wide reduction before
+// or after it), and nothing is loaded where it is used.
+//
+// [1024, 202048] bf16, 64 slots and a tail: 154 us, 5.4 TB/s read and written (a forward and a
+// backward kernel: 80 + 122 us). [333, 50021] f32, 100 slots, rows 50028 apart: 36 us, 3.6 TB/s.
+// Tried and slower: reading the part a second time from L2 instead of keeping it; a
+// persistent CTA that sums one row while it writes the gradient of the one before
+// (273 against 198 us then); loads per thread instead of bulk copies; a bit map of the
+// named elements instead of -inf in their place.
 //
 // The waits for copies are bounded. One that runs out is recorded
 // (argreduce_read_error); its CTA goes on with what is in shared memory, so that the cluster's
