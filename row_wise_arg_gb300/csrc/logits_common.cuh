@@ -54,6 +54,29 @@ __device__ __forceinline__ typename Tag::raw narrow_elem(float v) {
 }
 
 // ---------------------------------------------------------------------------
+// Order of the alternatives: larger values first, equal ones (both zeros are
+// equal) by index, NaNs after every number. order32() is larger for an earlier
+// value, at least 1; a key adds the index and is larger for an earlier
+// alternative. order_value() undoes order32() (a zero comes back as +0).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ unsigned order32(float v) {
+    const unsigned b = __float_as_uint(v + 0.0f);
+    const unsigned u = b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
+    return v != v ? 1u : u;
+}
+constexpr unsigned kOrderNegInf = 0x007fffffu;  // order32 of -inf, the least number
+__device__ __forceinline__ float order_value(unsigned u) {
+    const unsigned b = u ^ ((u & 0x80000000u) ? 0x80000000u : 0xffffffffu);
+    return u == 1u ? quiet_nan() : __uint_as_float(b);
+}
+__device__ __forceinline__ unsigned long long order_key(float v, int index) {
+    return static_cast<unsigned long long>(order32(v)) << 32 | (0xffffffffu - static_cast<unsigned>(index));
+}
+__device__ __forceinline__ int key_index(unsigned long long k) {
+    return static_cast<int>(0xffffffffu - static_cast<unsigned>(k));
+}
+
+// ---------------------------------------------------------------------------
 // Softmax statistics.
 // ---------------------------------------------------------------------------
 struct SoftSum {
@@ -88,10 +111,7 @@ struct SoftSum {
 
 // The warp's triple, in every lane: one common reference, then plain sums.
 __device__ __forceinline__ SoftSum warp_softsum(SoftSum c, float scale2) {
-    float to = c.m;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
-    c.rebase(to, scale2);
+    c.rebase(order_value(__reduce_max_sync(0xffffffffu, order32(c.m))), scale2);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
         c.s += __shfl_xor_sync(0xffffffffu, c.s, o);
@@ -100,26 +120,34 @@ __device__ __forceinline__ SoftSum warp_softsum(SoftSum c, float scale2) {
     return c;
 }
 
-// The CTA's triple, in every thread of warp 0. `smem` holds 3 * 32 floats.
-// Contains __syncthreads().
-__device__ __forceinline__ SoftSum block_softsum(SoftSum c, float scale2, float* smem) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+// The CTA's triple in two steps with a barrier between them: every warp's to `smem`
+// (3 * 32 floats), and the whole in every thread of the warp that asks.
+__device__ __forceinline__ void softsum_to(SoftSum c, float scale2, float* smem) {
     c = warp_softsum(c, scale2);
-    __syncthreads();
-    if (lane == 0) {
-        smem[warp] = c.m;
-        smem[32 + warp] = c.s;
-        smem[64 + warp] = c.t;
+    if ((threadIdx.x & 31) == 0) {
+        smem[threadIdx.x >> 5] = c.m;
+        smem[32 + (threadIdx.x >> 5)] = c.s;
+        smem[64 + (threadIdx.x >> 5)] = c.t;
     }
-    __syncthreads();
-    if (warp != 0) return c;
+}
+__device__ __forceinline__ SoftSum softsum_from(float scale2, const float* smem) {
+    const int lane = threadIdx.x & 31;
     SoftSum r;
-    if (lane < nwarps) {
+    if (lane < static_cast<int>(blockDim.x >> 5)) {
         r.m = smem[lane];
         r.s = smem[32 + lane];
         r.t = smem[64 + lane];
     }
     return warp_softsum(r, scale2);
+}
+
+// Both, in every thread of warp 0. Contains __syncthreads().
+__device__ __forceinline__ SoftSum block_softsum(SoftSum c, float scale2, float* smem) {
+    __syncthreads();
+    softsum_to(c, scale2, smem);
+    __syncthreads();
+    if (threadIdx.x < 32) c = softsum_from(scale2, smem);
+    return c;
 }
 
 // Sum over the CTA, in every thread and in a fixed order. `smem` holds 32 values.
@@ -132,28 +160,6 @@ __device__ __forceinline__ float block_sum(float v, float* smem) {
     float r = 0.0f;
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) r += smem[w];
     return r;
-}
-// ---------------------------------------------------------------------------
-// Order of the alternatives: larger values first, equal ones (both zeros are
-// equal) by index, NaNs after every number. order32() is larger for an earlier
-// value, at least 1; a key adds the index and is larger for an earlier
-// alternative. order_value() undoes order32() (a zero comes back as +0).
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ unsigned order32(float v) {
-    const unsigned b = __float_as_uint(v + 0.0f);
-    const unsigned u = b ^ (static_cast<unsigned>(static_cast<int>(b) >> 31) | 0x80000000u);
-    return v != v ? 1u : u;
-}
-constexpr unsigned kOrderNegInf = 0x007fffffu;  // order32 of -inf, the least number
-__device__ __forceinline__ float order_value(unsigned u) {
-    const unsigned b = u ^ ((u & 0x80000000u) ? 0x80000000u : 0xffffffffu);
-    return u == 1u ? quiet_nan() : __uint_as_float(b);
-}
-__device__ __forceinline__ unsigned long long order_key(float v, int index) {
-    return static_cast<unsigned long long>(order32(v)) << 32 | (0xffffffffu - static_cast<unsigned>(index));
-}
-__device__ __forceinline__ int key_index(unsigned long long k) {
-    return static_cast<int>(0xffffffffu - static_cast<unsigned>(k));
 }
 
 // ---------------------------------------------------------------------------

@@ -13,17 +13,17 @@
 // element. Groups are contiguous, so in the order (largest element, position)
 // the k first groups hold the k first elements: an element of any other group
 // comes after the largest elements of k groups. A threshold that k of the
-// threads' own largest elements reach (found bit by bit with barrier counts)
+// threads' own largest elements reach (found among 32 of them, or bit by bit with barrier counts)
 // picks the groups, usually hardly more than k of them; their elements are read
 // again (from L2) and the few that reach the threshold are ranked by counting. Where ties
 // make more groups reach it, the k first groups are found exactly.
 //
-// Bound by latency for few rows: [32, 202048] bf16, clusters of 8 CTAs of 512 threads, in a
-// graph: 5.5 us (13 MB, 2.4 TB/s), 19.8 us with the top 20 (the threshold's barriers, the second read
-// and the exchange over the cluster). For many rows by instruction issue and the barriers
-// between a CTA's phases: [8192, 32000] bf16 96 us, 5.5 TB/s; [4096, 32000] f16, top 5, 77 us,
-// 3.4 TB/s; [512, 100003] f16, 32 slots and a tail, 24.7 us, 4.2 TB/s (one wave: all CTAs read at
-// first and all finish at last).
+// Bound by latency for few rows: [32, 202048] bf16, in a graph: 5.8 us (13 MB, 2.2 TB/s), 10.2 us
+// with the top 20 (the threshold, the second read, the merge over the cluster; most of it is code
+// that runs once, so short loops beat unrolled ones). For many rows by instruction issue and the
+// barriers between a CTA's phases: [8192, 32000] bf16 96 us, 5.5 TB/s, with the top 20 123 us,
+// 4.2 TB/s; [4096, 50257] bf16, top 20, 96 us, 4.3 TB/s; [512, 100003] f16, 32 slots and a tail, 24.7 us,
+// 4.2 TB/s (one wave: all CTAs read at first and all finish at last).
 #pragma once
 
 #include "logits_common.cuh"
@@ -32,6 +32,7 @@ namespace argr {
 
 constexpr int kFwdMaxBlock = 512;
 constexpr int kListGroups = 1024; // groups picked by a threshold, at most
+constexpr int kFewTop = 20;       // alternatives that 32 values find a threshold for
 constexpr int kRankMax = 512;     // candidates ranked by counting, at most
 
 // Add a group whose largest element is `big`. Without ENT, t is left alone (and
@@ -240,37 +241,59 @@ __device__ __forceinline__ void merge_keys(const unsigned long long* src, int li
 }
 
 // Take a scanned segment into the best keys so far; returns their number. `most`
-// is the thread's largest element of the segment (order32).
+// is the thread's largest element of the segment (order32). Begins with a barrier
+// that completes the segment's slots, and ends with one.
 template <class Tag>
 __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const Segment<Tag>& sg, int k, int have,
                                             unsigned most, const TopShared& sh) {
-    constexpr int E = kGroupElems<Tag>;
-    const int t = threadIdx.x, nt = blockDim.x, lane = t & 31;
+    using R = typename Tag::raw;
+    constexpr int E = kGroupElems<Tag>, P = 16 / static_cast<int>(sizeof(R));
+    const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5, warps = nt >> 5;
     const int slots = sg.slots();
-    // A value that at least k elements reach (or 1: every element does): near the
-    // k-th largest of the threads' values, or (exact) that one.
-    const auto threshold = [&](bool exact) {
-        unsigned v = 0;
-        for (int b = 31; b >= 0; --b) {
-            const unsigned trial = v | 1u << b;
-            const int n = __syncthreads_count(most >= trial);
-            if (n >= k) {
-                v = trial;
-                if (!exact && n <= k + k / 4 + 2) break;
-            }
-        }
+    const auto usable = [&](unsigned v) {  // as a threshold
         if (have == k) v = max(v, static_cast<unsigned>(sh.best[k - 1] >> 32));
         return v > 1 && v < kOrderNegInf ? kOrderNegInf : max(v, 1u);  // (nothing lies between a NaN and -inf)
     };
-    unsigned at = threshold(false);
-    bool exact = false;
+    // A value that at least k elements reach (or 1: every element does). Few alternatives: the k-th
+    // largest of 32 values, each the largest of a 32nd of the threads (1.5 k elements or fewer reach it,
+    // as a rule); one barrier, and every warp ranks them itself. More: the k-th largest of the threads'
+    // values or near it, bit by bit, a barrier each.
+    if (t < 3) sh.count[t] = t == 1 ? have : 0;
+    unsigned at = 0;
+    if (k <= kFewTop) {
+        unsigned* tops = reinterpret_cast<unsigned*>(sh.cand);  // (all have read it, a barrier ago)
+        const int share = warps > 1 ? 1 << (32 - __clz(warps - 1)) : 1;  // threads, a power of two
+        unsigned v = most;
+        for (int o = share >> 1; o >= 1; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if ((lane & (share - 1)) == 0) tops[t / share] = v;
+        if (t < 32 && t >= nt / share) tops[t] = 0u;
+        __syncthreads();
+        v = tops[lane];
+        int over = 0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(tops + j);
+            over += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+        }
+        at = __reduce_min_sync(0xffffffffu, over < k ? v : ~0u);
+    } else {
+        for (int b = 31; b >= 0; --b) {
+            const unsigned trial = at | 1u << b;
+            const int n = __syncthreads_count(most >= trial);
+            if (n < k) continue;
+            at = trial;
+            if (n <= k + k / 4 + 2) break;
+        }
+    }
+    at = usable(at);
+    bool exact = false, again = false;
     // Mode 0 looks into every slot that reaches `at`, or exceeds it where many equal
     // it and k exceed it. Mode 1, where fewer than k slots exceed it and many equal it (a masked row, whose -inf fill the places that its
     // few numbers leave): into those that exceed it, and takes the first elements that equal it in
     // order. Mode 2, where still too many reach it: into the k first by (largest element,
     // position), found exactly.
     int mode = 0, cut = slots;  // cut: of the slots whose largest element equals `at`, those up to here
-    for (;;) {
+    for (;; again = true) {
         if (mode == 2) {
             at = 0;
             for (int b = 31; b >= 0; --b) {
@@ -289,21 +312,33 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
             }
             cut = lo;
         }
-        __syncthreads();
-        if (t == 0) {
-            sh.count[0] = 0;
-            sh.count[1] = have;
-            sh.count[2] = 0;
+        if (again) {
+            __syncthreads();
+            if (t < 3) sh.count[t] = t == 1 ? have : 0;
+            __syncthreads();
         }
-        for (int i = t; i < have; i += nt) sh.cand[i] = sh.best[i];
-        __syncthreads();
         int equal = 0;
-        for (int i = t; i < slots; i += nt) {
-            const unsigned o = sh.big[i];
-            equal += o == at;
-            if (o > at || (o == at && i <= cut && mode != 1)) {
+        if (most >= at) {  // a thread looks at the slots that it wrote
+            const auto picks = [&](int i) {
+                const unsigned o = sh.big[i];
+                equal += o == at;
+                return o > at || (o == at && i <= cut && mode != 1);
+            };
+            for (int g = t; g < sg.body;) {
+                unsigned in = 0;
+                const int first = g;
+#pragma unroll 4
+                for (int u = 0; u < 32 && g < sg.body; ++u, g += nt) in |= static_cast<unsigned>(picks(g + 1)) << u;
+                if (in == 0) continue;
+                int p = atomicAdd(&sh.count[0], __popc(in));
+                for (; in; in &= in - 1, ++p)
+                    if (p < kListGroups) sh.list[p] = static_cast<unsigned short>(first + (__ffs(in) - 1) * nt + 1);
+            }
+            // the ragged ends: lane 0 of the first warp and of the last
+            for (int end = 0; end < 2; ++end) {
+                if (t != (end ? nt - 32 : 0) || !picks(end ? sg.body + 1 : 0)) continue;
                 const int p = atomicAdd(&sh.count[0], 1);
-                if (p < kListGroups) sh.list[p] = static_cast<unsigned short>(i);
+                if (p < kListGroups) sh.list[p] = static_cast<unsigned short>(end ? sg.body + 1 : 0);
             }
         }
         if (mode == 0 && equal) atomicAdd(&sh.count[2], equal);
@@ -321,7 +356,10 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
             if (exact) {
                 mode = 2;
             } else {
-                at = threshold(true);
+                unsigned v = 0;  // the k-th largest of the threads' values
+                for (int b = 31; b >= 0; --b)
+                    if (__syncthreads_count(most >= (v | 1u << b)) >= k) v |= 1u << b;
+                at = usable(v);
                 exact = true;
                 mode = 0;
             }
@@ -330,34 +368,42 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
             too_many();
             continue;
         }
-        // the picked slots' elements, U times 32 / E slots per warp at a time
-        constexpr int U = 4, S = 32 / E;
-        for (int p0 = (t >> 5) * (U * S); p0 < picked; p0 += (nt >> 5) * (U * S)) {
-            float x[U];
-            int at_j[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int p = p0 + u * S + lane / E;
-                int lo = 0, n = 0;
-                if (p < picked) sg.range(sh.list[p], lo, n);
-                at_j[u] = lane % E < n ? lo + lane % E : -1;
-                x[u] = at_j[u] >= 0 ? widen_elem<Tag>(ld_scalar(row + at_j[u])) : 0.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                unsigned long long key = 0;
-                if (at_j[u] >= 0) {
-                    key = order_key(x[u], at_j[u]);
-                    const unsigned o = static_cast<unsigned>(key >> 32);
-                    if (o < at || (o == at && mode == 1)) key = 0;
+        for (int i = t; i < have; i += nt) sh.cand[i] = sh.best[i];
+        // the picked slots' elements that reach `floor`, 16 bytes per lane, 8 slots per warp at a time
+        const unsigned floor = at + (mode == 1);
+        for (int p0 = 8 * warp; p0 < picked; p0 += 8 * warps) {
+            const int p = p0 + (lane >> 2);
+            if (p >= picked) continue;
+            const int slot = sh.list[p];
+            if (slot < 1 || slot > sg.body) {  // a ragged end, element by element
+                int first, n;
+                sg.range(slot, first, n);
+                for (int i = lane & 3; i < n; i += 4) {
+                    const unsigned long long key = order_key(widen_elem<Tag>(ld_scalar(row + first + i)), first + i);
+                    if (static_cast<unsigned>(key >> 32) < floor) continue;
+                    const int q = atomicAdd(&sh.count[1], 1);
+                    if (q < sh.room) sh.cand[q] = key;
                 }
-                const unsigned got = __ballot_sync(0xffffffffu, key != 0);
-                if (got == 0) continue;  // (of the whole warp)
-                int base = 0;
-                if (lane == 0) base = atomicAdd(&sh.count[1], __popc(got));
-                base = __shfl_sync(0xffffffffu, base, 0);
-                const int q = base + __popc(got & ((1u << lane) - 1u));
-                if (key != 0 && q < sh.room) sh.cand[q] = key;
+                continue;
+            }
+            const int lo = sg.body_lo + (slot - 1) * E + (lane & 3) * P;
+            const uint4 w = ld_stream16(row + lo);
+            const auto elem = [&](int e) {
+                if constexpr (P == 4) {
+                    return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
+                } else {
+                    const uint32_t v = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
+                    return Tag::widen(static_cast<uint16_t>(e & 1 ? v >> 16 : v & 0xffffu));
+                }
+            };
+            unsigned hits = 0;
+#pragma unroll
+            for (int e = 0; e < P; ++e) hits |= static_cast<unsigned>(order32(elem(e)) >= floor) << e;
+            if (hits == 0) continue;
+            int q = atomicAdd(&sh.count[1], __popc(hits));
+            for (; hits; hits &= hits - 1, ++q) {
+                const int e = __ffs(hits) - 1;
+                if (q < sh.room) sh.cand[q] = order_key(elem(e), lo + e);
             }
         }
         __syncthreads();
@@ -385,11 +431,10 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
             }
             if (lane == 0) sh.count[1] = n < k ? n : k;
         }
+        if (mode == 1) __syncthreads();
         break;
     }
-    __syncthreads();
     const int n = sh.count[1] < sh.room ? sh.count[1] : sh.room;
-    __syncthreads();
     rank_keys(sh.cand, n, k, sh.best, sh.best + ARGR_LOGITS_MAX_TOP, sh.count);
     return n < k ? n : k;
 }
@@ -417,8 +462,8 @@ inline __host__ __device__ int cand_room(int k, int group_elems) {
     return n < kRankMax ? kRankMax : n;
 }
 
-template <class Tag, bool TOP>
-__global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsProblem pr, float scale2, int ranks,
+template <class Tag, bool TOP, int BLOCK, int PER_SM>
+__global__ void __launch_bounds__(BLOCK, PER_SM) logprobs_kernel(const LogitsProblem pr, float scale2, int ranks,
                                                                    int seg_slots) {
     using R = typename Tag::raw;
     extern __shared__ __align__(16) unsigned char dyn[];
@@ -433,11 +478,11 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
     unsigned long long* gathered = nullptr;  // CTA 0: every CTA's best
     if constexpr (TOP) {
         sh.room = cand_room(k, kGroupElems<Tag>);
-        sh.cand = reinterpret_cast<unsigned long long*>(dyn);
+        sh.big = reinterpret_cast<unsigned*>(dyn);  // (seg_slots is a multiple of 4: `cand` is aligned to 16 bytes)
+        sh.cand = reinterpret_cast<unsigned long long*>(sh.big + seg_slots);
         sh.best = sh.cand + sh.room;
         gathered = sh.best + 2 * ARGR_LOGITS_MAX_TOP;
-        sh.big = reinterpret_cast<unsigned*>(gathered + (ranks > 1 ? ranks * k : 0));
-        sh.list = reinterpret_cast<unsigned short*>(sh.big + seg_slots);
+        sh.list = reinterpret_cast<unsigned short*>(gathered + (ranks > 1 ? ranks * k : 0));
         sh.count = count;
     }
     allow_dependents();
@@ -463,13 +508,17 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
             scan_segment<Tag, true, TOP, false>(d, row, sg, scale2, sh.big, nullptr, most, row + part.end());
             c.join(d, scale2);
             if constexpr (TOP) {
+                if (at + sg.body >= part.count) softsum_to(c, scale2, red);
                 have = take_segment<Tag>(row, sg, k, have, most, sh);
-                __syncthreads();
             }
             at += sg.body;
             if (at >= part.count) break;
         }
-        c = block_softsum(c, scale2, red);
+        if constexpr (!TOP) {
+            softsum_to(c, scale2, red);
+            __syncthreads();
+        }
+        if (t < 32) c = softsum_from(scale2, red);
         if (ranks > 1) {
             cluster_wait();
             if (t == 0) {
@@ -525,6 +574,8 @@ __global__ void __launch_bounds__(kFwdMaxBlock, 2) logprobs_kernel(const LogitsP
                         row_ln_s == neg_inf() ? neg_inf() : (v - row_m) / pr.temperature - row_ln_s;
             }
             __syncthreads();
+        } else if (ranks == 1 && r + slots < pr.rows) {
+            __syncthreads();  // `red` has been read
         }
     }
 }

@@ -58,12 +58,22 @@ cudaError_t launch_logprobs_t(const argr_plan& p, const LogitsProblem& pr) {
     const int slots = segment_slots<Tag>(p, pr.cols);
     if (pr.top_k == 0) {
         static KernelLaunchCache cache;
-        return launch_forward(logprobs_kernel<Tag, false>, cache, p, pr, 0, slots);
+        return launch_forward(logprobs_kernel<Tag, false, kFwdMaxBlock, 2>, cache, p, pr, 0, slots);
     }
-    static KernelLaunchCache cache;
+    // Alternatives need about 100 registers; with 64, what is spilled costs more than the CTAs that fewer
+    // registers leave room for bring ([4096, 50257] bf16, top 20, 256 threads: 127, 99, 111 us with 64,
+    // 80, 128 registers; [2048, 32000] f16, top 5, 128 threads: 41, 36, 42 with 64, 96, 128). All of
+    // them where the grid then still fits ([32, 202048] bf16, top 20: 15.8 and 10.5 us with 64 and 128).
+    static KernelLaunchCache caches[3];
     const size_t keys = cand_room(pr.top_k, kGroupElems<Tag>) + 2 * ARGR_LOGITS_MAX_TOP +
                         (p.cluster > 1 ? p.cluster * pr.top_k : 0);
-    return launch_forward(logprobs_kernel<Tag, true>, cache, p, pr, 8 * keys + 4 * slots + 2 * kListGroups, slots);
+    const size_t smem = 8 * keys + 4 * slots + 2 * kListGroups;
+    argr_caps caps;
+    if (current_caps(&caps) != ARGR_OK) return cudaErrorInvalidDevice;
+    if (p.block > 256 || p.grid_rows * p.cluster * p.block <= static_cast<int64_t>(caps.sm_count) * kFwdMaxBlock)
+        return launch_forward(logprobs_kernel<Tag, true, kFwdMaxBlock, 1>, caches[0], p, pr, smem, slots);
+    return p.block > 128 ? launch_forward(logprobs_kernel<Tag, true, 256, 3>, caches[1], p, pr, smem, slots)
+                         : launch_forward(logprobs_kernel<Tag, true, 128, 5>, caches[2], p, pr, smem, slots);
 }
 template <class Tag>
 cudaError_t launch_distill_t(const argr_plan& p, const LogitsProblem& pr) {

@@ -104,12 +104,33 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
             return ARGR_OK;
         }
     }
+    if (!distill && k > 0) {
+        // With alternatives: clusters while every CTA still has an SM of its own ([32, 202048] bf16, top 20:
+        // 10.4, 15.4 us with 4, 8 CTAs of 512, 256 threads; [100, 100000]: 11.0, 17.0 us with 1, 2). Then
+        // 512 threads; 256 for two CTAs per SM, and where neither smaller CTAs fit one wave nor 16 groups a
+        // thread suffice ([256, 128000] bf16, top 64: 45, 19 us with 512, 256; [700, 65536], top 40: 38, 23, 37
+        // us with 256, 128, 64; [4096, 50257], top 20: 118, 98, 110; [8192, 32000]: 182, 138, 122, 146 down to 32;
+        // [1000, 131072]: 63, 81 with 256, 128).
+        while (out->cluster < std::min(16, caps.max_cluster) && 2 * rows * out->cluster <= caps.sm_count &&
+               groups / (2 * out->cluster) >= 128)
+            out->cluster *= 2;
+        const int64_t per_cta = groups / out->cluster, n = rows * out->cluster;
+        if (n > caps.sm_count) {
+            out->block = 256;
+            while (out->block > 32 && per_cta <= 8 * out->block &&
+                   n > (out->block == 256 ? 3 : 640 / out->block) * static_cast<int64_t>(caps.sm_count))
+                out->block /= 2;
+            // the threshold for alternatives needs more threads than alternatives to be near them
+            while (out->block < 256 && out->block < 2 * k) out->block *= 2;
+        } else {
+            while (out->block > 32 && out->block / 2 >= per_cta && out->block > 2 * k) out->block /= 2;
+        }
+        return ARGR_OK;
+    }
     // Clusters until there are about three CTAs for two SMs, a group per thread, and
-    // 256 threads where more than two CTAs per SM would make a second wave ([32, 202048]
-    // bf16, top 20: 32, 23, 24 us with 16, 8, 4 CTAs; [64, 202048], 64 slots: 25, 16 us with 16, 8).
-    // Where the rows alone are three per SM, about eight groups per thread: small CTAs, whose phases
-    // overlap ([4096, 32000] f16, top 5: 127, 81, 70, 88 us with 512, 256, 128, 64 threads;
-    // [512, 100003] f16, 32 slots: 29, 25, 34 us with 512, 256, 128).
+    // 256 threads where more than two CTAs per SM would make a second wave ([64, 202048] bf16, 64 slots:
+    // 25, 16 us with 16, 8 CTAs). Where the rows alone are three per SM, about eight groups per thread:
+    // small CTAs, whose phases overlap ([512, 100003] f16, 32 slots: 29, 25, 34 us with 512, 256, 128 threads).
     while (out->cluster < std::min(16, caps.max_cluster) && 5 * rows * out->cluster < 7 * caps.sm_count &&
            groups / (2 * out->cluster) >= 128)
         out->cluster *= 2;
@@ -120,9 +141,6 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
         if (rows * out->cluster > ctas) out->block = 256;
         while (out->block > 32 && out->block / 2 >= per_cta) out->block /= 2;
     }
-    // the threshold for alternatives needs more threads than alternatives to be near them
-    if (!distill)
-        while (out->block < 512 && out->block < 2 * k) out->block *= 2;
     return ARGR_OK;
 }
 
