@@ -18,7 +18,7 @@
 // CTA and joins all of them itself (one cluster barrier, no CTA-wide reduction before
 // or after it), and nothing is loaded where it is used.
 //
-// [1024, 202048] bf16, 64 slots and a tail: 154 us, 5.4 TB/s read and written (a forward and a
+// [1024, 202048] bf16, 64 slots and a tail: 152 us, 5.4 TB/s read and written (a forward and a
 // backward kernel: 80 + 122 us). [333, 50021] f32, 100 slots, rows 50028 apart: 36 us, 3.6 TB/s.
 // Tried and slower: reading the part a second time from L2 instead of keeping it; a
 // persistent CTA that sums one row while it writes the gradient of the one before
