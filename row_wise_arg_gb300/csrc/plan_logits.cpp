@@ -23,8 +23,8 @@ bool valid_problem(int what, int64_t rows, int64_t cols, int dtype, int k) {
 // Finishing warps that keep up with the streaming ones. Measured (two CTAs per SM): a
 // row streams at 22 bytes per ns; a finish takes about 5 us, 0.1 us per slot of a
 // distillation, or 0.3 us per alternative and 4 ns per 128-byte group of the row.
-// [2048, 202048] bf16, top 20: 171, 156, 159 us with 1, 2, 3 of them; top 64: 236,
-// 190, 180 us; [4096, 65536] bf16, 32 slots: 116, 94 us with 1, 2.
+// [2048, 202048] bf16, top 20: 164, 152, 154 us with 1, 2, 3 of them; top 64: 222,
+// 176, 168 us; [4096, 65536] bf16, 32 slots: 112, 90 us with 1, 2.
 int stream_finishers(bool distill, int64_t row_bytes, int k) {
     const double row_us = row_bytes / 22.0e3;
     const double finish_us = 5.0 + (distill ? 0.1 * k : k > 0 ? 0.3 * k + 0.004 * (row_bytes / 128) : 0.0);
@@ -89,7 +89,7 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
     // Long rows, and enough of them to keep two persistent CTAs per SM busy: the
     // streaming kernel. Rows below the limits finish too often for it ([8192, 32000]
     // bf16: 120 us against 100 us with a CTA of 128 threads per row; [4096, 65536] bf16: 98
-    // against 104 us, with 20 alternatives 136 against 133 us); so does a last round that few CTAs
+    // against 104 us, with 20 alternatives 119 against 116 us); so does a last round that few CTAs
     // take part in ([512, 100003] f16, 32 slots: 27.4 against 24.5 us).
     const int es = dtype == ARGR_F32 ? 4 : 2;
     const bool distill = what != ARGR_LOGITS_LOGPROBS;
