@@ -9,7 +9,10 @@
 // take the loss, and prepare the buffer for the row that will use it next. Row i
 // uses buffer i mod (F + 1) and finisher i mod F; a pair of named barriers per
 // buffer hands it over ("full" from the streamers, "free" back), so that no
-// streaming warp waits as long as a finish takes less than F rows' time. The 4 KB
+// streaming warp waits as long as a finish takes less than F rows' time. A named barrier
+// counts warps, whoever they are, and successive rows of a buffer belong to different finishers: each
+// waits for its row only after the finisher of the row before has met the streamers there ("turn", a barrier per
+// pair of neighbours). Rows become complete in this order, so it delays nobody. The 4 KB
 // tiles of successive rows are dealt to the warps in one sequence, so that rows of few tiles keep
 // all warps equally busy.
 //
@@ -38,10 +41,12 @@ enum StreamMode { kStreamSums = 0, kStreamTop = 1, kStreamLoss = 2, kStreamLossT
 
 template <class Tag> constexpr int kWideElems = 2 * kGroupElems<Tag>;
 
-// Barriers of a buffer: one warp on the finishers' side.
+// Barriers of a buffer: one warp on the finishers' side; of a finisher: it waits, the one before it arrives.
 constexpr int kMaxFinishers = 3;
+static_assert(1 + 2 * (kMaxFinishers + 1) + kMaxFinishers <= 16, "named barriers of a CTA");
 __device__ __forceinline__ int full_bar(int buffer) { return 1 + 2 * buffer; }
 __device__ __forceinline__ int free_bar(int buffer) { return 2 + 2 * buffer; }
+__device__ __forceinline__ int turn_bar(int finisher) { return 1 + 2 * (kMaxFinishers + 1) + finisher; }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -593,7 +598,10 @@ __device__ __forceinline__ void finish_rows(const LogitsProblem& pr, float scale
         const int at = static_cast<int>(i % buffers);
         unsigned char* buf = dyn + at * lay.buffer;
         const WideRow<Tag> row(pr, r);
+        if (lay.finishers > 1 && i > 0) bar_sync(turn_bar(finisher), 64);
         bar_sync(full_bar(at), threads);
+        if (lay.finishers > 1 && r + ctas < pr.rows)
+            bar_arrive(turn_bar(finisher + 1 < lay.finishers ? finisher + 1 : 0), 64);
         SoftSum c = joined_sums(buf + lay.sums, lay.streamers, scale2);
         if constexpr (!LOSS) {
             const float ln_s = c.empty() ? neg_inf() : logf(c.s);
