@@ -72,11 +72,13 @@ __device__ __forceinline__ void add_group(SoftSum& c, const Group<Tag>& g, float
 
 // L2 prefetch of a CTA's part: the first kAheadBytes before anything else (also
 // before the wait for the previous grid), then, while the part is read, the bytes kAheadBytes ahead of
-// the loads. DRAM latency is then hidden without registers for loads in flight.
+// the loads. DRAM latency is then hidden without registers for loads in flight. (A caller's plan
+// may have more row slots than there are rows.)
 constexpr int kAheadBytes = 128 * 1024;
 template <class Tag>
 __device__ __forceinline__ void prefetch_part(const LogitsProblem& pr, int64_t r, int rank, int ranks) {
     using R = typename Tag::raw;
+    if (r >= pr.rows) return;
     const R* row = static_cast<const R*>(pr.x) + r * pr.row_stride;
     const Part<Tag> part(row, pr.cols, rank, ranks);
     prefetch_l2_range(row + part.begin(), row + part.end(), kAheadBytes);

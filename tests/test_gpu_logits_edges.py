@@ -33,3 +33,17 @@ def test_many_short_rows_per_persistent_cta(finishers):
         for tail in (False, True):
             ids, val = slots_for(rng, rows, cols, 5, tail, 0.2)
             check_distill(x, "f32", ids, val, 1.0, tail, plan=plan)
+
+
+@pytest.mark.parametrize("cluster,block,grid", [(1, 128, 700), (4, 64, 40), (2, 512, 9)])
+def test_plans_with_more_row_slots_than_rows(cluster, block, grid):
+    """CTAs without a row do nothing, a prefetch included: it would be of addresses past the logits."""
+    rng = np.random.default_rng(grid)
+    x = rng.normal(0, 3, (5, 30011)).astype(np.float32)
+    ids, val = slots_for(rng, 5, 30011, 9, True, 0.2)
+    for dtype in DT:
+        plan = forward_plan(cluster, block, grid, grid)
+        check_logprobs(x, dtype, rng.integers(-1, 30011, 5), 7, plan=plan)
+        check_distill(x, dtype, ids, val, 1.0, True, plan=plan, grad_plan=grad_plan(3, 128, grid),
+                      step_plan=step_plan(cluster, min(block, 256), grid))
+        check_logprobs(x, dtype, None, 7, plan=stream_plan(2, 512, grid))
