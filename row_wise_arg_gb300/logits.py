@@ -86,6 +86,37 @@ def _arg(t, what, dtype, shape, device):
     raise ValueError(f"{what} must be a contiguous tensor on {device}")
 
 
+def _side(stream, x):
+    """`stream` (a torch stream or a raw handle) as a torch stream, None where it is the current one."""
+    if not x.is_cuda:
+        return None
+    dev = x.get_device()
+    handle = _stream_ptr(stream, dev)
+    if handle == _stream_ptr(None, dev):
+        return None
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)
+    if stream.device != x.device:
+        raise ValueError(f"stream must be of {x.device}, got one of {stream.device}")
+    return stream
+
+
+def _under(side, given, call, *args, **kw):
+    """`call` with `side` as torch's current stream: what it allocates belongs to that stream, and automatic
+    differentiation runs the backward pass there, ordered with the streams that it takes gradients from and
+    gives them to. What was given is kept until that stream is done with it, what it returns until the present one is."""
+    here = torch.cuda.current_stream(side.device)
+    with torch.cuda.stream(side):
+        out = call(*args, **kw)
+    for t in given:
+        if t is not None:
+            t.record_stream(side)
+    for t in (out,) if isinstance(out, torch.Tensor) else out:
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 def _plan(plan):
     return ctypes.byref(plan) if plan is not None else None
 
@@ -106,7 +137,7 @@ def _grad_out(x, grad):
     return grad, stride
 
 
-def _forward_logprobs(x, tokens, top_k, temperature, with_stats, dtype, plan, stream):
+def _forward_logprobs(x, tokens, top_k, temperature, with_stats, dtype, plan):
     rows, cols, stride, code = _rows(x, dtype)
     lead, dev = x.shape[:-1], x.device
     tok = _arg(tokens, "tokens", _I64, lead, dev)
@@ -127,7 +158,7 @@ def _forward_logprobs(x, tokens, top_k, temperature, with_stats, dtype, plan, st
         p_ids, p_top = ids.data_ptr(), top.data_ptr()
     st = _LIB.argreduce_logprobs(x.data_ptr(), code, rows, cols, stride, temperature, tok, top_k, p_logprob,
                                  entropy.data_ptr(), lse.data_ptr(), p_ids, p_top, p_stats, _plan(plan),
-                                 _stream_ptr(stream, dev.index) or None)
+                                 _stream_ptr(None, dev.index) or None)
     if st != ARGR_OK:
         raise ArgreduceError(st, "argreduce_logprobs")
     return logprob, entropy, lse, ids, top, stats
@@ -135,10 +166,10 @@ def _forward_logprobs(x, tokens, top_k, temperature, with_stats, dtype, plan, st
 
 class _TokenLogprobsFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, tokens, top_k, temperature, dtype, plan, stream):
-        out = _forward_logprobs(x, tokens, top_k, temperature, True, dtype, plan, stream)
+    def forward(ctx, x, tokens, top_k, temperature, dtype, plan):
+        out = _forward_logprobs(x, tokens, top_k, temperature, True, dtype, plan)
         ctx.save_for_backward(x, tokens, out[5])
-        ctx.temperature, ctx.dtype, ctx.stream = temperature, dtype, stream
+        ctx.temperature, ctx.dtype = temperature, dtype
         ctx.mark_non_differentiable(*(t for t in out[3:] if t is not None))
         ctx.set_materialize_grads(False)
         return out
@@ -148,10 +179,10 @@ class _TokenLogprobsFunction(torch.autograd.Function):
     def backward(ctx, grad_logprob, grad_entropy, grad_lse, *_):
         x, tokens, stats = ctx.saved_tensors
         if grad_logprob is None and grad_entropy is None and grad_lse is None:
-            return (None,) * 7
+            return (None,) * 6
         given = [None if g is None else g.contiguous() for g in (grad_logprob, grad_entropy, grad_lse)]
-        return (token_logprobs_backward(x, tokens, stats, *given, temperature=ctx.temperature, dtype=ctx.dtype,
-                                        stream=ctx.stream),) + (None,) * 6
+        return (token_logprobs_backward(x, tokens, stats, *given, temperature=ctx.temperature,
+                                        dtype=ctx.dtype),) + (None,) * 5
 
 
 def token_logprobs(logits, tokens=None, top_k: int = 0, *, temperature: float = 1.0, with_stats: bool = False,
@@ -161,10 +192,13 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, *, temperature: float = 
     exponentials, and the ``top_k`` (at most 128) likeliest tokens with their
     log p. ``with_stats``: also what ``token_logprobs_backward`` needs (always there
     where the logits require a gradient). Runs on ``stream`` (default: torch's current stream) without
-    synchronising."""
+    synchronising, as if called with that stream as the current one."""
+    if stream is not None and (side := _side(stream, logits)) is not None:
+        return _under(side, (logits, tokens), token_logprobs, logits, tokens, top_k, temperature=temperature,
+                      with_stats=with_stats, dtype=dtype, plan=plan)
     if torch.is_grad_enabled() and logits.requires_grad:
-        return TokenLogprobs(*_TokenLogprobsFunction.apply(logits, tokens, top_k, temperature, dtype, plan, stream))
-    return TokenLogprobs(*_forward_logprobs(logits, tokens, top_k, temperature, with_stats, dtype, plan, stream))
+        return TokenLogprobs(*_TokenLogprobsFunction.apply(logits, tokens, top_k, temperature, dtype, plan))
+    return TokenLogprobs(*_forward_logprobs(logits, tokens, top_k, temperature, with_stats, dtype, plan))
 
 
 def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entropy=None, grad_lse=None, *,
@@ -173,6 +207,10 @@ def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entro
     grad_lse * lse) to the logits; ``stats`` from ``token_logprobs(...,
     with_stats=True)`` of the same logits and temperature. ``grad``: a tensor for the result, which may be
     ``logits`` itself (then overwritten)."""
+    if stream is not None and (side := _side(stream, logits)) is not None:
+        return _under(side, (logits, tokens, stats, grad_logprob, grad_entropy, grad_lse, grad), token_logprobs_backward,
+                      logits, tokens, stats, grad_logprob, grad_entropy, grad_lse, temperature=temperature, grad=grad,
+                      dtype=dtype, plan=plan)
     rows, cols, stride, code = _rows(logits, dtype)
     lead, dev = logits.shape[:-1], logits.device
     tok = _arg(tokens, "tokens", _I64, lead, dev)
@@ -182,8 +220,8 @@ def token_logprobs_backward(logits, tokens, stats, grad_logprob=None, grad_entro
             _arg(grad_entropy, "grad_entropy", _F32, lead, dev), _arg(grad_lse, "grad_lse", _F32, lead, dev))
     grad, grad_stride = _grad_out(logits, grad)
     _check(_LIB.argreduce_logprobs_backward(logits.data_ptr(), code, rows, cols, stride, temperature, *args,
-                                                   grad.data_ptr(), grad_stride, _plan(plan),
-                                                   _stream_ptr(stream, logits.get_device()) or None), "argreduce_logprobs_backward")
+                                            grad.data_ptr(), grad_stride, _plan(plan),
+                                            _stream_ptr(None, logits.get_device()) or None), "argreduce_logprobs_backward")
     return grad
 
 
@@ -198,23 +236,23 @@ def _slots(x, ids, teacher):
     return _arg(ids, "ids", _I64, ids.shape, x.device), _arg(teacher, "teacher", _F32, ids.shape, x.device), slots
 
 
-def _forward_distill(x, ids, teacher, temperature, tail, with_stats, dtype, plan, stream):
+def _forward_distill(x, ids, teacher, temperature, tail, with_stats, dtype, plan):
     rows, cols, stride, code = _rows(x, dtype)
     i, t, slots = _slots(x, ids, teacher)
     loss = _empty(x.shape[:-1], dtype=_F32, device=x.device)
     stats = _empty((*x.shape[:-1], 4), dtype=_F32, device=x.device) if with_stats else None
     _check(_LIB.argreduce_distill(x.data_ptr(), code, rows, cols, stride, temperature, i, t, slots, bool(tail),
-                                         loss.data_ptr(), stats.data_ptr() if with_stats else None, _plan(plan),
-                                  _stream_ptr(stream, x.get_device()) or None), "argreduce_distill")
+                                  loss.data_ptr(), stats.data_ptr() if with_stats else None, _plan(plan),
+                                  _stream_ptr(None, x.get_device()) or None), "argreduce_distill")
     return loss, stats
 
 
 class _DistillFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, ids, teacher, temperature, tail, dtype, plan, stream):
-        loss, stats = _forward_distill(x, ids, teacher, temperature, tail, True, dtype, plan, stream)
+    def forward(ctx, x, ids, teacher, temperature, tail, dtype, plan):
+        loss, stats = _forward_distill(x, ids, teacher, temperature, tail, True, dtype, plan)
         ctx.save_for_backward(x, ids, teacher, stats)
-        ctx.given = dict(temperature=temperature, tail=tail, dtype=dtype, stream=stream)
+        ctx.given = dict(temperature=temperature, tail=tail, dtype=dtype)
         ctx.mark_non_differentiable(stats)
         return loss, stats
 
@@ -222,7 +260,7 @@ class _DistillFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_loss, _):
         x, ids, teacher, stats = ctx.saved_tensors
-        return (distill_topk_backward(x, ids, teacher, stats, grad_loss.contiguous(), **ctx.given),) + (None,) * 7
+        return (distill_topk_backward(x, ids, teacher, stats, grad_loss.contiguous(), **ctx.given),) + (None,) * 6
 
 
 def distill_topk(logits, ids, teacher, *, temperature: float = 1.0, tail: bool = False, with_stats: bool = False,
@@ -233,10 +271,13 @@ def distill_topk(logits, ids, teacher, *, temperature: float = 1.0, tail: bool =
     softmax (at ``temperature``) over the slots is taught, or, with ``tail``,
     the teacher's log probabilities, taught together with what they leave of 1
     as one more outcome. Sums over rows, and a factor of temperature ** 2 where
-    one is wanted, are the caller's. ``with_stats`` as in ``token_logprobs``."""
+    one is wanted, are the caller's. ``with_stats`` and ``stream`` as in ``token_logprobs``."""
+    if stream is not None and (side := _side(stream, logits)) is not None:
+        return _under(side, (logits, ids, teacher), distill_topk, logits, ids, teacher, temperature=temperature, tail=tail,
+                      with_stats=with_stats, dtype=dtype, plan=plan)
     if torch.is_grad_enabled() and logits.requires_grad:
-        return DistillLoss(*_DistillFunction.apply(logits, ids, teacher, temperature, tail, dtype, plan, stream))
-    return DistillLoss(*_forward_distill(logits, ids, teacher, temperature, tail, with_stats, dtype, plan, stream))
+        return DistillLoss(*_DistillFunction.apply(logits, ids, teacher, temperature, tail, dtype, plan))
+    return DistillLoss(*_forward_distill(logits, ids, teacher, temperature, tail, with_stats, dtype, plan))
 
 
 def distill_topk_backward(logits, ids, teacher, stats, grad_loss, *, temperature: float = 1.0, tail: bool = False,
@@ -244,6 +285,9 @@ def distill_topk_backward(logits, ids, teacher, stats, grad_loss, *, temperature
     """The gradient of sum(grad_loss * loss) to the logits; ``stats`` from
     ``distill_topk(..., with_stats=True)`` with the same arguments. ``grad`` as in
     ``token_logprobs_backward``."""
+    if stream is not None and (side := _side(stream, logits)) is not None:
+        return _under(side, (logits, ids, teacher, stats, grad_loss, grad), distill_topk_backward, logits, ids, teacher,
+                      stats, grad_loss, temperature=temperature, tail=tail, grad=grad, dtype=dtype, plan=plan)
     rows, cols, stride, code = _rows(logits, dtype)
     lead = logits.shape[:-1]
     i, t, slots = _slots(logits, ids, teacher)
@@ -251,8 +295,9 @@ def distill_topk_backward(logits, ids, teacher, stats, grad_loss, *, temperature
     g = _arg(grad_loss, "grad_loss", _F32, lead, logits.device)
     grad, grad_stride = _grad_out(logits, grad)
     _check(_LIB.argreduce_distill_backward(logits.data_ptr(), code, rows, cols, stride, temperature, i, t,
-                                                  slots, bool(tail), st, g, grad.data_ptr(), grad_stride,
-                                                  _plan(plan), _stream_ptr(stream, logits.get_device()) or None), "argreduce_distill_backward")
+                                           slots, bool(tail), st, g, grad.data_ptr(), grad_stride,
+                                           _plan(plan), _stream_ptr(None, logits.get_device()) or None),
+           "argreduce_distill_backward")
     return grad
 
 
@@ -261,6 +306,9 @@ def distill_topk_step(logits, ids, teacher, grad_loss, *, temperature: float = 1
     """(loss, gradient) in one call, for a training step that knows each row's
     weight ``grad_loss`` beforehand: what ``distill_topk`` and
     ``distill_topk_backward`` would give."""
+    if stream is not None and (side := _side(stream, logits)) is not None:
+        return _under(side, (logits, ids, teacher, grad_loss, grad), distill_topk_step, logits, ids, teacher, grad_loss,
+                      temperature=temperature, tail=tail, grad=grad, dtype=dtype, plan=plan)
     rows, cols, stride, code = _rows(logits, dtype)
     lead = logits.shape[:-1]
     i, t, slots = _slots(logits, ids, teacher)
@@ -269,7 +317,7 @@ def distill_topk_step(logits, ids, teacher, grad_loss, *, temperature: float = 1
     loss = _empty(lead, dtype=_F32, device=logits.device)
     stats = _empty((*lead, 4), dtype=_F32, device=logits.device)
     _check(_LIB.argreduce_distill_step(logits.data_ptr(), code, rows, cols, stride, temperature, i, t, slots,
-                                              bool(tail), g, loss.data_ptr(), stats.data_ptr(), grad.data_ptr(),
-                                              grad_stride, _plan(plan), _stream_ptr(stream, logits.get_device()) or None),
+                                       bool(tail), g, loss.data_ptr(), stats.data_ptr(), grad.data_ptr(),
+                                       grad_stride, _plan(plan), _stream_ptr(None, logits.get_device()) or None),
            "argreduce_distill_step")
     return loss, grad

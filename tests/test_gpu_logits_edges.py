@@ -47,3 +47,86 @@ def test_plans_with_more_row_slots_than_rows(cluster, block, grid):
         check_distill(x, dtype, ids, val, 1.0, True, plan=plan, grad_plan=grad_plan(3, 128, grid),
                       step_plan=step_plan(cluster, min(block, 256), grid))
         check_logprobs(x, dtype, None, 7, plan=stream_plan(2, 512, grid))
+
+
+def busy():
+    """Some milliseconds of work on the current stream."""
+    a = torch.full((4096, 4096), 1.0 / 4096, device="cuda")
+    for _ in range(20):
+        a = a @ a
+    return a.sum() * 0.0
+
+
+def stream_kinds():
+    side = torch.cuda.Stream()
+    return [side, side.cuda_stream, torch.cuda.ExternalStream(side.cuda_stream)]
+
+
+def test_gradients_of_calls_on_another_stream():
+    """Gradients that are made late reach a backward pass whose forward pass ran on another stream, and its own are used
+    at once on this one; the forward pass's tensors are dropped as soon as they can be."""
+    g = torch.Generator("cuda").manual_seed(31)
+    x = torch.randn(300, 20011, device="cuda", generator=g)
+    tok = torch.randint(0, 20011, (300,), device="cuda", generator=g)
+    ids = torch.stack([torch.randperm(20011, device="cuda", generator=g)[:8] for _ in range(300)])
+    val = torch.log_softmax(torch.randn(300, 9, device="cuda", generator=g), -1)[:, :8].contiguous()
+    weights = torch.rand(300, device="cuda", generator=g)
+
+    def as_stream(s):
+        return s if not isinstance(s, int) else torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+
+    def pass_(how, stream):
+        leaf = x.clone().requires_grad_()
+        scaled = leaf * 1.5  # the operator's own input is dropped after the backward pass
+        if stream is not None:
+            as_stream(stream).wait_stream(torch.cuda.current_stream())
+        if how == "logprobs":
+            r = A.token_logprobs(scaled, tok, 5, stream=stream)
+            parts = (r.logprob, r.entropy, r.lse)
+        else:
+            parts = (A.distill_topk(scaled, ids, val, tail=True, stream=stream).loss,)
+        del scaled
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(as_stream(stream))
+        late = weights + busy()
+        sum((p * late * (i + 1)).sum() for i, p in enumerate(parts)).backward()
+        used = leaf.grad * 2.0
+        junk = [torch.full((300, 20011), 7.0, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all((j == 7.0).all() for j in junk)
+        return used
+
+    for how in ("logprobs", "distill"):
+        want = pass_(how, None)
+        assert want.abs().sum() > 0
+        for stream in stream_kinds() * 2:
+            assert torch.equal(pass_(how, stream), want)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):  # from a side stream to the default one, by its handle
+            assert torch.equal(pass_(how, 0), want)
+
+
+def test_memory_of_calls_on_another_stream():
+    """What a call makes for itself, and what it returns and is dropped at once, is not handed out while the other stream
+    still writes it."""
+    g = torch.Generator("cuda").manual_seed(32)
+    x = torch.randn(2000, 3001, device="cuda", generator=g)
+    ids = torch.stack([torch.randperm(3001, device="cuda", generator=g)[:4] for _ in range(2000)])
+    val = torch.log_softmax(torch.randn(2000, 5, device="cuda", generator=g), -1)[:, :4].contiguous()
+    w = torch.rand(2000, device="cuda", generator=g)
+    want = A.distill_topk_step(x, ids, val, w, tail=True)
+    stats = A.token_logprobs(x, ids[:, 0].contiguous(), with_stats=True).stats
+    torch.cuda.synchronize()
+    for stream in stream_kinds():
+        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        for _ in range(3):
+            with torch.cuda.stream(s):
+                busy()
+            got = A.distill_topk_step(x, ids, val, w, tail=True, stream=stream)
+            A.token_logprobs(x, ids[:, 0].contiguous(), 3, with_stats=True, stream=stream)
+            A.token_logprobs_backward(x, ids[:, 0].contiguous(), stats, w.clone(), stream=stream)
+            junk = [torch.full((2000, n), 7.0, device="cuda") for n in (1, 2, 3, 4, 3001) for _ in range(4)]
+            s.synchronize()
+            torch.cuda.synchronize()
+            assert all((j == 7.0).all() for j in junk)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
