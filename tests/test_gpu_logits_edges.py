@@ -115,16 +115,20 @@ def test_memory_of_calls_on_another_stream():
     val = torch.log_softmax(torch.randn(2000, 5, device="cuda", generator=g), -1)[:, :4].contiguous()
     w = torch.rand(2000, device="cuda", generator=g)
     want = A.distill_topk_step(x, ids, val, w, tail=True)
-    stats = A.token_logprobs(x, ids[:, 0].contiguous(), with_stats=True).stats
+    tok = ids[:, 0].contiguous()
+    stats = A.token_logprobs(x, tok, with_stats=True).stats
     torch.cuda.synchronize()
     for stream in stream_kinds():
         s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
         for _ in range(3):
             with torch.cuda.stream(s):
                 busy()
+            late = w.clone()  # an input that is dropped at once, too
+            s.wait_stream(torch.cuda.current_stream())
             got = A.distill_topk_step(x, ids, val, w, tail=True, stream=stream)
-            A.token_logprobs(x, ids[:, 0].contiguous(), 3, with_stats=True, stream=stream)
-            A.token_logprobs_backward(x, ids[:, 0].contiguous(), stats, w.clone(), stream=stream)
+            A.token_logprobs(x, tok, 3, with_stats=True, stream=stream)
+            A.token_logprobs_backward(x, tok, stats, late, stream=stream)
+            del late
             junk = [torch.full((2000, n), 7.0, device="cuda") for n in (1, 2, 3, 4, 3001) for _ in range(4)]
             s.synchronize()
             torch.cuda.synchronize()
