@@ -11,8 +11,8 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 
 import row_wise_arg_gb300 as A  # noqa: E402
-from test_gpu_logits import (DT, check_distill, check_logprobs, forward_plan, grad_plan, slots_for, step_plan,  # noqa: E402
-                             stream_plan)
+from test_gpu_logits import (DT, check_distill, check_logprobs, close, forward_plan, grad_plan, slots_for,  # noqa: E402
+                             step_plan, stream_plan)
 
 
 @pytest.fixture(scope="module", autouse=True)
