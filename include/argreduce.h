@@ -467,13 +467,14 @@ argr_status argreduce_logprobs_backward(const void* x, argr_dtype dtype, int64_t
  *              is one more outcome: loss = sum_i q_i (ln q_i - ln p_{id_i}) +
  *              rest (ln rest - ln p_rest), p_rest being the student's probability
  *              of every index no slot names, summed over those indices (not
- *              taken as a difference from 1). The last term is left out where
- *              p_rest = 0.
+ *              taken as a difference from 1) and kept as a logarithm. The last term
+ *              is left out where p_rest = 0, that is below e^-745, as in binary64
+ *              (a tail masked by the type's lowest value).
  * A slot with q = 0 adds nothing; one with q > 0 and p = 0 makes the loss
  * +inf. A row without a filled slot (tail == 0: or with teacher -inf in all of
  * them) has loss 0 and gradient 0. stats receives
  * 4 floats per row, {m, ln s, ln s_rest, 0}, s_rest = the part of s over the
- * indices that no slot names (ln s where tail == 0): what
+ * indices that no slot names (ln s where tail == 0, -inf where p_rest = 0): what
  * argreduce_distill_backward() needs. 0 <= slots <= ARGR_LOGITS_MAX_SLOTS.
  */
 argr_status argreduce_distill(const void* x, argr_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,

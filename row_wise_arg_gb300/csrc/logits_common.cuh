@@ -428,6 +428,19 @@ __device__ __forceinline__ Teacher teacher_of(const LogitsProblem& pr, const Slo
     return teacher_of(pr, sl, [](const Teacher&) {});
 }
 
+// The tail's share of a row, p_rest, may be far below what binary32 holds, so the
+// tail's sum stays relative to the tail's own largest element and p_rest a logarithm. Below
+// kLeastTail it is 0 in binary64 as well: tails masked by finite values (an f16 row's
+// lowest, say) count as masked.
+constexpr float kLeastTail = -745.0f;
+
+// ln s_rest of a tail, against the row's largest element m; -inf where there is none.
+__device__ __forceinline__ float tail_log(const LogitsProblem& pr, const SoftSum& rest, float m, float ln_s) {
+    if (rest.empty()) return neg_inf();
+    const float ln_rest = logf(rest.s) + (rest.m - m) / pr.temperature;
+    return ln_rest - ln_s < kLeastTail ? neg_inf() : ln_rest;
+}
+
 // What a slot adds to the loss of a row with largest element m.
 __device__ __forceinline__ float slot_loss(const LogitsProblem& pr, const Teacher& q, const Slots& sl, int i, float m,
                                            float ln_s) {
@@ -451,24 +464,35 @@ __device__ __forceinline__ float row_loss(const LogitsProblem& pr, const Teacher
     return whole_loss(q, block_sum(loss, red), ln_s, ln_rest);
 }
 
-// The weights of a row's gradient: named elements g (total p - q), others dense p;
+// The weights of a row's gradient. Named elements: g (total p - q). Others: without a
+// tail g total p; with one g (total p_rest - rest) p / p_rest, the last factor (at most 1) one
+// exponential against the tail's own sum, ln_rest against the element rest_m (the row's largest
+// one will do), so that neither factor leaves binary32's range where p and p_rest do.
 // `none`: every element is `dense`.
 struct GradWeights {
-    float g, total, dense, m, ls2;
+    float g, total, m, ls2;
+    float dense, dense_m, dense_ls2;
     bool none;
 
     GradWeights() = default;
     __device__ __forceinline__ GradWeights(const LogitsProblem& pr, const Teacher& q, float grad_loss, float row_m,
-                                           float ln_s, float ln_rest) {
+                                           float ln_s, float rest_m, float ln_rest) {
         const float rest = ln_rest > neg_inf() ? q.rest : 0.0f;
         g = grad_loss / pr.temperature;
         if (q.bad || (ln_s != ln_s && q.any)) g = quiet_nan();
         none = ln_s == neg_inf() || !q.any;  // nothing is taught, or nothing can be
         total = q.total + rest;
-        dense = g * (rest > 0.0f ? total - rest * expf(ln_s - ln_rest) : total);
-        if (none) dense = q.bad ? g : 0.0f;
+        dense = g * total;
         m = none ? 0.0f : row_m;
         ls2 = none ? 0.0f : ln_s * kLog2E;
+        dense_m = m;
+        dense_ls2 = ls2;
+        if (none) dense = q.bad ? g : 0.0f;
+        else if (rest > 0.0f) {
+            dense = g * (total * expf((rest_m - row_m) / pr.temperature + ln_rest - ln_s) - rest);
+            dense_m = rest_m;
+            dense_ls2 = ln_rest * kLog2E;
+        }
     }
     __device__ __forceinline__ float named(float x, float lnq, float scale2) const {
         return g * (total * ex2((x - m) * scale2 - ls2) - expf(lnq));
@@ -489,15 +513,12 @@ __device__ __forceinline__ void finish_distill(const LogitsProblem& pr, int64_t 
         for (int i = t; i < pr.slots; i += blockDim.x)
             if (sl.id[i] >= 0) d.add(sl.x[i], scale2);
         d = block_softsum(d, scale2, red);
-        if (t < 32) {
-            all.join(d, scale2);
-            c.rebase(all.m, scale2);
-        }
+        if (t < 32) all.join(d, scale2);
     }
     if (t == 0) {
         m_ln_s[0] = all.empty() ? neg_inf() : all.m;
         m_ln_s[1] = all.empty() ? neg_inf() : logf(all.s);
-        m_ln_s[2] = c.empty() ? neg_inf() : logf(c.s);
+        m_ln_s[2] = TAIL ? tail_log(pr, c, all.m, m_ln_s[1]) : m_ln_s[1];
     }
     __syncthreads();
     const float m = m_ln_s[0], ln_s = m_ln_s[1], ln_rest = m_ln_s[2];

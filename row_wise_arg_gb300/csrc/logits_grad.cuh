@@ -9,7 +9,8 @@
 // and the single entries are read before the dense pass writes any.
 //
 //   log probabilities: dx_j = ((g_lse - g_lp) p_j - g_H p_j (log p_j + H) + [j = token] g_lp) / T
-//   distillation:      dx_j = g (w p_j - q_j) / T at a slot's index, g w' p_j / T elsewhere
+//   distillation:      dx_j = g (w p_j - q_j) / T at a slot's index, g w p_j / T elsewhere, with a tail
+//                      g (w p_rest - rest) (p_j / p_rest) / T there
 //
 // Bound by the memory: [2048, 202048] bf16 239 us, 6.9 TB/s read and written; [1024, 262144]
 // bf16, 64 slots, 157 us, 6.9 TB/s; [1024, 100000] f32 121 us, 6.8 TB/s (a copy: 6.8).
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const Lo
         // its barriers order the reads above before the stores below
         const Teacher q = teacher_of(pr, sl, [&](const Teacher& sums) {
             const float4 st = pr.stats[r];
-            if (t == 0) weights = GradWeights(pr, sums, pr.grad_logprob[r], st.x, st.y, st.z);
+            if (t == 0) weights = GradWeights(pr, sums, pr.grad_logprob[r], st.x, st.y, st.x, st.z);
         });
         const GradWeights w = weights;
         if (w.none) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const Lo
             for (unsigned i = t; i < static_cast<unsigned>(hi - lo); i += blockDim.x) out[lo + i] = fill;
         } else {
             const auto nothing = [](int, int) {};
-            grad_chunk<Tag>(row, out, pr.cols, blockIdx.x, gridDim.x, w.m, w.ls2, scale2,
+            grad_chunk<Tag>(row, out, pr.cols, blockIdx.x, gridDim.x, w.dense_m, w.dense_ls2, scale2,
                             [&](float y) { return w.dense * ex2(y); }, nothing, nothing);
             __syncthreads();
             for (int i = t; i < pr.slots; i += blockDim.x) {

@@ -11,7 +11,7 @@
 //   p_j = exp2((x_j - m) scale2 - log2 s), (m, s) joined over the cluster;
 //   dx_j = w p_j, and at the elements that slots name (Q + tail) p_j - q_j. With a
 //   tail bucket the named elements are left out of the sums (-inf in their place in shared
-//   memory) and summed by themselves.
+//   memory) and summed by themselves, and w p_j is w' times the element's share of the tail.
 //
 // A CTA's time is a chain: copies, sums, exchange, gradient; what is not memory
 // in it (about half) bounds the kernel. Hence: every warp sends its own sums to every
@@ -190,24 +190,21 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
         }
         c = warp_softsum(c, scale2);
         SoftSum all = c;
-        if constexpr (TAIL) {
-            all.join(warp_softsum(d, scale2), scale2);
-            c.rebase(all.m, scale2);
-        }
+        if constexpr (TAIL) all.join(warp_softsum(d, scale2), scale2);
         const float m = all.empty() ? neg_inf() : all.m;
         const float ln_s = all.empty() ? neg_inf() : logf(all.s);
-        const float ln_rest = TAIL ? (c.empty() ? neg_inf() : logf(c.s)) : ln_s;
+        const float ln_rest = TAIL ? tail_log(pr, c, all.m, ln_s) : ln_s;
         const Teacher q = *sl.sums;
-        const GradWeights w(pr, q, grad_loss, m, ln_s, ln_rest);
-        const auto f = [&](float x) { return narrow_elem<Tag>(w.dense * ex2((x - w.m) * scale2 - w.ls2)); };
+        const GradWeights w(pr, q, grad_loss, m, ln_s, TAIL ? c.m : m, TAIL && ln_rest != neg_inf() ? logf(c.s) : ln_rest);
+        const auto f = [&](float x) { return narrow_elem<Tag>(w.dense * ex2((x - w.dense_m) * scale2 - w.dense_ls2)); };
         // every element that slots name has been read, by all CTAs, before the first is written
         if (w.none) {
             const R fill = narrow_elem<Tag>(w.dense);
             for (int j = lo + t; j < hi; j += nt) out[j] = fill;
         } else {
             if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
-                const f32x2 minus = pack2(-w.m, -w.m), scale = pack2(scale2, scale2), shift = pack2(-w.ls2, -w.ls2);
-                const f32x2 dense = pack2(w.dense, w.dense);
+                const f32x2 minus = pack2(-w.dense_m, -w.dense_m), scale = pack2(scale2, scale2);
+                const f32x2 shift = pack2(-w.dense_ls2, -w.dense_ls2), dense = pack2(w.dense, w.dense);
                 uint4* to = reinterpret_cast<uint4*>(out + body);
                 const auto grads = [&](Group<Tag>& v) {
 #pragma unroll

@@ -646,11 +646,10 @@ __device__ __forceinline__ void finish_rows(const LogitsProblem& pr, float scale
                 for (int i = lane; i < pr.slots; i += 32)
                     if (sl.id[i] >= 0) d.add(sl.x[i], scale2);
                 all.join(warp_softsum(d, scale2), scale2);
-                c.rebase(all.m, scale2);
             }
             const float m = all.empty() ? neg_inf() : all.m;
             const float ln_s = all.empty() ? neg_inf() : logf(all.s);
-            const float ln_rest = c.empty() ? neg_inf() : logf(c.s);
+            const float ln_rest = MODE == kStreamLossTail ? tail_log(pr, c, all.m, ln_s) : ln_s;
             float loss = 0.0f;
             for (int i = lane; i < pr.slots; i += 32) loss += slot_loss(pr, q, sl, i, m, ln_s);
 #pragma unroll

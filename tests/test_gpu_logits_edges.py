@@ -45,7 +45,7 @@ def test_plans_with_more_row_slots_than_rows(cluster, block, grid):
         plan = forward_plan(cluster, block, grid, grid)
         check_logprobs(x, dtype, rng.integers(-1, 30011, 5), 7, plan=plan)
         check_distill(x, dtype, ids, val, 1.0, True, plan=plan, grad_plan=grad_plan(3, 128, grid),
-                      step_plan=step_plan(cluster, min(block, 256), grid))
+                      step_plan=step_plan(max(cluster, 2), min(block, 256), grid))
         check_logprobs(x, dtype, None, 7, plan=stream_plan(2, 512, grid))
 
 
@@ -134,3 +134,87 @@ def test_memory_of_calls_on_another_stream():
             torch.cuda.synchronize()
             assert all((j == 7.0).all() for j in junk)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---------------------------------------------------------------------------
+# Ranges of numbers.
+# ---------------------------------------------------------------------------
+def tail_in_logs(x, ids, val, temp, g):
+    """(loss, gradient, bounds of both) with the tail, in 64 bits, the tail's mass as a logarithm. Every row's slots
+    are filled, its tail is neither empty nor masked.
+
+    Bounds: a sum is off by a share of sum_error (logits_ref), an exponential's argument y by 8 |y| u, what is left of 1
+    by sum_error itself; ln p_rest multiplies that, and the weight of a tail element is its share of the tail."""
+    rows, cols = x.shape
+    loss, grad = np.zeros(rows), np.zeros((rows, cols))
+    lbound, terms = np.zeros(rows), np.zeros((rows, cols))
+    for r in range(rows):
+        z = x[r] / temp
+        named = np.zeros(cols, bool)
+        named[ids[r]] = True
+        lse = np.logaddexp.reduce(z)
+        lse_rest = np.logaddexp.reduce(z[~named])
+        q = np.exp(val[r].astype(np.float64))
+        rest = 1.0 - q.sum()
+        lp = z - lse
+        used = q > 0
+        loss[r] = (q[used] * (val[r][used] - lp[ids[r]][used])).sum() + rest * (np.log(rest) - (lse_rest - lse))
+        share = np.where(named, 0.0, np.exp(np.minimum(z - lse_rest, 0.0)))
+        d = (q.sum() + rest) * np.exp(lp) - rest * share
+        np.subtract.at(d, ids[r], q)
+        grad[r] = d * g[r] / temp
+        far = abs(lse_rest - lse)
+        lbound[r] = ref.logprob_bound(loss[r], cols) + ref.sum_error(cols) * (
+            2 * np.abs(lp[ids[r]][used]).max() + np.log(len(q)) + 3 + far + abs(np.log(rest)) + 8)
+        t = np.exp(lp) * (1 + np.abs(lp)) + share * (1 + np.abs(np.where(named, 0.0, lp)) + far)
+        np.add.at(t, ids[r], q * (2 + np.abs(np.where(used, val[r], 0.0))))
+        terms[r] = t * abs(g[r]) / temp
+    return loss, grad, lbound, terms
+
+
+TAIL_PLANS = [(forward_plan(1, 128, 2, 2), step_plan(1, 128, 2)), (forward_plan(4, 64, 5, 5), step_plan(4, 64, 3)),
+              (stream_plan(1, 128, 2), step_plan(2, 32, 1)), (stream_plan(2, 256, 3), None), (None, None)]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("gap,temp", [(20, 1.0), (60, 1.0), (80, 1.0), (84, 1.0), (86, 1.0), (87, 1.0), (88, 1.0),
+                                      (90, 1.0), (100, 1.0), (150, 1.0), (700, 1.0), (26, 0.3), (27, 0.3), (200, 0.3),
+                                      (300, 3.0)])
+def test_a_tail_far_below_the_row(gap, temp, dtype):
+    """A student that gives the tail next to nothing is told so: its logarithm is finite however small it is."""
+    rng = np.random.default_rng(gap)
+    rows, cols, slots = 5, 3001, 64
+    x = np.round(rng.normal(-gap, 0.5, (rows, cols)) * 8) / 8
+    ids = np.stack([rng.permutation(cols)[:slots] for _ in range(rows)]).astype(np.int64)
+    for r in range(rows):
+        x[r, ids[r]] = np.round(rng.normal(0, 0.5, slots) * 8) / 8 if r else 0.0
+    x[0, np.setdiff1d(np.arange(cols), ids[0])[1:]] -= gap  # a lone element leads the tail
+    t = torch.from_numpy(x).to(DT[dtype])
+    x64, xd = t.double().numpy(), t.cuda()
+    val = np.log(rng.dirichlet(np.full(slots, 2.0), rows) * rng.uniform(0.5, 0.95, (rows, 1))).astype(np.float32)
+    g = rng.normal(size=rows).astype(np.float32)
+    loss, grad, lbound, terms = tail_in_logs(x64, ids, val, temp, g)
+    gbound = ref.grad_bound(grad, terms, cols, dtype)
+    i, v, w = (torch.from_numpy(a).cuda() for a in (ids, val, g))
+    kw = dict(temperature=temp, tail=True)
+    for plan, splan in TAIL_PLANS:
+        r = A.distill_topk(xd, i, v, plan=plan, with_stats=True, **kw)
+        close(r.loss, loss, lbound, "loss")
+        close(A.distill_topk_backward(xd, i, v, r.stats, w, **kw), grad, gbound, "grad")
+        both = A.distill_topk_step(xd, i, v, w, plan=splan, **kw)
+        close(both[0], loss, lbound, "step's loss")
+        close(both[1], grad, gbound, "step's grad")
+
+
+def test_a_tail_that_is_masked_is_left_out():
+    """By -inf, or so low that its probability is 0 in binary64 as well: finite, and as without the term."""
+    rng = np.random.default_rng(4)
+    ids = np.stack([rng.permutation(3001)[:64] for _ in range(3)]).astype(np.int64)
+    val = np.log(rng.dirichlet(np.full(64, 2.0), 3) * 0.9).astype(np.float32)
+    for dtype in DT:
+        for low in (-np.inf, -1e4, -6e4):
+            x = np.full((3, 3001), low)
+            for r in range(3):
+                x[r, ids[r]] = rng.normal(0, 1, 64)
+            for plan, splan in TAIL_PLANS:
+                check_distill(x.astype(np.float32), dtype, ids, val, 1.0, True, plan=plan, step_plan=splan)
