@@ -260,7 +260,7 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
     // largest of 32 values, each the largest of a 32nd of the threads (1.5 k elements or fewer reach it,
     // as a rule); one barrier, and every warp ranks them itself. More: the k-th largest of the threads'
     // values or near it, bit by bit, a barrier each.
-    if (t < 3) sh.count[t] = t == 1 ? have : 0;
+    if (t < 3) sh.count[t] = 0;
     unsigned at = 0;
     if (k <= kFewTop) {
         unsigned* tops = reinterpret_cast<unsigned*>(sh.cand);  // (all have read it, a barrier ago)
@@ -316,7 +316,7 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
         }
         if (again) {
             __syncthreads();
-            if (t < 3) sh.count[t] = t == 1 ? have : 0;
+            if (t < 3) sh.count[t] = 0;
             __syncthreads();
         }
         int equal = 0;
@@ -370,7 +370,10 @@ __device__ __forceinline__ int take_segment(const typename Tag::raw* row, const 
             too_many();
             continue;
         }
-        for (int i = t; i < have; i += nt) sh.cand[i] = sh.best[i];
+        // the best so far that reach `at`: k elements do, so the others are out, and must not stand in for
+        // elements that equal it
+        for (int i = t; i < have; i += nt)
+            if (static_cast<unsigned>(sh.best[i] >> 32) >= at) sh.cand[atomicAdd(&sh.count[1], 1)] = sh.best[i];
         // the picked slots' elements that reach `floor`, 16 bytes per lane, 8 slots per warp at a time
         const unsigned floor = at + (mode == 1);
         for (int p0 = 8 * warp; p0 < picked; p0 += 8 * warps) {

@@ -218,3 +218,30 @@ def test_a_tail_that_is_masked_is_left_out():
                 x[r, ids[r]] = rng.normal(0, 1, 64)
             for plan, splan in TAIL_PLANS:
                 check_distill(x.astype(np.float32), dtype, ids, val, 1.0, True, plan=plan, step_plan=splan)
+
+
+# ---------------------------------------------------------------------------
+# Ties across the segments of a CTA's part (8192 groups of 64 bytes).
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", list(DT))
+def test_ties_in_a_later_segment(dtype):
+    """Many equal values that come after a segment of smaller ones, with fewer larger ones than alternatives."""
+    seg = 8192 * (16 if dtype == "f32" else 32)
+    cols = 2 * seg + 777
+    for first, later in ((-1.0, 0.0), (-np.inf, -5.0), (-5.0, -5.0), (np.nan, -5.0)):
+        x = np.full((2, cols), later, np.float32)
+        x[:, :seg + 100] = first
+        x[1, seg + 300:] = first  # a few of them only
+        x[:, seg + 5000:seg + 5003] = 2.0
+        x[:, 70] = 1.0
+        x[:, 2 * seg + 500] = 1.0
+        for k in (1, 5, 20, 128):
+            for plan in (forward_plan(1, 512, 2, 2), forward_plan(1, 64, 2, 2), None):
+                check_logprobs(x, dtype, None, k, plan=plan)
+    # the planner's own choice of a CTA per row
+    rows = 90
+    assert A.argreduce_logits_plan("logprobs", rows, cols, dtype, 20, A.make_caps(152)).cluster == 1
+    t = torch.full((rows, cols), -1.0, dtype=DT[dtype], device="cuda")
+    t[:, seg + 100:] = 0.0
+    got = A.token_logprobs(t, None, 20).top_ids
+    assert torch.equal(got, torch.arange(seg + 100, seg + 120, device="cuda").expand(rows, 20))
