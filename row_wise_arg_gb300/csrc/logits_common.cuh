@@ -338,7 +338,8 @@ struct Part {
 // The teacher's side of a row, in shared memory.
 // ---------------------------------------------------------------------------
 struct Teacher {
-    float shift;  // ln q = v - shift
+    float top;    // without the tail: ln q = (v - top) / T - ln_sum, so that what the values have in common
+    float ln_sum; // costs no digits, and the largest differences overflow to q = 0 alone
     float total;  // sum of q over the filled slots
     float rest;   // what the tail holds
     bool any;     // a slot holds something
@@ -347,7 +348,7 @@ struct Teacher {
 
 struct Slots {
     int* id;   // the index named, kNoId or kBadId
-    float* v;  // teacher / T without the tail, teacher with it
+    float* v;  // teacher
     float* x;  // the row's element, where it was asked for
     Teacher* sums;
 
@@ -371,12 +372,11 @@ __device__ __forceinline__ void load_slots(const LogitsProblem& pr, int64_t r, c
                                            int hi, const Slots& sl) {
     const int64_t* ids = pr.ids + r * pr.slots;
     const float* val = pr.teacher + r * pr.slots;
-    const float inv_t = pr.tail ? 1.0f : 1.0f / pr.temperature;
     for (int i = threadIdx.x; i < pr.slots; i += blockDim.x) {
         const int64_t id = ids[i];
         const int j = id < 0 ? kNoId : id >= pr.cols ? kBadId : static_cast<int>(id);
         sl.id[i] = j;
-        sl.v[i] = val[i] * inv_t;
+        sl.v[i] = val[i];
         if (j >= lo && j < hi) sl.x[i] = widen_elem<Tag>(row[j]);
     }
 }
@@ -395,16 +395,17 @@ __device__ __forceinline__ Teacher warp_teacher(const LogitsProblem& pr, const S
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float shift = pr.tail ? 0.0f : top;
+    const float inv_t = 1.0f / pr.temperature;
     float sum = 0.0f;
     for (int i = lane; i < pr.slots; i += 32)
-        if (sl.id[i] != kNoId) sum += expf(sl.v[i] - shift);
+        if (sl.id[i] != kNoId) sum += expf(pr.tail ? sl.v[i] : (sl.v[i] - top) * inv_t);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     Teacher q;
     q.any = __any_sync(0xffffffffu, any);
     q.bad = __any_sync(0xffffffffu, bad);
-    q.shift = pr.tail || !q.any ? 0.0f : shift + logf(sum);
+    q.top = top;
+    q.ln_sum = q.any ? logf(sum) : 0.0f;  // (nothing given: every ln q is -inf)
     q.total = pr.tail ? sum : q.any ? 1.0f : 0.0f;
     q.rest = pr.tail && q.any ? fmaxf(0.0f, 1.0f - sum) : 0.0f;
     return q;
@@ -441,11 +442,16 @@ __device__ __forceinline__ float tail_log(const LogitsProblem& pr, const SoftSum
     return ln_rest - ln_s < kLeastTail ? neg_inf() : ln_rest;
 }
 
+// ln q of a slot with this value.
+__device__ __forceinline__ float teacher_log(const LogitsProblem& pr, const Teacher& q, float v) {
+    return pr.tail ? v : (v - q.top) / pr.temperature - q.ln_sum;
+}
+
 // What a slot adds to the loss of a row with largest element m.
 __device__ __forceinline__ float slot_loss(const LogitsProblem& pr, const Teacher& q, const Slots& sl, int i, float m,
                                            float ln_s) {
     if (sl.id[i] < 0) return 0.0f;
-    const float lnq = sl.v[i] - q.shift;
+    const float lnq = teacher_log(pr, q, sl.v[i]);
     const float p = expf(lnq);
     const float lp = ln_s == neg_inf() ? neg_inf() : (sl.x[i] - m) / pr.temperature - ln_s;
     return p == 0.0f ? 0.0f : p * (lnq - lp);

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const Lo
             __syncthreads();
             for (int i = t; i < pr.slots; i += blockDim.x) {
                 const int j = sl.id[i];
-                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(w.named(sl.x[i], sl.v[i] - q.shift, scale2));
+                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(w.named(sl.x[i], teacher_log(pr, q, sl.v[i]), scale2));
             }
         }
         __syncthreads();

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
             __syncthreads();
             for (int i = t; i < pr.slots; i += nt) {
                 const int j = sl.id[i];
-                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(w.named(sl.x[i], sl.v[i] - q.shift, scale2));
+                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(w.named(sl.x[i], teacher_log(pr, q, sl.v[i]), scale2));
             }
         }
         if (rank == 0 && warp == 0) {

@@ -524,7 +524,6 @@ __device__ __forceinline__ void prepare_loss(const LogitsProblem& pr, const Wide
     const int lane = threadIdx.x & 31;
     const int64_t* ids = pr.ids + r * pr.slots;
     const float* val = pr.teacher + r * pr.slots;
-    const float inv_t = pr.tail ? 1.0f : 1.0f / pr.temperature;
     constexpr int U = 4;  // slots per lane at a time
     for (int i0 = lane; i0 < pr.slots; i0 += 32 * U) {
         int id[U];
@@ -534,7 +533,7 @@ __device__ __forceinline__ void prepare_loss(const LogitsProblem& pr, const Wide
             const int i = i0 + 32 * u;
             const int64_t j = i < pr.slots ? ids[i] : -1;
             id[u] = j < 0 ? kNoId : j >= pr.cols ? kBadId : static_cast<int>(j);
-            v[u] = i < pr.slots ? val[i] * inv_t : 0.0f;
+            v[u] = i < pr.slots ? val[i] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = id[u] >= 0 ? widen_elem<Tag>(ld_scalar(row.p + id[u])) : 0.0f;

@@ -245,3 +245,23 @@ def test_ties_in_a_later_segment(dtype):
     t[:, seg + 100:] = 0.0
     got = A.token_logprobs(t, None, 20).top_ids
     assert torch.equal(got, torch.arange(seg + 100, seg + 120, device="cuda").expand(rows, 20))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_teacher_logits_of_any_size(dtype):
+    """Their softmax does not depend on what they have in common; differences come before the temperature."""
+    rng = np.random.default_rng(12)
+    rows, cols, slots = 6, 2003, 33
+    x = rng.normal(0, 2, (rows, cols)).astype(np.float32)
+    ids, val = slots_for(rng, rows, cols, slots, False)
+    top = 3.4028234663852886e38
+    for shift, temp in ((0.0, 1.0), (1e3, 1.0), (-1e4, 1.0), (1e4, 0.5), (1e6, 0.7)):
+        check_distill(x, dtype, ids, (val + np.float32(shift)).astype(np.float32), temp, False)
+    low = np.full_like(val, -top)
+    high = np.full_like(val, top)
+    one = low.copy()
+    one[:, 4] = 1.0
+    for v in (low, high, one):
+        for temp in (0.5, 1.0, 2.0):
+            check_distill(x, dtype, ids, v, temp, False)
+            check_distill(x, dtype, ids, v, temp, False, plan=stream_plan(1, 128, 2))
