@@ -29,8 +29,7 @@ __all__ = [
     "argmax", "argmin", "argreduce_with_plan", "argreduce_plan", "argreduce_plan_check", "argreduce_scratch_bytes",
     "argreduce_scratch_init", "argreduce_read_error", "argreduce_device_caps", "argreduce_status_string",
     "argreduce_version", "argreduce_plan_scratch_bytes", "ArgreduceError", "Scratch", "make_caps",
-    "token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward", "distill_topk_step",
-    "TokenLogprobs", "DistillLoss", "argreduce_logits_plan",
+    "argreduce_logits_plan",
 ]
 
 
@@ -326,9 +325,13 @@ _LOGITS = ("token_logprobs", "token_logprobs_backward", "distill_topk", "distill
 
 
 def __getattr__(name):
-    """The vocabulary-row operators, loaded with torch when first asked for."""
+    """The vocabulary-row operators, loaded with torch and the library when first asked for
+    (so they are not in __all__: a star import needs neither)."""
     if name in _LOGITS:
-        from . import logits
+        try:
+            from . import logits
+        except (ImportError, RuntimeError, OSError) as e:
+            raise AttributeError(f"module {__name__!r} cannot load {name!r}: {e}") from e
         globals().update((n, getattr(logits, n)) for n in _LOGITS)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

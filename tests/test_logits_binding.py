@@ -1,0 +1,40 @@
+"""The vocabulary-row operators' binding without a GPU: import, refusals before any device work."""
+import ctypes
+import os
+import subprocess
+import sys
+
+import pytest
+
+import row_wise_arg_gb300 as A
+from row_wise_arg_gb300 import _lib
+from row_wise_arg_gb300.build import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+X = 0x10000  # a fake, never dereferenced address, 16-byte aligned
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build()
+
+
+def python(code):
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_star_import_needs_no_torch():
+    python("import sys; sys.modules['torch'] = None\n"
+           "from row_wise_arg_gb300 import *\n"
+           "assert callable(argreduce) and callable(argreduce_logits_plan)")
+
+
+@pytest.mark.parametrize("lacking", ["sys.modules['torch'] = None",
+                                     "_lib.load = lambda: (_ for _ in ()).throw(RuntimeError('not built'))"])
+def test_operators_are_absent_where_they_cannot_be_loaded(lacking):
+    """As attributes are: hasattr says so, and the reason is named."""
+    python("import sys\nimport row_wise_arg_gb300 as A\nfrom row_wise_arg_gb300 import _lib\n" + lacking + "\n"
+           "assert not hasattr(A, 'token_logprobs')\n"
+           "try:\n    A.distill_topk\nexcept AttributeError as e:\n    assert e.__cause__ is not None and 'distill_topk' in str(e)\n"
+           "else:\n    raise SystemExit('no error')")
