@@ -409,8 +409,8 @@ argr_status argreduce_noalloc(const void* x, argr_dtype dtype, int64_t rows, int
  *     row's log probability (loss) and gradient become NaN, and nothing is
  *     read or written outside the row.
  *
- * temperature must be positive and finite. Results do not depend on timing:
- * no floating-point atomics are used.
+ * temperature must be positive and finite, and so must log2(e) / temperature.
+ * Results do not depend on timing: no floating-point atomics are used.
  */
 
 /* The operators, for argreduce_logits_plan(). */

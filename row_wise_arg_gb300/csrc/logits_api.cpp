@@ -23,7 +23,8 @@ argr_status check_rows(const void* x, int dtype, int64_t rows, int64_t cols, int
     if (dtype == ARGR_F64 || dtype == ARGR_I32 || dtype == ARGR_I64) return ARGR_EUNSUPPORTED;
     if (dtype != ARGR_F32 && dtype != ARGR_F16 && dtype != ARGR_BF16) return ARGR_EINVAL;
     if (rows < 0 || cols < 1 || cols > INT_MAX || row_stride < 0) return ARGR_EINVAL;
-    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature)) return ARGR_EINVAL;
+    // the kernels scale by log2(e) / T
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.44269504f / temperature)) return ARGR_EINVAL;
     if (rows == 0) return ARGR_OK;
     int64_t bytes;
     if (!extent(rows, cols, row_stride, elem_size(dtype), &bytes)) return ARGR_EINVAL;

@@ -38,3 +38,16 @@ def test_operators_are_absent_where_they_cannot_be_loaded(lacking):
            "assert not hasattr(A, 'token_logprobs')\n"
            "try:\n    A.distill_topk\nexcept AttributeError as e:\n    assert e.__cause__ is not None and 'distill_topk' in str(e)\n"
            "else:\n    raise SystemExit('no error')")
+
+
+def test_temperature_whose_scale_overflows():
+    """log2(e) / T multiplies every difference of logits: infinite, it would turn 0 * inf into NaN."""
+    lib = _lib.load()
+    t = ctypes.c_float(4e-39)  # 1 / t is finite, log2(e) / t is not
+    rows = (X, 0, 3, 100, 100, t)
+    far = X + (1 << 30)
+    assert lib.argreduce_logprobs(*rows, X, 0, X, X, X, None, None, None, None, None) == _lib.ARGR_EINVAL
+    assert lib.argreduce_logprobs_backward(*rows, X, X, X, None, None, far, 100, None, None) == _lib.ARGR_EINVAL
+    assert lib.argreduce_distill(*rows, X, X, 4, 0, X, None, None, None) == _lib.ARGR_EINVAL
+    assert lib.argreduce_distill_backward(*rows, X, X, 4, 0, X, X, far, 100, None, None) == _lib.ARGR_EINVAL
+    assert lib.argreduce_distill_step(*rows, X, X, 4, 0, X, X, X, far, 100, None, None) == _lib.ARGR_EINVAL
