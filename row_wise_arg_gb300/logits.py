@@ -29,6 +29,10 @@ _F32, _I64 = torch.float32, torch.int64
 _empty = torch.empty
 
 
+def _current_device():
+    return torch.cuda.current_device()
+
+
 class TokenLogprobs(NamedTuple):
     logprob: Optional[torch.Tensor]  #: [...] log p of the given token, 0 where it is negative; None without tokens
     entropy: torch.Tensor            #: [...] -sum p log p, in nats
@@ -50,6 +54,9 @@ def _rows(x, dtype):
     """(rows, cols, row stride, type code) of logits."""
     if not x.is_cuda:
         raise ValueError("logits must be a CUDA tensor (the library has no CPU path)")
+    if x.get_device() != _current_device():
+        raise ValueError(f"logits are on cuda:{x.get_device()}, but the current device is cuda:{_current_device()} "
+                         "(the library plans and launches there: enter torch.cuda.device(logits.device))")
     code = _CODES.get(x.dtype) if dtype is None else dtype_code(x, dtype)
     if code is None or code > _lib.ARGR_BF16:
         raise TypeError("logits must be float32, float16 or bfloat16")

@@ -51,3 +51,26 @@ def test_temperature_whose_scale_overflows():
     assert lib.argreduce_distill(*rows, X, X, 4, 0, X, None, None, None) == _lib.ARGR_EINVAL
     assert lib.argreduce_distill_backward(*rows, X, X, 4, 0, X, X, far, 100, None, None) == _lib.ARGR_EINVAL
     assert lib.argreduce_distill_step(*rows, X, X, 4, 0, X, X, X, far, 100, None, None) == _lib.ARGR_EINVAL
+
+
+class Elsewhere:
+    """What the binding looks at of logits that lie on another GPU than the current one."""
+    is_cuda, requires_grad, shape = True, False, (4, 100)
+
+    def get_device(self):
+        return 1
+
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was used of logits on another device")
+
+
+def test_logits_of_another_device_are_refused(monkeypatch):
+    """The library plans and launches on the current device."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = Elsewhere()
+    for call in (lambda: A.token_logprobs(x), lambda: A.token_logprobs_backward(x, None, None),
+                 lambda: A.distill_topk(x, None, None), lambda: A.distill_topk_backward(x, None, None, None, None),
+                 lambda: A.distill_topk_step(x, None, None, None)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
