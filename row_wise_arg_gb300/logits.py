@@ -19,6 +19,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib, _stream_ptr, dtype_code
@@ -57,6 +58,8 @@ def _rows(x, dtype):
     if x.get_device() != _current_device():
         raise ValueError(f"logits are on cuda:{x.get_device()}, but the current device is cuda:{_current_device()} "
                          "(the library plans and launches there: enter torch.cuda.device(logits.device))")
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(x).tangent is not None:
+        raise NotImplementedError("forward-mode differentiation of the vocabulary rows (the tangent would be lost)")
     code = _CODES.get(x.dtype) if dtype is None else dtype_code(x, dtype)
     if code is None or code > _lib.ARGR_BF16:
         raise TypeError("logits must be float32, float16 or bfloat16")

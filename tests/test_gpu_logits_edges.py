@@ -265,3 +265,20 @@ def test_teacher_logits_of_any_size(dtype):
         for temp in (0.5, 1.0, 2.0):
             check_distill(x, dtype, ids, v, temp, False)
             check_distill(x, dtype, ids, v, temp, False, plan=stream_plan(1, 128, 2))
+
+
+def test_forward_mode_is_refused():
+    """A tangent would be dropped without a word."""
+    import torch.autograd.forward_ad as fwd
+    x = torch.randn(3, 50, device="cuda")
+    tok = torch.zeros(3, dtype=torch.int64, device="cuda")
+    ids, val, one = tok[:, None].contiguous(), torch.zeros(3, 1, device="cuda"), torch.ones(3, device="cuda")
+    s = A.token_logprobs(x, tok, with_stats=True).stats
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones_like(x))
+        for call in (lambda: A.token_logprobs(dual, tok), lambda: A.token_logprobs_backward(dual, tok, s, one),
+                     lambda: A.distill_topk(dual, ids, val), lambda: A.distill_topk_step(dual, ids, val, one),
+                     lambda: A.distill_topk_backward(dual, ids, val, s, one)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        A.token_logprobs(x, tok)  # without a tangent all is well
