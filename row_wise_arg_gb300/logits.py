@@ -144,6 +144,8 @@ def _grad_out(x, grad):
     if grad.shape != x.shape or grad.dtype is not x.dtype or grad.device != x.device:
         raise ValueError("grad must have the shape, type and device of logits")
     _, _, stride, _ = _rows(grad, "f32" if grad.element_size() == 4 else "bf16")
+    if not grad.is_inference():
+        torch.autograd.graph.increment_version(grad)  # written through its pointer: graphs that saved it have to know
     return grad, stride
 
 

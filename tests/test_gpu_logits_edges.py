@@ -282,3 +282,28 @@ def test_forward_mode_is_refused():
             with pytest.raises(NotImplementedError, match="forward-mode"):
                 call()
         A.token_logprobs(x, tok)  # without a tangent all is well
+
+
+def test_gradients_written_over_tensors_are_seen_by_autograd():
+    """A graph that saved logits which a gradient has since overwritten says so; inference tensors have no such count."""
+    g = torch.Generator("cuda").manual_seed(7)
+    leaf = torch.randn(4, 300, device="cuda", generator=g, requires_grad=True)
+    tok = torch.randint(0, 300, (4,), device="cuda", generator=g)
+    ids, val, one = tok[:, None].contiguous(), torch.zeros(4, 1, device="cuda"), torch.ones(4, device="cuda")
+    for how in ("logprobs", "distill", "step"):
+        x = leaf * 2.0
+        loss = A.token_logprobs(x, tok).logprob.sum()
+        over = x.detach()
+        if how == "logprobs":
+            A.token_logprobs_backward(over, tok, A.token_logprobs(over, tok, with_stats=True).stats, one, grad=over)
+        elif how == "distill":
+            s = A.distill_topk(over, ids, val, with_stats=True).stats
+            A.distill_topk_backward(over, ids, val, s, one, grad=over)
+        else:
+            A.distill_topk_step(over, ids, val, one, grad=over)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():
+        x = torch.randn(4, 300, device="cuda", generator=g)
+        want = A.distill_topk_step(x, ids, val, one)[1]
+        assert torch.equal(A.distill_topk_step(x, ids, val, one, grad=x)[1], want)
