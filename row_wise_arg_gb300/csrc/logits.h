@@ -16,7 +16,7 @@ struct LogitsProblem {
     int64_t rows;
     int cols;
     int64_t row_stride;  // elements
-    float temperature;
+    float temperature, inv_t;  // and 1 / temperature
     // log probabilities
     const int64_t* tokens;
     int top_k;

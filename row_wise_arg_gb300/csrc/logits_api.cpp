@@ -69,6 +69,7 @@ LogitsProblem rows_problem(const void* x, int dtype, int64_t rows, int64_t cols,
     pr.cols = static_cast<int>(cols);
     pr.row_stride = row_stride;
     pr.temperature = temperature;
+    pr.inv_t = 1.0f / temperature;
     pr.stats = reinterpret_cast<float4*>(stats);
     pr.stream = reinterpret_cast<cudaStream_t>(stream);
     return pr;

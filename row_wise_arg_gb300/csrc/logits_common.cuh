@@ -393,12 +393,13 @@ __device__ __forceinline__ Teacher warp_teacher(const LogitsProblem& pr, const S
         bad = bad || id == kBadId;
         if (id != kNoId) top = fmaxf(top, sl.v[i]);
     }
+    if (!pr.tail) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float inv_t = 1.0f / pr.temperature;
+        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
     float sum = 0.0f;
     for (int i = lane; i < pr.slots; i += 32)
-        if (sl.id[i] != kNoId) sum += expf(pr.tail ? sl.v[i] : (sl.v[i] - top) * inv_t);
+        if (sl.id[i] != kNoId) sum += expf(pr.tail ? sl.v[i] : (sl.v[i] - top) * pr.inv_t);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     Teacher q;
@@ -438,13 +439,13 @@ constexpr float kLeastTail = -745.0f;
 // ln s_rest of a tail, against the row's largest element m; -inf where there is none.
 __device__ __forceinline__ float tail_log(const LogitsProblem& pr, const SoftSum& rest, float m, float ln_s) {
     if (rest.empty()) return neg_inf();
-    const float ln_rest = logf(rest.s) + (rest.m - m) / pr.temperature;
+    const float ln_rest = logf(rest.s) + (rest.m - m) * pr.inv_t;
     return ln_rest - ln_s < kLeastTail ? neg_inf() : ln_rest;
 }
 
 // ln q of a slot with this value.
 __device__ __forceinline__ float teacher_log(const LogitsProblem& pr, const Teacher& q, float v) {
-    return pr.tail ? v : (v - q.top) / pr.temperature - q.ln_sum;
+    return pr.tail ? v : (v - q.top) * pr.inv_t - q.ln_sum;
 }
 
 // What a slot adds to the loss of a row with largest element m.
@@ -472,8 +473,9 @@ __device__ __forceinline__ float row_loss(const LogitsProblem& pr, const Teacher
 
 // The weights of a row's gradient. Named elements: g (total p - q). Others: without a
 // tail g total p; with one g (total p_rest - rest) p / p_rest, the last factor (at most 1) one
-// exponential against the tail's own sum, ln_rest against the element rest_m (the row's largest
-// one will do), so that neither factor leaves binary32's range where p and p_rest do.
+// exponential against the tail's own sum, so that neither factor leaves binary32's range
+// where p and p_rest do. ln_rest is against the row's largest element, own_ln_rest the same against
+// own_m (the tail's largest where it is known, else the row's).
 // `none`: every element is `dense`.
 struct GradWeights {
     float g, total, m, ls2;
@@ -482,9 +484,9 @@ struct GradWeights {
 
     GradWeights() = default;
     __device__ __forceinline__ GradWeights(const LogitsProblem& pr, const Teacher& q, float grad_loss, float row_m,
-                                           float ln_s, float rest_m, float ln_rest) {
+                                           float ln_s, float ln_rest, float own_m, float own_ln_rest) {
         const float rest = ln_rest > neg_inf() ? q.rest : 0.0f;
-        g = grad_loss / pr.temperature;
+        g = grad_loss * pr.inv_t;
         if (q.bad || (ln_s != ln_s && q.any)) g = quiet_nan();
         none = ln_s == neg_inf() || !q.any;  // nothing is taught, or nothing can be
         total = q.total + rest;
@@ -495,9 +497,9 @@ struct GradWeights {
         dense_ls2 = ls2;
         if (none) dense = q.bad ? g : 0.0f;
         else if (rest > 0.0f) {
-            dense = g * (total * expf((rest_m - row_m) / pr.temperature + ln_rest - ln_s) - rest);
-            dense_m = rest_m;
-            dense_ls2 = ln_rest * kLog2E;
+            dense = g * (total * expf(ln_rest - ln_s) - rest);
+            dense_m = own_m;
+            dense_ls2 = own_ln_rest * kLog2E;
         }
     }
     __device__ __forceinline__ float named(float x, float lnq, float scale2) const {

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kGradMaxBlock, 4) distill_grad_kernel(const Lo
         // its barriers order the reads above before the stores below
         const Teacher q = teacher_of(pr, sl, [&](const Teacher& sums) {
             const float4 st = pr.stats[r];
-            if (t == 0) weights = GradWeights(pr, sums, pr.grad_logprob[r], st.x, st.y, st.x, st.z);
+            if (t == 0) weights = GradWeights(pr, sums, pr.grad_logprob[r], st.x, st.y, st.z, st.x, st.z);
         });
         const GradWeights w = weights;
         if (w.none) {

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
     // of every warp of the cluster: (m, s), and the same of the elements that slots name
     __shared__ __align__(16) uint4 parts[kMaxRanks * kStepMaxBlock / 32];
     __shared__ __align__(8) unsigned long long bars[kStepStages + 1];  // the stages', and the exchange's
+    __shared__ GradWeights weights;
     __shared__ unsigned ends[2];  // the named elements of the ragged ends, a bit each
     const int t = threadIdx.x, nt = blockDim.x, lane = t & 31, warp = t >> 5, warps = nt >> 5;
     const int rank = static_cast<int>(blockIdx.x % ranks);
@@ -194,8 +195,8 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
         const float m = all.empty() ? neg_inf() : all.m;
         const float ln_s = all.empty() ? neg_inf() : logf(all.s);
         const float ln_rest = TAIL ? tail_log(pr, c, all.m, ln_s) : ln_s;
-        const Teacher q = *sl.sums;
-        const GradWeights w(pr, q, grad_loss, m, ln_s, TAIL ? c.m : m, TAIL && ln_rest != neg_inf() ? logf(c.s) : ln_rest);
+        const GradWeights w(pr, *sl.sums, grad_loss, m, ln_s, ln_rest, TAIL ? c.m : m, TAIL ? logf(c.s) : ln_rest);
+        if (t == 0) weights = w;  // for the named elements: they come last
         const auto f = [&](float x) { return narrow_elem<Tag>(w.dense * ex2((x - w.dense_m) * scale2 - w.dense_ls2)); };
         // every element that slots name has been read, by all CTAs, before the first is written
         if (w.none) {
@@ -243,12 +244,15 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
             if (has_head) out[lo + lane] = f(x_head);
             if (has_tail) out[tail + lane] = f(x_tail);
             __syncthreads();
+            const Teacher q = *sl.sums;
+            const GradWeights named = weights;
             for (int i = t; i < pr.slots; i += nt) {
                 const int j = sl.id[i];
-                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(w.named(sl.x[i], teacher_log(pr, q, sl.v[i]), scale2));
+                if (j >= lo && j < hi) out[j] = narrow_elem<Tag>(named.named(sl.x[i], teacher_log(pr, q, sl.v[i]), scale2));
             }
         }
         if (rank == 0 && warp == 0) {
+            const Teacher q = *sl.sums;
             float loss = 0.0f;
             for (int i = lane; i < pr.slots; i += 32) loss += slot_loss(pr, q, sl, i, m, ln_s);
 #pragma unroll
