@@ -410,7 +410,8 @@ argr_status argreduce_noalloc(const void* x, argr_dtype dtype, int64_t rows, int
  *     read or written outside the row.
  *
  * temperature must be positive and finite, and so must log2(e) / temperature.
- * Results do not depend on timing: no floating-point atomics are used.
+ * Results do not depend on timing: no floating-point atomics are used (but see
+ * the distillation's ids).
  */
 
 /* The operators, for argreduce_logits_plan(). */
@@ -458,8 +459,12 @@ argr_status argreduce_logprobs_backward(const void* x, argr_dtype dtype, int64_t
 
 /*
  * Distillation of a student (x) from a teacher's top logits. ids[rows, slots]
- * name distinct indices of the row (negative: an empty slot), teacher[rows,
- * slots] holds the teacher's value for each.
+ * name distinct indices of the row (negative: an empty slot; give places that
+ * are left over a negative id, not an index with teacher -inf), teacher[rows,
+ * slots] holds the teacher's value for each. An index that a row names several
+ * times is a mistake that the host cannot see: with a tail the row's sum counts
+ * it as often, and its gradient is that of one of its slots, which one is a
+ * matter of timing. Nothing outside the row is read or written.
  *   tail == 0: q = softmax of teacher / temperature over the row's filled slots;
  *              loss = sum_i q_i (ln q_i - ln p_{id_i}).
  *   tail != 0: q_i = exp(teacher_i): teacher holds log probabilities (taken at

@@ -278,7 +278,8 @@ class _DistillFunction(torch.autograd.Function):
 def distill_topk(logits, ids, teacher, *, temperature: float = 1.0, tail: bool = False, with_stats: bool = False,
                  dtype: Optional[str] = None, plan=None, stream=None) -> DistillLoss:
     """Loss of a student's logits against a teacher's top ones, for each row:
-    ``ids`` [..., slots] int64 names distinct tokens (negative: an empty slot),
+    ``ids`` [..., slots] int64 names distinct tokens (negative: an empty slot; places that
+    are left over take a negative id too, not a token named already),
     ``teacher`` [..., slots] float32 holds the teacher's logits for them, whose
     softmax (at ``temperature``) over the slots is taught, or, with ``tail``,
     the teacher's log probabilities, taught together with what they leave of 1
