@@ -18,12 +18,13 @@
 // again (from L2) and the few that reach the threshold are ranked by counting. Where ties
 // make more groups reach it, the k first groups are found exactly.
 //
-// Bound by latency for few rows: [32, 202048] bf16, in a graph: 5.8 us (13 MB, 2.2 TB/s), 10.2 us
-// with the top 20 (the threshold, the second read, the merge over the cluster; most of it is code
-// that runs once, so short loops beat unrolled ones). For many rows by instruction issue and the
-// barriers between a CTA's phases: [8192, 32000] bf16 96 us, 5.5 TB/s, with the top 20 123 us,
-// 4.2 TB/s; [4096, 50257] bf16, top 20, 96 us, 4.3 TB/s; [512, 100003] f16, 32 slots and a tail, 24.7 us,
-// 4.2 TB/s (one wave: all CTAs read at first and all finish at last).
+// Bound by latency for few rows: [32, 202048] bf16, in a graph of calls whose inputs rotate past
+// L2: 6.1 us (13 MB, 2.1 TB/s), 12 us with the top 20 (the threshold, the second read, the merge over
+// the cluster; most of it is code that runs once, so short loops beat unrolled ones; how many ties the
+// threshold meets moves it by 3 us). For many rows by instruction issue and the barriers between
+// a CTA's phases: [8192, 32000] bf16 92 us, 5.7 TB/s, with the top 20 123 us, 4.2 TB/s; [4096, 50257]
+// bf16, top 20, 99 us, 4.2 TB/s; [512, 100003] f16, 32 slots and a tail, 24.6 us, 4.2 TB/s (one wave:
+// all CTAs read at first and all finish at last).
 #pragma once
 
 #include "logits_common.cuh"
@@ -32,7 +33,10 @@ namespace argr {
 
 constexpr int kFwdMaxBlock = 512;
 constexpr int kListGroups = 1024; // groups picked by a threshold, at most
-constexpr int kFewTop = 20;       // alternatives that 32 values find a threshold for
+// Alternatives that 32 values find a threshold for; more of them bit by bit. Crossing, 32 values / bit by bit,
+// us: [128, 50257] f32 9.9 / 10.2 for the top 8, 10.1 / 10.4 16, 10.9 / 10.5 20, 12.0 / 10.8 28; [4096, 50257]
+// bf16 89 / 91, 102 / 101, 99 / 102, 105 / 109, and 119 / 109 for 32; [32, 202048] bf16 12.9 / 19.3 for 20, 15.6 / 17.9 for 32.
+constexpr int kFewTop = 20;
 constexpr int kRankMax = 512;     // candidates ranked by counting, at most
 
 // Add a group whose largest element is `big`. Without ENT, t is left alone (and

@@ -13,7 +13,8 @@
 //                      g (w p_rest - rest) (p_j / p_rest) / T there
 //
 // Bound by the memory: [2048, 202048] bf16 239 us, 6.9 TB/s read and written; [1024, 262144]
-// bf16, 64 slots, 157 us, 6.9 TB/s; [1024, 100000] f32 121 us, 6.8 TB/s (a copy: 6.8).
+// bf16, 64 slots, 157 us, 6.9 TB/s; [1024, 100000] f32 121 us, 6.8 TB/s (a copy: 6.8). By words of 2 to 8
+// bytes it is not: [1024, 50257] bf16, 64 slots and a tail, 39 us, with rows 50304 apart and the gradient's 50257 97 us.
 #pragma once
 
 #include "logits_common.cuh"

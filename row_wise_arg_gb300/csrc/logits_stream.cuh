@@ -22,7 +22,7 @@
 // reference for the exponentials that moves only when a group exceeds it by more
 // than 2^kSlack.
 //
-// [2048, 202048] bf16: 138 us, 6.0 TB/s; 147, 157, 169 us with the top 1, 20, 64 (the finishing warps
+// [2048, 202048] bf16: 138 us, 6.0 TB/s; 147, 157, 171 us with the top 1, 20, 64 (the finishing warps
 // take issue slots, and the last rows' finish is not hidden); distillation, 64 slots and a tail,
 // 145 us. [2048, 100000] f32 138 us, 6.0 TB/s; [1500, 65537] f32, top 1, 70 us, 5.6 TB/s. A CTA of 256
 // threads and twice as many of them, and picked groups staged in shared memory for the finisher,

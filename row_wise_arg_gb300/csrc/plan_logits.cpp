@@ -1,4 +1,6 @@
-// Planner of the vocabulary-row operators: pure host code.
+// Planner of the vocabulary-row operators: pure host code. Unless a rule says
+// otherwise, its figures come from one call repeated on one input, which up to about 100 MB
+// then comes from L2 (both sides of a rule alike).
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -90,7 +92,10 @@ argr_status make_logits_plan(int what, int64_t rows, int64_t cols, int dtype, in
     // streaming kernel. Rows below the limits finish too often for it ([8192, 32000]
     // bf16: 120 us against 100 us with a CTA of 128 threads per row; [4096, 65536] bf16: 98
     // against 104 us, with 20 alternatives 119 against 116 us); so does a last round that few CTAs
-    // take part in ([512, 100003] f16, 32 slots: 27.4 against 24.5 us).
+    // take part in. Streaming against a CTA per row, us, inputs rotating past L2, the last round 54, 69, 79,
+    // 84, 89, 99% full (330 to 600 rows): [., 202048] bf16 31 / 35, 40 / 39, 41 / 42, 42 / 45, 42 / 48, 43 / 54, with the top
+    // 20 43 / 51, 54 / 46, 54 / 54, 55 / 60, 55 / 65, 55 / 71; [., 100003] f16, 32 slots and a tail 22.7 / 21.7, 25.9 / 22.7,
+    // 26.6 / 23.7, 27.1 / 24.4, 27.1 / 24.5, 27.4 / 26.1. The limit, 85%, lies between these.
     const int es = dtype == ARGR_F32 ? 4 : 2;
     const bool distill = what != ARGR_LOGITS_LOGPROBS;
     const int64_t ctas = 2 * static_cast<int64_t>(caps.sm_count), row_bytes = cols * es;
