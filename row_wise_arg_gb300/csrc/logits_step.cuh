@@ -30,7 +30,7 @@
 //
 // The waits for copies are bounded. One that runs out is recorded
 // (argreduce_read_error); its CTA goes on with what is in shared memory, so that the cluster's
-// barriers are kept, waits again for the copies in flight, and the row's outputs
+// barriers are kept, waits again for the copies and sums in flight, and the row's outputs
 // are undefined.
 #pragma once
 
@@ -266,11 +266,13 @@ __global__ void __launch_bounds__(kStepMaxBlock, 4) distill_step_kernel(const Lo
             }
         }
         if (!__syncthreads_and(landed) && !dead) {
-            // leave no copy in flight behind, and copy no more
+            // leave nothing in flight behind, and copy no more: a CTA whose wait for the exchange ran out stays
+            // until those that still wait for copies, a limit per stage, have sent it their sums
             dead = true;
             if (t == 0) {
                 record_device_error(kErrWaitExpired);
                 for (int s = 0; s < kStepStages; ++s) mbar_wait_bounded(bar + 8 * s, parity, limit);
+                if (ranks > 1) mbar_wait_bounded(bar + 8 * kStepStages, parity, (kStepStages + 1) * kWaitLimitNs);
             }
         }
     }
