@@ -513,6 +513,97 @@ argr_status argreduce_distill_step(const void* x, argr_dtype dtype, int64_t rows
 argr_status argreduce_logits_plan(argr_logits_op what, int64_t rows, int64_t cols, argr_dtype dtype, int32_t k,
                                   const argr_caps* caps, argr_plan* out);
 
+/*
+ * Beam search: the step from the totals of an item's beams and their logits to
+ * the best continuations, and the reordering of what the beams keep.
+ *
+ * x is [items * beams, cols] logits as above (row r of item r / beams), scores[items,
+ * beams] the totals so far. A continuation (b, v) of an item has the total
+ *     scores[b] + x_bv / temperature - lse_b
+ * (lse_b as above), a beam with ended[b] != 0 only one, (b, end_token), with the
+ * total scores[b]. The `count` continuations of the largest scale[b] * total come out, the
+ * first of them first, ties to the lowest (b, v): tokens, parents (the beam b in
+ * [0, beams)) and totals, [items, count] each. ended and scale may be NULL (none
+ * has ended; 1).
+ *   - Only totals above -inf count. Places that none is left for get token -1,
+ *     parent -1 and total -inf.
+ *   - A beam with the total -inf has not begun (or is over): it has no
+ *     continuation. Its logits are not looked at, nor are those of ended beams.
+ *   - An item with a total that is NaN or +inf, a scale (of a beam above -inf) that is
+ *     not positive and finite, or a NaN or +inf among the logits it looks at
+ *     gets tokens and parents -1 and totals NaN.
+ * Totals are formed in binary64 and rounded once; lse_b's sum is binary32, so
+ * continuations of different beams whose totals differ by less than about 1e-6
+ * may come in either order (and equal ones, where the beams' rows do not begin
+ * at the same place between two 32-byte boundaries). Within a beam the order is exact.
+ * 1 <= beams <= ARGR_BEAM_MAX_BEAMS, 1 <= count <= ARGR_LOGITS_MAX_TOP. Errors as
+ * for argreduce_logprobs().
+ */
+#define ARGR_BEAM_MAX_BEAMS 64
+argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items, int32_t beams, int64_t cols,
+                                  int64_t row_stride, float temperature, const float* scores, const uint8_t* ended,
+                                  int64_t end_token, const float* scale, int32_t count, int64_t* tokens,
+                                  int64_t* parents, float* out_scores, argr_stream stream);
+
+/*
+ * Beam j of item i takes over what beam parents[i * beams + j] kept, in each of the
+ * `n_states` states (an array in host memory of device pointers, read during the
+ * call), in place. Beam j's part of item i's state lies at i * item_stride + j *
+ * beam_stride (strides in bytes): `outer` segments, outer_stride apart, of `positions` *
+ * position_bytes contiguous bytes. Only the first lengths[i] positions (NULL:
+ * all; clamped to [0, positions]) of each segment change.
+ *   - A parent outside [0, beams) names nothing: the beam keeps its own state.
+ *   - Several beams may have the same parent, and beams may exchange places.
+ * No state may overlap itself (its dimensions have to nest: no stride smaller than what lies within it),
+ * another one, parents or lengths: ARGR_EINVAL. At most ARGR_REORDER_MAX_STATES of them.
+ */
+#define ARGR_REORDER_MAX_STATES 1024
+argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_t items, int32_t beams,
+                                   int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
+                                   int64_t positions, int64_t position_bytes, const int64_t* parents,
+                                   const int64_t* lengths, argr_stream stream);
+
+/*
+ * A router's choice of experts. x is [rows, experts] logits (types, strides and
+ * arithmetic as for the vocabulary rows, temperature 1). For each row: ids, the top_k
+ * largest logits' indices in descending order, ties to the lowest index; their
+ * weights, p at the ids, divided by their sum where normalize != 0; lse. What is not
+ * above -inf is not chosen: id -1, weight 0. A row with valid[r] == 0 (valid may
+ * be NULL) is padding: it is not looked at; it and a row of -inf alone get ids -1, weights 0,
+ * lse -inf and take part in nothing below. A row with a NaN or +inf has NaN weights and
+ * lse (NaNs are not chosen) and makes the loss NaN.
+ *   counts[e]  how many rows chose expert e
+ *   taken      N, how many rows take part (one value)
+ *   balance    experts * sum_e (counts[e] / (top_k N)) * (sum of p_e over the rows / N);
+ *              1 when all is even, 0 when N = 0 (one value)
+ * counts and taken may be NULL together, balance always; balance needs counts. They need
+ * scratch (argreduce_route_scratch_bytes(), 16-byte aligned, no preparation), which
+ * belongs to the call until it has finished on the stream.
+ * 1 <= experts <= ARGR_ROUTE_MAX_EXPERTS, 1 <= top_k <= min(experts, ARGR_ROUTE_MAX_TOP).
+ * Results do not depend on timing.
+ */
+#define ARGR_ROUTE_MAX_EXPERTS 1024
+#define ARGR_ROUTE_MAX_TOP 32
+size_t argreduce_route_scratch_bytes(int64_t rows, int64_t experts);
+argr_status argreduce_route(const void* x, argr_dtype dtype, int64_t rows, int64_t experts, int64_t row_stride,
+                            int32_t top_k, int normalize, const uint8_t* valid, float* weights, int64_t* ids,
+                            float* lse, int64_t* counts, int64_t* taken, float* balance, void* scratch,
+                            size_t scratch_bytes, argr_stream stream);
+
+/*
+ * The gradient of sum(grad_weights * weights) + sum(grad_lse * lse) + grad_balance *
+ * balance with respect to x, choice and counts held fixed; each of the three may be NULL (zero). ids,
+ * weights, lse, counts and taken as argreduce_route() wrote them for the same x
+ * (ids and weights are needed with grad_weights, counts and taken with
+ * grad_balance). Rows with lse -inf are not looked at and get 0. grad as in
+ * argreduce_logprobs_backward().
+ */
+argr_status argreduce_route_backward(const void* x, argr_dtype dtype, int64_t rows, int64_t experts,
+                                     int64_t row_stride, int32_t top_k, int normalize, const float* weights,
+                                     const int64_t* ids, const float* lse, const int64_t* counts,
+                                     const int64_t* taken, const float* grad_weights, const float* grad_lse,
+                                     const float* grad_balance, void* grad, int64_t grad_stride, argr_stream stream);
+
 /* Properties of `device` as the planner sees them (queried once, cached). */
 argr_status argreduce_device_caps(int device, argr_caps* out);
 

@@ -320,18 +320,23 @@ def argmin(x, **kw):
     return argreduce(x, "min", **kw)[0]
 
 
-_LOGITS = ("token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward", "distill_topk_step",
-           "TokenLogprobs", "DistillLoss")
+# The operators over rows of scores, by the module that has them.
+_LAZY = {"logits": ("token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward",
+                    "distill_topk_step", "TokenLogprobs", "DistillLoss"),
+         "beam": ("beam_select", "beam_reorder", "BeamSelection"),
+         "route": ("route_topk", "route_topk_backward", "Route")}
 
 
 def __getattr__(name):
-    """The vocabulary-row operators, loaded with torch and the library when first asked for
+    """The operators over rows of scores, loaded with torch and the library when first asked for
     (so they are not in __all__: a star import needs neither)."""
-    if name in _LOGITS:
-        try:
-            from . import logits
-        except (ImportError, RuntimeError, OSError) as e:
-            raise AttributeError(f"module {__name__!r} cannot load {name!r}: {e}") from e
-        globals().update((n, getattr(logits, n)) for n in _LOGITS)
-        return globals()[name]
+    for module, names in _LAZY.items():
+        if name in names:
+            import importlib
+            try:
+                found = importlib.import_module(f"{__name__}.{module}")
+            except (ImportError, RuntimeError, OSError) as e:
+                raise AttributeError(f"module {__name__!r} cannot load {name!r}: {e}") from e
+            globals().update((n, getattr(found, n)) for n in names)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,209 @@
+"""Beam search: the step from an item's beams and their logits to the best
+continuations, and the reordering of what the beams keep
+(argreduce_beam_select, argreduce_beam_reorder in include/argreduce.h, where the
+semantics stand).
+
+    chosen = beam_select(logits, totals, 2 * beams)        # [batch, beams, vocab], [batch, beams]
+    ...                                                    # the caller's rules: which of them go on
+    beam_reorder(caches + [histories], parents, lengths, dim=2)
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+from torch.autograd import forward_ad
+
+from . import _lib, _stream_ptr
+from ._lib import ARGR_OK, ArgreduceError
+from .logits import _arg, _current_device, _rows, _side, _under
+
+_LIB = _lib.load()  # looked up once: these calls are short
+_F32, _I64, _BOOL = torch.float32, torch.int64, torch.bool
+_empty = torch.empty
+
+
+class BeamSelection(NamedTuple):
+    tokens: torch.Tensor   #: [..., count] int64, the best continuation first; -1: none was left
+    parents: torch.Tensor  #: [..., count] int64, the beam that it continues; -1: none was left
+    scores: torch.Tensor   #: [..., count] float32, its total; -inf: none was left, NaN: see beam_select
+
+
+def _no_gradient(what, *tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{what} has no gradient: call it under torch.no_grad(), or on detached tensors")
+
+
+def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, scale=None, temperature: float = 1.0,
+                dtype: Optional[str] = None, stream=None) -> BeamSelection:
+    """The ``count`` (at most 128) best continuations of each item's beams:
+    ``logits`` [..., beams, vocab] (strides as in ``token_logprobs``, at most 64
+    beams), ``scores`` [..., beams] float32 the beams' totals of log
+    probabilities so far. A continuation's total is its beam's and the token's log
+    probability; beams with ``ended`` (bool) have one continuation, ``end_token``, with their
+    own total. ``scale`` (float32, positive) multiplies a beam's totals where they are compared, a penalty for
+    length, but not in the scores that are returned. Ties go to the lowest (beam, token).
+
+    A beam with the total -inf has no continuation, and its logits are not looked
+    at (a first step: one beam has begun); neither are an ended beam's. Places that no
+    continuation above -inf is left for hold -1, -1 and -inf. An item with a NaN (or +inf) in what is looked at
+    holds -1, -1 and NaN. Totals of different beams that differ by less than about 1e-6 may come in
+    either order (within a beam the order is exact). Runs on ``stream`` as ``token_logprobs`` does. There is no gradient."""
+    if stream is not None and (side := _side(stream, logits)) is not None:
+        return BeamSelection(*_under(side, (logits, scores, ended, scale), beam_select, logits, scores, count, ended=ended,
+                                     end_token=end_token, scale=scale, temperature=temperature, dtype=dtype))
+    _no_gradient("beam_select", logits, scores, scale)
+    rows, cols, stride, code = _rows(logits, dtype)
+    if logits.dim() < 2:
+        raise ValueError("logits must have the dimensions [..., beams, vocab]")
+    lead, dev = logits.shape[:-1], logits.device
+    beams = lead[-1]
+    if not 1 <= beams <= _lib.BEAM_MAX_BEAMS:
+        raise ValueError(f"between 1 and {_lib.BEAM_MAX_BEAMS} beams, got {beams}")
+    if not 1 <= count <= min(beams * cols, _lib.LOGITS_MAX_TOP):
+        raise ValueError(f"count must be in [1, {min(beams * cols, _lib.LOGITS_MAX_TOP)}], got {count}")
+    if scores is None:
+        raise TypeError("scores must be a tensor of the beams' totals")
+    args = (_arg(scores, "scores", _F32, lead, dev), _arg(ended, "ended", _BOOL, lead, dev), end_token,
+            _arg(scale, "scale", _F32, lead, dev))
+    out = (*lead[:-1], count)
+    tokens, parents = _empty(out, dtype=_I64, device=dev), _empty(out, dtype=_I64, device=dev)
+    totals = _empty(out, dtype=_F32, device=dev)
+    st = _LIB.argreduce_beam_select(logits.data_ptr(), code, rows // beams, beams, cols, stride, temperature, *args, count,
+                                    tokens.data_ptr(), parents.data_ptr(), totals.data_ptr(),
+                                    _stream_ptr(None, dev.index) or None)
+    if st != ARGR_OK:
+        raise ArgreduceError(st, "argreduce_beam_select")
+    return BeamSelection(tokens, parents, totals)
+
+
+def _even(shape, stride):
+    """(count, stride) of evenly spaced dimensions as one, None where they are not."""
+    count, step = 1, 0
+    for n, s in zip(reversed(shape), reversed(stride)):
+        if n == 1:
+            continue
+        if count == 1:
+            step = s
+        elif s != count * step:
+            return None
+        count *= n
+    return count, step
+
+
+def _geometry(t, items, beams, dim):
+    """(item stride, beam stride, segments, their stride, positions, bytes of one) of a state, strides in bytes."""
+    shape, stride, es = t.shape, t.stride(), t.element_size()
+    if len(shape) >= 1 and shape[0] == items * beams:
+        lead, strides = 1, (beams * stride[0], stride[0])
+    elif len(shape) >= 2 and shape[0] == items and shape[1] == beams:
+        lead, strides = 2, stride[:2]
+    else:
+        raise ValueError(f"a state must have the leading dimensions [{items}, {beams}] or [{items * beams}], got {tuple(shape)}")
+    if dim is not None:
+        at = dim + len(shape) if dim < 0 else dim
+        if not lead <= at < len(shape):
+            raise ValueError(f"dim {dim} is not a dimension of a beam's state of shape {tuple(shape[lead:])}")
+    else:
+        at = len(shape)  # the longest contiguous end
+        size = 1
+        while at > lead and (shape[at - 1] == 1 or stride[at - 1] == size):
+            size *= shape[at - 1]
+            at -= 1
+    inner = _even(shape[at + (dim is not None):], stride[at + (dim is not None):])
+    outer = _even(shape[lead:at], stride[lead:at])
+    if inner is None or outer is None or (inner[0] > 1 and inner[1] != 1):
+        raise ValueError("a beam's state must be evenly spaced segments of contiguous positions (make it contiguous)")
+    positions = shape[at] if dim is not None else 1
+    if positions > 1 and stride[at] != inner[0]:
+        raise ValueError("the positions of a state must be contiguous (make it contiguous)")
+    return (strides[0] * es, strides[1] * es, outer[0], outer[1] * es, positions, inner[0] * es)
+
+
+def _span(g, items, beams):
+    """Bytes from a state's first to past its last."""
+    return (items - 1) * g[0] + (beams - 1) * g[1] + (g[2] - 1) * g[3] + g[4] * g[5]
+
+
+def _apart(a, ga, b, gb, items, beams):
+    """Whether two states of different geometry, at the addresses a <= b, certainly share no byte:
+    one ends before the other begins, or they are columns of the same rows."""
+    if a + _span(ga, items, beams) <= b:
+        return True
+    row = ga[1]
+    if ga[:2] != gb[:2] or ga[0] != beams * row or row == 0:
+        return False
+    na, nb = _span(ga, 1, 1), _span(gb, 1, 1)
+    return (b - a) % row >= na and (b - a) % row + nb <= row
+
+
+def beam_reorder(states, parents, lengths=None, *, dim: Optional[int] = None, stream=None):
+    """Reorder what beams keep, in place: in each of ``states`` (a tensor or a
+    list of them: caches, token histories, recurrent states, of any types and sizes) beam j of
+    item i takes over what beam ``parents[i, j]`` had. ``parents`` is int64 [batch, beams] (at most 64
+    beams); a state is [batch, beams, ...] or [batch * beams, ...], a view if need be. A parent outside
+    [0, beams), as beam_select gives where nothing was left, leaves the beam's own state.
+
+    ``lengths`` int64 [batch] with ``dim``, the dimension of the positions (of every state): only the first
+    ``lengths[i]`` positions are moved, later ones stay as they are. Positions and what is within them must be
+    contiguous, the dimensions before evenly spaced; states may not overlap. Returns ``states``."""
+    group = [states] if isinstance(states, torch.Tensor) else list(states)
+    if stream is not None and group and (side := _side(stream, group[0])) is not None:
+        _under(side, (*group, parents, lengths), lambda: [beam_reorder(group, parents, lengths, dim=dim)][1:])
+        return states
+    if parents is None or parents.dim() != 2:
+        raise ValueError("parents must have the dimensions [batch, beams]")
+    items, beams = parents.shape
+    dev = parents.device
+    if not parents.is_cuda:
+        raise ValueError("parents must be a CUDA tensor (the library has no CPU path)")
+    if parents.get_device() != _current_device():
+        raise ValueError(f"parents are on cuda:{parents.get_device()}, but the current device is cuda:{_current_device()} "
+                         "(the library launches there: enter torch.cuda.device(parents.device))")
+    if not 1 <= beams <= _lib.BEAM_MAX_BEAMS:
+        raise ValueError(f"between 1 and {_lib.BEAM_MAX_BEAMS} beams, got {beams}")
+    if lengths is not None and dim is None:
+        raise ValueError("lengths need dim, the dimension of the positions")
+    p_parents = _arg(parents, "parents", _I64, parents.shape, dev)
+    p_lengths = _arg(lengths, "lengths", _I64, (items,), dev)
+    _no_gradient("beam_reorder", *group)
+    plans = {}  # geometry: pointers; states of a kind are looked at once
+    kinds = {}
+    for t in group:
+        key = (t.shape, t.stride(), t.dtype)
+        g = kinds.get(key)
+        if g is None:
+            if t.is_sparse or t.is_complex() and t.is_conj() or t.is_neg():
+                raise ValueError("states must be plain tensors")
+            g = kinds[key] = _geometry(t, items, beams, dim if lengths is not None else None)
+            if lengths is None and dim is not None:
+                _geometry(t, items, beams, dim)  # refuses what it would refuse with lengths
+        if t.device != dev:
+            raise ValueError(f"states must be on {dev}, got one on {t.device}")
+        if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("forward-mode differentiation of beam_reorder (the tangent would be lost)")
+        if t.numel():
+            plans.setdefault(g, []).append(t.data_ptr())
+    if items == 0 or not plans:
+        return states
+    if len(plans) > 1:
+        spans = sorted((p, g) for g, pointers in plans.items() for p in pointers)
+        for i, (p, g) in enumerate(spans):
+            for q, h in spans[i + 1:]:
+                if q >= p + max(_span(k, items, beams) for k in plans):
+                    break
+                if h != g and not _apart(p, g, q, h, items, beams):
+                    raise ValueError("states must not overlap")
+    handle = _stream_ptr(None, dev.index) or None
+    for g, pointers in plans.items():
+        if len(pointers) > _lib.REORDER_MAX_STATES:
+            raise ValueError(f"at most {_lib.REORDER_MAX_STATES} states of a kind, got {len(pointers)}")
+        st = _LIB.argreduce_beam_reorder((ctypes.c_void_p * len(pointers))(*pointers), len(pointers), items, beams, *g,
+                                         p_parents, p_lengths, handle)
+        if st != ARGR_OK:
+            raise ArgreduceError(st, "argreduce_beam_reorder (do states overlap, themselves or one another?)")
+    for t in group:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)  # written through its pointer: graphs that saved it have to know
+    return states

@@ -1,0 +1,84 @@
+// Host-side declarations of the selections over rows of scores
+// (argreduce_beam_select, argreduce_beam_reorder, argreduce_route and its
+// gradient): the problems as the launchers see them, and the launchers.
+#pragma once
+
+#include "logits.h"
+
+namespace argr {
+
+struct BeamProblem {
+    LogitsProblem rows;   // x, cols, row_stride, temperature; rows = items * beams
+    int64_t items;
+    int beams;
+    int count;
+    const float* scores;          // [items, beams]
+    const uint8_t* ended;         // [items, beams] or null
+    const float* scale;           // [items, beams] or null
+    int64_t end_token;
+    double inv_t;                 // 1 / temperature
+    int64_t* tokens;              // [items, count]
+    int64_t* parents;
+    float* out_scores;
+};
+
+constexpr int kReorderStates = 128;  // tensors of one launch
+
+struct ReorderProblem {
+    unsigned char* states[kReorderStates];
+    int n;
+    int64_t items;
+    int beams;
+    int64_t item_stride, beam_stride;  // bytes
+    int64_t outer, outer_stride;       // segments of a beam's state, bytes
+    int64_t positions, pos_bytes;      // a segment is positions * pos_bytes contiguous bytes
+    int word;                          // bytes that every address is a multiple of: 1, 2, 4, 8 or 16
+    const int64_t* parents;            // [items, beams]
+    const int64_t* lengths;            // [items] or null
+    cudaStream_t stream;
+};
+
+struct RouteProblem {
+    const void* x;
+    int dtype;
+    int64_t rows;
+    int experts;
+    int64_t row_stride;  // elements
+    int k;
+    int normalize;
+    const uint8_t* valid;  // [rows] or null
+    // forward
+    float* weights;  // [rows, k]
+    int64_t* ids;
+    float* lse;         // [rows]
+    int64_t* counts;    // [experts] or null
+    int64_t* taken;     // rows that take part
+    float* balance;     // or null
+    float* part_sums;   // scratch: [ctas, experts] sums of the softmax
+    int* part_counts;   // scratch: [ctas, experts + 1] choices, and the rows that take part
+    int ctas;
+    // gradient
+    const float* grad_weights;  // or null
+    const float* grad_lse;      // or null
+    const float* grad_balance;  // one value, or null
+    void* grad;
+    int64_t grad_stride;
+    cudaStream_t stream;
+};
+
+constexpr int kRouteBlock = 256;
+constexpr int kRouteMaxCtas = 1024;  // CTAs that leave partial sums
+int route_ctas(int64_t rows, int experts, const argr_caps& caps);
+
+cudaError_t launch_beam_reorder(const ReorderProblem& pr, const argr_caps& caps);
+cudaError_t launch_route_finish(const RouteProblem& pr);
+#define ARGR_DECLARE_SELECT(sfx)                                                         \
+    cudaError_t launch_beam_select_##sfx(const BeamProblem& pr, const argr_caps& caps);  \
+    cudaError_t launch_route_##sfx(const RouteProblem& pr, const argr_caps& caps);       \
+    cudaError_t launch_route_grad_##sfx(const RouteProblem& pr, const argr_caps& caps);
+ARGR_DECLARE_SELECT(f32)
+ARGR_DECLARE_SELECT(f16)
+ARGR_DECLARE_SELECT(bf16)
+#undef ARGR_DECLARE_SELECT
+
+}  // namespace argr
