@@ -536,14 +536,18 @@ argr_status argreduce_logits_plan(argr_logits_op what, int64_t rows, int64_t col
  * continuations of different beams whose totals differ by less than about 1e-6
  * may come in either order (and equal ones, where the beams' rows do not begin
  * at the same place between two 32-byte boundaries). Within a beam the order is exact.
- * 1 <= beams <= ARGR_BEAM_MAX_BEAMS, 1 <= count <= ARGR_LOGITS_MAX_TOP. Errors as
- * for argreduce_logprobs().
+ * 1 <= beams <= ARGR_BEAM_MAX_BEAMS, 1 <= count <= ARGR_LOGITS_MAX_TOP. Steps of many
+ * rows need scratch (argreduce_beam_scratch_bytes(), 0 for the others; 16-byte aligned, no
+ * preparation), which belongs to the call until it has finished on the stream. Errors as
+ * for argreduce_logprobs(); ARGR_ESCRATCH.
  */
 #define ARGR_BEAM_MAX_BEAMS 64
 argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items, int32_t beams, int64_t cols,
                                   int64_t row_stride, float temperature, const float* scores, const uint8_t* ended,
                                   int64_t end_token, const float* scale, int32_t count, int64_t* tokens,
-                                  int64_t* parents, float* out_scores, argr_stream stream);
+                                  int64_t* parents, float* out_scores, void* scratch, size_t scratch_bytes,
+                                  argr_stream stream);
+size_t argreduce_beam_scratch_bytes(int64_t items, int32_t beams, int64_t cols, argr_dtype dtype, int32_t count);
 
 /*
  * Beam j of item i takes over what beam parents[i * beams + j] kept, in each of the

@@ -54,7 +54,8 @@ EXPORTS = (
     "argreduce_axis", "argreduce_axis_plan", "argreduce_axis_with_plan", "argreduce_cum", "argreduce_cum_plan",
     "argreduce_cum_with_plan", "argreduce_cum_scratch_bytes", "argreduce_plan_check",
     "argreduce_logprobs", "argreduce_logprobs_backward", "argreduce_distill", "argreduce_distill_backward",
-    "argreduce_distill_step", "argreduce_logits_plan", "argreduce_beam_select", "argreduce_beam_reorder",
+    "argreduce_distill_step", "argreduce_logits_plan", "argreduce_beam_select", "argreduce_beam_scratch_bytes",
+    "argreduce_beam_reorder",
     "argreduce_route", "argreduce_route_backward", "argreduce_route_scratch_bytes",
 )
 
@@ -153,7 +154,7 @@ def load() -> ctypes.CDLL:
         for f in (lib.argreduce_logprobs, lib.argreduce_logprobs_backward, lib.argreduce_distill,
                   lib.argreduce_distill_backward, lib.argreduce_distill_step, lib.argreduce_logits_plan):
             f.restype = i32
-        lib.argreduce_beam_select.argtypes = [vp, i32, i64, i32, i64, i64, f32, vp, vp, i64, vp, i32, vp, vp, vp, vp]
+        lib.argreduce_beam_select.argtypes = [vp, i32, i64, i32, i64, i64, f32, vp, vp, i64, vp, i32, vp, vp, vp, vp, sz, vp]
         lib.argreduce_beam_reorder.argtypes = [vp, i32, i64, i32, i64, i64, i64, i64, i64, i64, vp, vp, vp]
         lib.argreduce_route.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         lib.argreduce_route_backward.argtypes = [vp, i32, i64, i64, i64, i32, i32] + [vp] * 9 + [i64, vp]
@@ -162,6 +163,8 @@ def load() -> ctypes.CDLL:
             f.restype = i32
         lib.argreduce_route_scratch_bytes.argtypes = [i64, i64]
         lib.argreduce_route_scratch_bytes.restype = sz
+        lib.argreduce_beam_scratch_bytes.argtypes = [i64, i32, i64, i32, i32]
+        lib.argreduce_beam_scratch_bytes.restype = sz
         lib.argreduce_version.argtypes = []
         lib.argreduce_version.restype = ctypes.c_char_p
         del i64p

@@ -70,9 +70,14 @@ def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, s
     out = (*lead[:-1], count)
     tokens, parents = _empty(out, dtype=_I64, device=dev), _empty(out, dtype=_I64, device=dev)
     totals = _empty(out, dtype=_F32, device=dev)
-    st = _LIB.argreduce_beam_select(logits.data_ptr(), code, rows // beams, beams, cols, stride, temperature, *args, count,
+    items = rows // beams
+    scratch = None
+    nbytes = _LIB.argreduce_beam_scratch_bytes(items, beams, cols, code, count)
+    if nbytes:  # this call's own: torch keeps it from others until the stream has passed the call
+        scratch = _empty(nbytes, dtype=torch.uint8, device=dev)
+    st = _LIB.argreduce_beam_select(logits.data_ptr(), code, items, beams, cols, stride, temperature, *args, count,
                                     tokens.data_ptr(), parents.data_ptr(), totals.data_ptr(),
-                                    _stream_ptr(None, dev.index) or None)
+                                    scratch.data_ptr() if nbytes else None, nbytes, _stream_ptr(None, dev.index) or None)
     if st != ARGR_OK:
         raise ArgreduceError(st, "argreduce_beam_select")
     return BeamSelection(tokens, parents, totals)

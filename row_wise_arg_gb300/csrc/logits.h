@@ -36,6 +36,11 @@ struct LogitsProblem {
     const float* grad_logprob;  // grad_loss for the distillation
     const float* grad_entropy;
     const float* grad_lse;
+    // the beams' lists, for a later merge (select.h)
+    unsigned long long* beam_keys;  // [rows, top_k]
+    float2* beam_sums;              // [rows] largest element, sum
+    const float* beam_scores;       // [rows], with
+    const uint8_t* beam_ended;      // [rows] or null: which rows are looked at
     void* grad;
     int64_t grad_stride;
     cudaStream_t stream;

@@ -37,7 +37,8 @@ constexpr float kSlack = 8.0f;        // in powers of two; sums stay far below o
 constexpr int kStreamCands = 1024;    // candidates for alternatives, at most
 constexpr int kStreamList = 640;      // slots looked into at a time, at most
 constexpr int kRankKeys = 192;        // keys that the finisher ranks by counting, at most (and its spare keys)
-enum StreamMode { kStreamSums = 0, kStreamTop = 1, kStreamLoss = 2, kStreamLossTail = 3 };
+enum StreamMode { kStreamSums = 0, kStreamTop = 1, kStreamLoss = 2, kStreamLossTail = 3, kStreamBeam = 4 };
+inline __host__ __device__ constexpr bool stream_top(int mode) { return mode == kStreamTop || mode == kStreamBeam; }
 
 template <class Tag> constexpr int kWideElems = 2 * kGroupElems<Tag>;
 
@@ -54,6 +55,11 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
     __syncwarp();
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Whether a beam's row is looked at (argreduce_beam_select).
+__device__ __forceinline__ bool beam_looks(const LogitsProblem& pr, int64_t r) {
+    return pr.beam_scores[r] != neg_inf() && !(pr.beam_ended && pr.beam_ended[r]);
 }
 
 // A row in wide groups. Slot 0 is its head, slots 1 .. body the groups, slot body + 1 its tail.
@@ -98,19 +104,19 @@ struct StreamLayout {
         sums = at;
         at += 4 * sizeof(float) * static_cast<size_t>(warps);
         most = at;
-        if (mode == kStreamTop) at += 4 * 32 * static_cast<size_t>(warps);
+        if (stream_top(mode)) at += 4 * 32 * static_cast<size_t>(warps);
         tile = at;
-        if (mode == kStreamTop) at += 4 * static_cast<size_t>((slots / 32 + 1 + 3) / 4 * 4);
+        if (stream_top(mode)) at += 4 * static_cast<size_t>((slots / 32 + 1 + 3) / 4 * 4);
         big = at;
-        if (mode == kStreamTop) at += 4 * static_cast<size_t>(slots);
+        if (stream_top(mode)) at += 4 * static_cast<size_t>(slots);
         named = at;
         if (mode == kStreamLossTail) at += (static_cast<size_t>(slots) * wide_elems / 8 + 15) / 16 * 16;
         teacher = at;
         if (mode == kStreamLoss || mode == kStreamLossTail) at += Slots::bytes(n);
         buffer = (at + 15) / 16 * 16;
         cand = (fin + 1) * buffer;
-        list = cand + (mode == kStreamTop ? 8 * static_cast<size_t>(fin) * (kStreamCands + kRankKeys) : 0);
-        total = list + (mode == kStreamTop ? 2 * static_cast<size_t>(fin) * kStreamList : 0);
+        list = cand + (stream_top(mode) ? 8 * static_cast<size_t>(fin) * (kStreamCands + kRankKeys) : 0);
+        total = list + (stream_top(mode) ? 2 * static_cast<size_t>(fin) * kStreamList : 0);
     }
 };
 
@@ -158,7 +164,7 @@ __device__ __forceinline__ void stream_rows(const LogitsProblem& pr, float scale
                                             unsigned char* dyn) {
     using R = typename Tag::raw;
     constexpr bool ENT = MODE == kStreamSums || MODE == kStreamTop;
-    constexpr bool TOP = MODE == kStreamTop, DROP = MODE == kStreamLossTail;
+    constexpr bool TOP = stream_top(MODE), DROP = MODE == kStreamLossTail;
     constexpr int E = kWideElems<Tag>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = (lay.streamers + 1) * 32;
     int at = 0;        // the row's buffer
@@ -168,7 +174,8 @@ __device__ __forceinline__ void stream_rows(const LogitsProblem& pr, float scale
         unsigned* big_at = reinterpret_cast<unsigned*>(buf + lay.big);
         const WideRow<Tag> row(pr, r);
         const R* body = row.p + row.align;
-        const int tiles = (row.body + 31) >> 5;
+        const bool look = MODE != kStreamBeam || beam_looks(pr, r);
+        const int tiles = look ? (row.body + 31) >> 5 : 0;
         bar_sync(free_bar(at), threads);  // the buffer is free (and holds this row's bits)
         SoftSum c;
         float top = neg_inf();
@@ -226,7 +233,7 @@ __device__ __forceinline__ void stream_rows(const LogitsProblem& pr, float scale
         }
         mine -= tiles;
         // the ragged ends: the head with the first warp, the tail with the last
-        if (warp == 0 || warp == lay.streamers - 1) {
+        if (look && (warp == 0 || warp == lay.streamers - 1)) {
 #pragma unroll
             for (int end = 0; end < 2; ++end) {
                 if (warp != (end ? lay.streamers - 1 : 0)) continue;
@@ -584,7 +591,7 @@ __device__ __forceinline__ void finish_rows(const LogitsProblem& pr, float scale
     // a row's token and its logit, loaded while the row before is finished
     int64_t tok = -1;
     float tok_x = 0.0f;
-    const auto load_token = [&](int64_t r) { return !LOSS && pr.logprob && r < pr.rows ? pr.tokens[r] : -1; };
+    const auto load_token = [&](int64_t r) { return !LOSS && MODE != kStreamBeam && pr.logprob && r < pr.rows ? pr.tokens[r] : -1; };
     const auto load_logit = [&](int64_t r, int64_t t) {
         return t >= 0 && t < pr.cols ? widen_elem<Tag>(ld_scalar(WideRow<Tag>(pr, r).p + t)) : 0.0f;
     };
@@ -602,7 +609,20 @@ __device__ __forceinline__ void finish_rows(const LogitsProblem& pr, float scale
         if (lay.finishers > 1 && r + ctas < pr.rows)
             bar_arrive(turn_bar(finisher + 1 < lay.finishers ? finisher + 1 : 0), 64);
         SoftSum c = joined_sums(buf + lay.sums, lay.streamers, scale2);
-        if constexpr (!LOSS) {
+        if constexpr (MODE == kStreamBeam) {
+            if (beam_looks(pr, r)) {
+                unsigned long long* cand = reinterpret_cast<unsigned long long*>(dyn + lay.cand) +
+                                           finisher * (kStreamCands + kRankKeys);
+                const int k = pr.top_k;
+                warp_top<Tag>(row, k, reinterpret_cast<const unsigned*>(buf + lay.big),
+                              reinterpret_cast<const unsigned*>(buf + lay.tile),
+                              reinterpret_cast<const unsigned*>(buf + lay.most), lay.streamers, cand,
+                              reinterpret_cast<unsigned short*>(dyn + lay.list) + finisher * kStreamList);
+                for (int i = lane; i < k; i += 32) pr.beam_keys[r * k + i] = cand[kStreamCands + i];
+                if (lane == 0) pr.beam_sums[r] = make_float2(c.m, c.s);
+                __syncwarp();
+            }
+        } else if constexpr (!LOSS) {
             const float ln_s = c.empty() ? neg_inf() : logf(c.s);
             if (lane == 0) {
                 const float h = kLn2 * (log2f(c.s) - c.t / c.s);

@@ -1,58 +1,80 @@
 // Joins what the CTAs of a router's kernel left: per-expert counts, the number of
-// rows that take part, and the balance loss (route.cuh).
-#include "logits_common.cuh"
+// rows that take part, and the balance loss (route.cuh). One cluster: each CTA
+// joins a share of the experts, a lane to an expert, its warps the CTAs' parts in turns.
+#include "logits_forward.cuh"
 #include "select.h"
 
 namespace argr {
 
-constexpr int kFinishBlock = 1024;
+constexpr int kFinishCtas = 8;
+constexpr int kFinishWarps = 32;
 
-__global__ void __launch_bounds__(kFinishBlock) route_finish_kernel(const RouteProblem pr) {
-    __shared__ double red[32];
-    __shared__ long long rows;
-    const int t = threadIdx.x, E = pr.experts;
+__global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(32 * kFinishWarps) route_finish_kernel(const RouteProblem pr) {
+    __shared__ int parts[kFinishWarps][32];
+    __shared__ float sums[kFinishWarps][32];
+    __shared__ double shares[kFinishCtas];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = pr.experts, cta = static_cast<int>(blockIdx.x);
     allow_dependents();
     grid_dependency_wait();
-    double sum = 0.0;
-    for (int e = t; e <= E; e += kFinishBlock) {
-        long long n = 0;
-        double p = 0.0;
-        for (int b = 0; b < pr.ctas; ++b) {
-            n += pr.part_counts[static_cast<int64_t>(b) * (E + 1) + e];
-            if (pr.balance && e < E) p += pr.part_sums[static_cast<int64_t>(b) * E + e];
+    double mine = 0.0;  // of warp 0's lanes
+    __shared__ long long rows;
+    // 32 experts at a time; the rows that take part follow the last expert
+    for (int e0 = 32 * cta; e0 <= E; e0 += 32 * kFinishCtas) {
+        const int e = e0 + lane;
+        int n = 0;
+        float p = 0.0f;
+        if (e <= E) {
+#pragma unroll 4
+            for (int b = warp; b < pr.ctas; b += kFinishWarps) {
+                n += pr.part_counts[static_cast<int64_t>(b) * (E + 1) + e];
+                if (pr.balance && e < E) p += pr.part_sums[static_cast<int64_t>(b) * E + e];
+            }
         }
-        if (e < E) pr.counts[e] = n;
-        else {
-            *pr.taken = n;
-            rows = n;
+        parts[warp][lane] = n;
+        sums[warp][lane] = p;
+        __syncthreads();
+        if (warp == 0 && e <= E) {
+            long long all = 0;
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFinishWarps; ++w) {
+                all += parts[w][lane];
+                t += sums[w][lane];
+            }
+            if (e < E) {
+                pr.counts[e] = all;
+                mine += static_cast<double>(all) * t;
+            } else {
+                *pr.taken = all;
+                rows = all;
+            }
         }
-        sum += static_cast<double>(n) * p;
+        __syncthreads();
     }
     if (!pr.balance) return;
+    if (warp == 0) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((t & 31) == 0) red[t >> 5] = sum;
-    __syncthreads();
-    if (t == 0) {
+        for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    }
+    // to the CTA that has the number of rows
+    const int owner = E / 32 % kFinishCtas;
+    cluster_ready();
+    cluster_wait();
+    if (threadIdx.x == 0)
+        st_cluster(cluster_addr(smem_u32(&shares[cta]), owner), static_cast<unsigned long long>(__double_as_longlong(mine)));
+    cluster_arrive();
+    cluster_wait();
+    if (cta == owner && threadIdx.x == 0) {
         double all = 0.0;
-        for (int w = 0; w < kFinishBlock / 32; ++w) all += red[w];
-        const double n = static_cast<double>(rows > 0 ? rows : 1);
-        *pr.balance = static_cast<float>(all * E / (pr.k * n * n));
+        for (int q = 0; q < kFinishCtas; ++q) all += shares[q];
+        *pr.balance = route_balance(all, rows, E, pr.k);
     }
 }
 
 cudaError_t launch_route_finish(const RouteProblem& pr) {
     argr_plan p = {};
     p.flags = ARGR_PLAN_PDL;
-    return launch_ex_smem(route_finish_kernel, dim3(1), dim3(kFinishBlock), 1, 0, p, pr.stream, pr);
-}
-
-int route_ctas(int64_t rows, int experts, const argr_caps& caps) {
-    (void)experts;
-    const int64_t want = (rows + kRouteBlock / 32 - 1) / (kRouteBlock / 32);
-    int64_t most = 4 * static_cast<int64_t>(caps.sm_count);
-    if (most > kRouteMaxCtas) most = kRouteMaxCtas;
-    return static_cast<int>(want < most ? want : most);
+    return launch_ex_smem(route_finish_kernel, dim3(kFinishCtas), dim3(32 * kFinishWarps), 1, 0, p, pr.stream, pr);
 }
 
 }  // namespace argr

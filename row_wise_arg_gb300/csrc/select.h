@@ -8,12 +8,10 @@
 namespace argr {
 
 struct BeamProblem {
-    LogitsProblem rows;   // x, cols, row_stride, temperature; rows = items * beams
+    LogitsProblem rows;   // x, cols, row_stride, temperature, beam_*; rows = items * beams
     int64_t items;
     int beams;
     int count;
-    const float* scores;          // [items, beams]
-    const uint8_t* ended;         // [items, beams] or null
     const float* scale;           // [items, beams] or null
     int64_t end_token;
     double inv_t;                 // 1 / temperature
@@ -66,10 +64,20 @@ struct RouteProblem {
     cudaStream_t stream;
 };
 
-constexpr int kRouteBlock = 256;
-constexpr int kRouteMaxCtas = 1024;  // CTAs that leave partial sums
-int route_ctas(int64_t rows, int experts, const argr_caps& caps);
+constexpr int kRouteBlock = 512;
+constexpr int kRouteMaxCtas = 512;  // CTAs that leave partial sums, at most
+constexpr int kRouteOneTurns = 2;   // turns of one cluster's CTAs over the rows, at most
 
+#ifdef __CUDACC__
+// The balance loss from sum_e counts_e (sum over the rows of p_e).
+__device__ __forceinline__ float route_balance(double sum, long long rows, int experts, int k) {
+    const double n = static_cast<double>(rows > 0 ? rows : 1);
+    return static_cast<float>(sum * experts / (k * n * n));
+}
+#endif
+
+// Scratch of a step, 0 where it is one launch.
+size_t beam_scratch_bytes(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps);
 cudaError_t launch_beam_reorder(const ReorderProblem& pr, const argr_caps& caps);
 cudaError_t launch_route_finish(const RouteProblem& pr);
 #define ARGR_DECLARE_SELECT(sfx)                                                         \

@@ -65,9 +65,14 @@ argr_status check_route(const void* x, int dtype, int64_t rows, int64_t experts,
     return ARGR_OK;
 }
 
+// CTAs that leave sums and counts in a route's scratch, at most: two per SM (route.cuh), and a row to each.
+int64_t route_parts(int64_t rows, const argr_caps& caps) {
+    return std::min<int64_t>(rows, std::min<int64_t>(2 * static_cast<int64_t>(caps.sm_count), kRouteMaxCtas));
+}
 // Scratch of a route: the CTAs' sums, then their counts.
-size_t route_bytes(int ctas, int64_t experts) {
-    return align_up(4 * static_cast<size_t>(ctas) * experts, 16) + 4 * static_cast<size_t>(ctas) * (experts + 1);
+size_t route_sums_bytes(int64_t parts, int64_t experts) { return align_up(4 * static_cast<size_t>(parts) * experts, 16); }
+size_t route_bytes(int64_t parts, int64_t experts) {
+    return route_sums_bytes(parts, experts) + 4 * static_cast<size_t>(parts) * (experts + 1);
 }
 
 }  // namespace
@@ -80,7 +85,8 @@ extern "C" {
 argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items, int32_t beams, int64_t cols,
                                   int64_t row_stride, float temperature, const float* scores, const uint8_t* ended,
                                   int64_t end_token, const float* scale, int32_t count, int64_t* tokens,
-                                  int64_t* parents, float* out_scores, argr_stream stream) {
+                                  int64_t* parents, float* out_scores, void* scratch, size_t scratch_bytes,
+                                  argr_stream stream) {
     if (beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items < 0 || items > INT_MAX / 16) return ARGR_EINVAL;
     argr_status s = check_rows(x, dtype, items * beams, cols, row_stride, temperature);
     if (s != ARGR_OK) return s;
@@ -104,15 +110,28 @@ argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items
     pr.items = items;
     pr.beams = beams;
     pr.count = count;
-    pr.scores = scores;
-    pr.ended = ended;
+    pr.rows.beam_scores = scores;
+    pr.rows.beam_ended = ended;
     pr.scale = scale;
     pr.end_token = end_token;
     pr.inv_t = 1.0 / static_cast<double>(temperature);
     pr.tokens = tokens;
     pr.parents = parents;
     pr.out_scores = out_scores;
+    if (const size_t need = beam_scratch_bytes(items, beams, cols, dtype, pr.rows.top_k, caps)) {
+        if (!scratch || misaligned(scratch, 16) || scratch_bytes < need) return ARGR_ESCRATCH;
+        pr.rows.beam_keys = static_cast<unsigned long long*>(scratch);
+        pr.rows.beam_sums = reinterpret_cast<float2*>(pr.rows.beam_keys + pr.rows.rows * pr.rows.top_k);
+    }
     return ARGR_SELECT_DISPATCH(launch_beam_select, dtype, pr, caps);
+}
+
+size_t argreduce_beam_scratch_bytes(int64_t items, int32_t beams, int64_t cols, argr_dtype dtype, int32_t count) {
+    argr_caps caps;
+    if (items < 1 || beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items > INT_MAX / 16 || cols < 1 || cols > INT_MAX || count < 1 ||
+        count > ARGR_LOGITS_MAX_TOP || (dtype != ARGR_F32 && dtype != ARGR_F16 && dtype != ARGR_BF16) || current_caps(&caps) != ARGR_OK)
+        return 0;
+    return beam_scratch_bytes(items, beams, cols, dtype, static_cast<int>(std::min<int64_t>(count, cols)), caps);
 }
 
 argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_t items, int32_t beams,
@@ -172,7 +191,7 @@ argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_
 size_t argreduce_route_scratch_bytes(int64_t rows, int64_t experts) {
     argr_caps caps;
     if (rows < 1 || experts < 1 || experts > ARGR_ROUTE_MAX_EXPERTS || current_caps(&caps) != ARGR_OK) return 0;
-    return route_bytes(route_ctas(rows, static_cast<int>(experts), caps), experts);
+    return route_bytes(route_parts(rows, caps), experts);
 }
 
 argr_status argreduce_route(const void* x, argr_dtype dtype, int64_t rows, int64_t experts, int64_t row_stride,
@@ -204,12 +223,12 @@ argr_status argreduce_route(const void* x, argr_dtype dtype, int64_t rows, int64
     pr.counts = counts;
     pr.taken = taken;
     pr.balance = balance;
-    pr.ctas = route_ctas(rows, pr.experts, caps);
     pr.stream = reinterpret_cast<cudaStream_t>(stream);
     if (counts && rows > 0) {
-        if (!scratch || misaligned(scratch, 16) || scratch_bytes < route_bytes(pr.ctas, experts)) return ARGR_ESCRATCH;
+        const int64_t parts = route_parts(rows, caps);
+        if (!scratch || misaligned(scratch, 16) || scratch_bytes < route_bytes(parts, experts)) return ARGR_ESCRATCH;
         pr.part_sums = static_cast<float*>(scratch);
-        pr.part_counts = reinterpret_cast<int*>(static_cast<char*>(scratch) + align_up(4 * static_cast<size_t>(pr.ctas) * experts, 16));
+        pr.part_counts = reinterpret_cast<int*>(static_cast<char*>(scratch) + route_sums_bytes(parts, experts));
     }
     if (rows == 0) return launched(launch_route_finish(pr));
     return ARGR_SELECT_DISPATCH(launch_route, dtype, pr, caps);
@@ -248,7 +267,6 @@ argr_status argreduce_route_backward(const void* x, argr_dtype dtype, int64_t ro
     pr.grad_balance = grad_balance;
     pr.grad = grad;
     pr.grad_stride = grad_stride;
-    pr.ctas = route_ctas(rows, pr.experts, caps);
     pr.stream = reinterpret_cast<cudaStream_t>(stream);
     return ARGR_SELECT_DISPATCH(launch_route_grad, dtype, pr, caps);
 }

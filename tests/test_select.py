@@ -22,7 +22,7 @@ def built():
 
 def select(**kw):
     a = dict(x=X, dtype=0, items=2, beams=3, cols=100, stride=100, temp=1.0, scores=FAR, ended=None, end=0, scale=None, count=4,
-             tokens=FAR, parents=FAR, out=FAR, stream=None)
+             tokens=FAR, parents=FAR, out=FAR, scratch=None, bytes=0, stream=None)
     a.update(kw)
     return _lib.load().argreduce_beam_select(*a.values())
 
