@@ -10,10 +10,12 @@
 //     dx_e = p_e (c_e - sum_j c_j p_j + h [- sum_i g_i w_i where not normalised])
 //            + [e is chosen i] w_i (g_i [- sum_j g_j w_j where normalised]).
 //
-// A row is held by G lanes of a warp, V contiguous elements to a lane, and every element is read
-// once. A warp takes RW rows at a time (32 / G side by side, or some one after the other where a row
-// takes all lanes), so that what is done once per row or per choice (logarithm,
-// quotients, ranks, stores) is done by different lanes for different rows. Warps own evenly dealt, contiguous rows
+// Two phases. A row is read once, by G lanes of a warp, in blocks of 8 elements dealt to the lanes in turns, the warp's
+// 32 / G rows side by side: sums, p, and the largest element of each block, which goes to shared memory. Then, for
+// up to 32 such rows, a lane to a row: it takes the block of the largest head, reads that block again, finds the
+// element and the block's next head, k times over. A choice so costs a handful of instructions of one lane and none of
+// them crosses lanes; with a warp, or 8 lanes, to a row a choice took most of 540 or 280 instructions a
+// row ([65536, 256], top 8), in chains of votes and shuffles. Warps own evenly dealt, contiguous rows
 // and keep the sums of p of their elements in registers. Sums over CTAs are joined in a fixed order, without
 // atomics: where one cluster suffices by it, through distributed shared memory;
 // else every CTA leaves its sums and counts in scratch and a second kernel joins them
@@ -47,18 +49,18 @@ __device__ __forceinline__ float group_max(float v) {
     }
 }
 
-// A lane's V elements [lo, lo + V) of a row of E, as they lie in memory; -inf past the row's end.
-template <class Tag, int V>
+// N contiguous elements [lo, lo + N) of a row of E, as they lie in memory; -inf past the row's end.
+template <class Tag, int N>
 struct LaneRow {
     using R = typename Tag::raw;
     static constexpr int P = 16 / static_cast<int>(sizeof(R));  // elements of 16 bytes
-    uint32_t w[V * sizeof(R) / 4];
+    uint32_t w[N * sizeof(R) / 4];
 
     // `wide`: rows begin at 16-byte boundaries.
     __device__ __forceinline__ void load(const R* row, int lo, int E, bool wide) {
-        if (wide && lo + V <= E) {
+        if (wide && lo + N <= E) {
 #pragma unroll
-            for (int i = 0; i < V / P; ++i) {
+            for (int i = 0; i < N / P; ++i) {
                 const uint4 v = *reinterpret_cast<const uint4*>(row + lo + i * P);
                 w[4 * i] = v.x;
                 w[4 * i + 1] = v.y;
@@ -67,7 +69,7 @@ struct LaneRow {
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < N; ++j) {
                 const R v = lo + j < E ? row[lo + j] : none();
                 if constexpr (sizeof(R) == 4) w[j] = __float_as_uint(v);
                 else if (j & 1) w[j >> 1] |= static_cast<uint32_t>(v) << 16;
@@ -77,23 +79,23 @@ struct LaneRow {
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < V * static_cast<int>(sizeof(R)) / 4; ++i)
+        for (int i = 0; i < N * static_cast<int>(sizeof(R)) / 4; ++i)
             w[i] = sizeof(R) == 4 ? 0xff800000u : std::is_same<Tag, TagBF16>::value ? 0xff80ff80u : 0xfc00fc00u;
     }
     static __device__ __forceinline__ R none() {
         if constexpr (sizeof(R) == 4) return neg_inf();
         else return std::is_same<Tag, TagBF16>::value ? 0xff80 : 0xfc00;
     }
-    __device__ __forceinline__ void widen(float (&x)[V]) const {
+    __device__ __forceinline__ void widen(float* x) const {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < N; ++j) {
             if constexpr (sizeof(R) == 4) x[j] = __uint_as_float(w[j]);
             else x[j] = Tag::widen(static_cast<uint16_t>(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu));
         }
     }
 };
 
-// Rows of a warp at a time, one after the other, where a row takes all its lanes (by the registers of a lane and the gradient's
+// Gradient: rows of a warp at a time, one after the other, where a row takes all its lanes (by the registers of a lane and the
 // shared memory).
 template <int G, int V> constexpr int kTurns = G < 32 ? 1 : V <= 8 ? 4 : V <= 16 ? 2 : 1;
 
@@ -101,106 +103,98 @@ template <int G, int V> constexpr int kTurns = G < 32 ? 1 : V <= 8 ? 4 : V <= 16
 struct WarpShare {
     int64_t lo, hi;
     __device__ __forceinline__ explicit WarpShare(int64_t units) {
-        const int64_t w = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+        const int64_t w = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // (what is over, an SM after the other)
         const int64_t all = static_cast<int64_t>(gridDim.x) * kRouteWarps, each = units / all, more = units - each * all;
         lo = w * each + (w < more ? w : more);
         hi = lo + each + (w < more);
     }
 };
 
-// What a lane's rows choose, in order: G lanes find the largest of what is left k times. Lane 0 of the
-// group hands each choice to `put(i, e, x)`.
-template <int G, int V, class Put>
-__device__ __forceinline__ void choose_in_turns(const float (&x)[V], int lg, int k, Put put) {
-    unsigned key[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = choice_key(x[j]);
-    for (int i = 0; i < k; ++i) {
-        unsigned best = 0;
-        int e = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                e = lg * V + j;
-            }
-        if constexpr (G == 32) {
-            const unsigned top = __reduce_max_sync(0xffffffffu, best);
-            e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(e) : ~0u));
-            best = top;
-        } else {
-#pragma unroll
-            for (int o = G / 2; o >= 1; o >>= 1) {
-                const unsigned b = __shfl_xor_sync(0xffffffffu, best, o);
-                const int f = __shfl_xor_sync(0xffffffffu, e, o);
-                if (b > best || (b == best && f < e)) {
-                    best = b;
-                    e = f;
-                }
-            }
-        }
-        put(i, best ? e : -1, best ? order_value(best) : neg_inf());
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e == lg * V + j) key[j] = 0u;
-    }
-}
-
-// What reaches the threshold of a row over a whole warp, collected in `cand` (32 keys, any order); returns how many, or -1
-// where they are more. The k-th largest of the lanes' own largest elements is reached by at
-// least k elements, seldom by many more.
-template <class Tag, int V>
-__device__ __forceinline__ int collect(const float (&x)[V], int lane, int k, unsigned long long* cand) {
-    float big = x[0];
-#pragma unroll
-    for (int j = 1; j < V; ++j) big = fmaxf(big, x[j]);
-    unsigned left = choice_key(big), at = 0;
-#pragma unroll 4
-    for (int i = 0; i < k; ++i) {
-        at = __reduce_max_sync(0xffffffffu, left);
-        if (left == at) left = 0u;
-    }
-    // fewer lanes than k have one: every element that can be chosen
-    const float least = at == 0u ? -FLT_MAX : order_value(at);
-    unsigned hits = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) hits |= static_cast<unsigned>(x[j] >= least) << j;
-    const unsigned below = (1u << lane) - 1u;
-    int n = 0;
-    for (;;) {
-        const unsigned has = __ballot_sync(0xffffffffu, hits != 0);
-        if (has == 0) return n;
-        const int p = n + __popc(has & below);
-        n += __popc(has);
-        if (n > 32) return -1;
-        if (hits) {
-            const int j = __ffs(hits) - 1;
-            hits &= hits - 1;
-            float v = x[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i)
-                if (i == j) v = x[i];
-            cand[p] = order_key(v, lane * V + j);
-        }
-    }
-}
-
-// Shared memory of the forward kernel: the CTA's choices and rows [E + 1], its sums of p [E] and half its warps'
-// on the way there, and per warp its rows' choices (weights, then ids) and, where a row takes all lanes, 32 keys for each.
+// Shared memory of the forward kernel: the CTA's choices and rows [E + 1], its sums of p [E]; per warp the rows' maxima and
+// sums, the heads of their blocks, from which element on a block's elements equal to its head are left, and
+// their choices (weights, then ids); at the end half the warps' sums.
 template <int G, int V>
 struct RouteLayout {
-    static constexpr int RW = 32 / G * kTurns<G, V>;
-    size_t hist, acc, half, stage, keys, each, total;
+    static constexpr int BLOCKS = G * V / 8;                          // of a row
+    static constexpr int ROWS = BLOCKS <= 32 ? 32 : 1024 / BLOCKS;    // of a batch
+    static constexpr int PITCH = ROWS + 1;                            // of a block's heads: lanes and blocks in different banks
+    size_t hist, acc, half, warp, sums, heads, after, weights, ids, each, total;
     __host__ __device__ RouteLayout(int E, int k) {
         hist = 0;
         acc = 4 * static_cast<size_t>((E + 1 + 3) / 4 * 4);
-        half = acc + 4 * static_cast<size_t>((E + 3) / 4 * 4);
-        stage = half + 4 * static_cast<size_t>(kRouteWarps / 2) * G * V;
-        keys = 8 * static_cast<size_t>(RW) * k;  // (in a warp's part)
-        each = (keys + (G == 32 ? 8 * 32 * static_cast<size_t>(RW) : 0) + 15) / 16 * 16;
-        total = stage + kRouteWarps * each;
+        half = warp = acc + 4 * static_cast<size_t>((E + 3) / 4 * 4);
+        sums = 0;  // (in a warp's part)
+        heads = 8 * ROWS;
+        after = heads + 4 * static_cast<size_t>(BLOCKS) * PITCH;
+        weights = (after + static_cast<size_t>(BLOCKS) * PITCH + 15) / 16 * 16;
+        ids = weights + 4 * static_cast<size_t>(ROWS) * k;
+        each = (ids + 4 * static_cast<size_t>(ROWS) * k + 15) / 16 * 16;
+        const size_t a = kRouteWarps * each, b = 4 * static_cast<size_t>(kRouteWarps / 2) * G * V;
+        total = warp + (a > b ? a : b);
     }
 };
+
+// The k choices of this lane's row, in order. Its heads are at heads[block * PITCH], with after[...] as above (0 at first).
+// Of the blocks' heads the largest of every 8 are kept in registers. A block's elements are taken in order, so what is left
+// of it is what is below the element taken last, or equals it further on.
+template <class Tag, int G, int V, class Put>
+__device__ __forceinline__ void choose(const typename Tag::raw* row, int E, bool wide, float* heads, unsigned char* after, int k,
+                                       Put put) {
+    constexpr int BLOCKS = RouteLayout<G, V>::BLOCKS, PITCH = RouteLayout<G, V>::PITCH;
+    constexpr int S = BLOCKS < 8 ? BLOCKS : 8, M = BLOCKS / S;  // M sets of S blocks
+    float most[M];
+#pragma unroll
+    for (int q = 0; q < M; ++q) {
+        most[q] = heads[q * S * PITCH];
+#pragma unroll
+        for (int i = 1; i < S; ++i) most[q] = fmaxf(most[q], heads[(q * S + i) * PITCH]);
+    }
+    int n = 0;
+    for (; n < k; ++n) {
+        float g = most[0];
+#pragma unroll
+        for (int q = 1; q < M; ++q) g = fmaxf(g, most[q]);
+        if (!(g > neg_inf())) break;  // (NaN: blocks of NaNs alone, which are never chosen)
+        int set = 0;
+#pragma unroll
+        for (int q = M - 1; q >= 0; --q)
+            if (most[q] == g) set = q;
+        float h[S];
+        int at = 0;
+#pragma unroll
+        for (int i = S - 1; i >= 0; --i) {
+            h[i] = heads[(set * S + i) * PITCH];
+            if (h[i] == g) at = i;
+        }
+        const int block = set * S + at, from = after[block * PITCH];
+        LaneRow<Tag, 8> raw;
+        raw.load(row, block * 8, E, wide);
+        float x[8];
+        raw.widen(x);
+        int j = 8, again = 8;
+        float below = neg_inf();
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            const bool same = x[i] == g && i >= from;
+            if (same) {
+                again = j;
+                j = i;
+            }
+            if (x[i] < g) below = fmaxf(below, x[i]);
+        }
+        const float next = again < 8 ? g : below;
+        heads[block * PITCH] = next;
+        after[block * PITCH] = static_cast<unsigned char>(again < 8 ? again : 0);
+        float best = neg_inf();
+#pragma unroll
+        for (int i = 0; i < S; ++i) best = fmaxf(best, i == at ? next : h[i]);
+#pragma unroll
+        for (int q = 0; q < M; ++q)
+            if (q == set) most[q] = best;
+        put(n, block * 8 + j, g);
+    }
+    for (; n < k; ++n) put(n, -1, neg_inf());
+}
 
 __device__ __forceinline__ int ld_cluster(unsigned addr) {
     int v;
@@ -211,16 +205,24 @@ __device__ __forceinline__ int ld_cluster(unsigned addr) {
 template <class Tag, int G, int V>
 __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(const RouteProblem pr, int cluster) {
     using R = typename Tag::raw;
-    constexpr int T = kTurns<G, V>, RW = 32 / G * T, LG = 32 / RW;  // rows at a time, and lanes to each where they are finished
+    using Layout = RouteLayout<G, V>;
+    constexpr int U = 32 / G, B = V / 8, ROWS = Layout::ROWS, PITCH = Layout::PITCH;  // U: rows of a unit; B: blocks of a lane
     extern __shared__ __align__(16) unsigned char dyn[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), sub = lane / G;
     const int E = pr.experts, k = pr.k;
-    const RouteLayout<G, V> lay(E, k);
+    const Layout lay(E, k);
     int* hist = reinterpret_cast<int*>(dyn + lay.hist);
     float* acc = reinterpret_cast<float*>(dyn + lay.acc);
-    unsigned char* stage = dyn + lay.stage + warp * lay.each;
-    float* weights = reinterpret_cast<float*>(stage);  // [RW][k]
-    int* ids = reinterpret_cast<int*>(weights + RW * k);
+    unsigned char* part = dyn + lay.warp + warp * lay.each;
+    float2* row_sums = reinterpret_cast<float2*>(part + lay.sums);
+    float* heads = reinterpret_cast<float*>(part + lay.heads);
+    unsigned char* after = part + lay.after;
+    float* weights = reinterpret_cast<float*>(part + lay.weights);  // [ROWS][k]
+    int* ids = reinterpret_cast<int*>(part + lay.ids);
+    const R* base = static_cast<const R*>(pr.x);
+    const bool wide = (reinterpret_cast<uintptr_t>(pr.x) | static_cast<uintptr_t>(pr.row_stride) * sizeof(R)) % 16 == 0;
+    const WarpShare share((pr.rows + U - 1) / U);
+    const int64_t end = share.hi * U < pr.rows ? share.hi * U : pr.rows;
     allow_dependents();
     if (pr.counts)
         for (int i = threadIdx.x; i <= E; i += kRouteBlock) hist[i] = 0;
@@ -229,129 +231,77 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
     for (int j = 0; j < V; ++j) sum_p[j] = 0.0f;
     grid_dependency_wait();
     __syncthreads();
-    const bool wide = (reinterpret_cast<uintptr_t>(pr.x) | static_cast<uintptr_t>(pr.row_stride) * sizeof(R)) % 16 == 0;
-    const R* base = static_cast<const R*>(pr.x);
     int taken = 0;
-    // units: passes of 32 / G rows, or rows
-    constexpr int U = G < 32 ? 32 / G : 1;
-    const WarpShare share((pr.rows + U - 1) / U);
-    const int64_t end = share.hi * U < pr.rows ? share.hi * U : pr.rows;
-    for (int64_t r0 = share.lo * U; r0 < end; r0 += RW) {
-        const int rows = end - r0 < RW ? static_cast<int>(end - r0) : RW;  // of this pass
-        const bool mine = lane < rows && (!pr.valid || pr.valid[r0 + lane]);
-        const unsigned valid = __ballot_sync(0xffffffffu, mine);
-        // of row lane / LG, for what is done once a row
-        float ref = 0.0f, m = neg_inf(), s = 0.0f, all = 0.0f;
-        if constexpr (G < 32) {
-            LaneRow<Tag, V> raw;
-            raw.clear();
-            if (valid >> sub & 1u) raw.load(base + (r0 + sub) * pr.row_stride, lg * V, E, wide);
-            float x[V], p[V];
-            raw.widen(x);
-            m = x[0];
-#pragma unroll
-            for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
-            m = group_max<G>(m);
-            if (m != m) m = neg_inf();  // (NaN alone)
-            ref = m == neg_inf() ? 0.0f : m;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                p[j] = ex2((x[j] - ref) * kLog2E);
-                s += p[j];
-            }
-            s = group_sum<G>(s);
-            if (pr.balance && s != 0.0f) {
-                const float inv = 1.0f / s;
-#pragma unroll
-                for (int j = 0; j < V; ++j) sum_p[j] += p[j] * inv;
-            }
-            choose_in_turns<G, V>(x, lg, k, [&](int i, int e, float v) {
-                const float w = ex2((v - ref) * kLog2E);  // (0 where nothing was chosen)
-                all += w;
-                if (lg == 0) {
-                    weights[sub * k + i] = w;
-                    ids[sub * k + i] = e;
-                }
-            });
-        } else {
-            unsigned long long* cand = reinterpret_cast<unsigned long long*>(stage + lay.keys);  // [RW][32]
-            int found = 0;
-            LaneRow<Tag, V> raw;
-            raw.clear();
-            if (valid & 1u) raw.load(base + r0 * pr.row_stride, lane * V, E, wide);
-            for (int q = 0; q < rows; ++q) {
-                float x[V], p[V];
-                raw.widen(x);
-                raw.clear();
-                if (valid >> 1 >> q & 1u) raw.load(base + (r0 + q + 1) * pr.row_stride, lane * V, E, wide);
-                if (!(valid >> q & 1u)) continue;
-                float big = x[0];
-#pragma unroll
-                for (int j = 1; j < V; ++j) big = fmaxf(big, x[j]);
-                big = group_max<32>(big);
-                if (big != big) big = neg_inf();  // (NaN alone)
-                const float r = big == neg_inf() ? 0.0f : big;
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    p[j] = ex2((x[j] - r) * kLog2E);
-                    sum += p[j];
-                }
-                sum = group_sum<32>(sum);
-                if (pr.balance && sum != 0.0f) {
-                    const float inv = 1.0f / sum;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) sum_p[j] += p[j] * inv;
-                }
-                int n = collect<Tag, V>(x, lane, k, cand + 32 * q);
-                if (n < 0) {
-                    n = 0;
-                    choose_in_turns<G, V>(x, lane, k, [&](int i, int e, float v) {
-                        if (e >= 0) {
-                            if (lane == 0) cand[32 * q + i] = order_key(v, e);
-                            n = i + 1;
-                        }
-                    });
-                }
-                if (lane / LG == q) {
-                    m = big;
-                    ref = r;
-                    s = sum;
-                    found = n;
-                }
-            }
-            __syncwarp();
-            // ranks by counting, LG lanes to a row
-            const int q = lane / LG;
-            const unsigned long long* mine = cand + 32 * q;
-            for (int c = lane % LG; c < found; c += LG) {
-                const unsigned long long key = mine[c];
-                int rank = 0;
+    for (int64_t r0 = share.lo * U; r0 < end; r0 += ROWS) {
+        const int rows = end - r0 < ROWS ? static_cast<int>(end - r0) : ROWS;
+        const bool here = lane < rows && (!pr.valid || pr.valid[r0 + lane]);
+        const unsigned valid = __ballot_sync(0xffffffffu, here);
+        if (lane < ROWS) {
 #pragma unroll 4
-                for (int i = 0; i < found; ++i) rank += mine[i] > key;
-                if (rank < k) {
-                    const float w = ex2((order_value(static_cast<unsigned>(key >> 32)) - ref) * kLog2E);
-                    all += w;
-                    weights[q * k + rank] = w;
-                    ids[q * k + rank] = key_index(key);
-                }
-            }
-            for (int i = found + lane % LG; i < k; i += LG) {
-                weights[q * k + i] = 0.0f;
-                ids[q * k + i] = -1;
-            }
-            all = group_sum<LG>(all);
+            for (int b = 0; b < Layout::BLOCKS; ++b) after[b * PITCH + lane] = 0;
         }
-        const bool live = s != 0.0f;  // (a NaN is live)
-        const float inv = !live ? 0.0f : s != s ? quiet_nan() : 1.0f / (pr.normalize ? all : s);
-        if (lane % LG == 0 && lane / LG < rows) {
-            pr.lse[r0 + lane / LG] = live ? m + logf(s) : neg_inf();
+        for (int q0 = 0; q0 < rows; q0 += U) {
+            const int q = q0 + sub;  // row of the batch
+            const bool on = valid >> q & 1u;
+            const R* row = base + (r0 + q) * pr.row_stride;
+            float x[V], top = neg_inf();
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                LaneRow<Tag, 8> raw;
+                raw.clear();
+                if (on) raw.load(row, (b * G + lg) * 8, E, wide);
+                raw.widen(x + 8 * b);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float* y = x + 8 * b;
+                const float h = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+                heads[(b * G + lg) * PITCH + q] = h;
+                top = fmaxf(top, h);
+            }
+            const float m = group_max<G>(top), ref = m == neg_inf() ? 0.0f : m;
+            const f32x2 minus = pack2(-ref, -ref), scale = pack2(kLog2E, kLog2E);
+            f32x2 sums = 0;
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                unpack2(mul2(add2(pack2(x[j], x[j + 1]), minus), scale), x[j], x[j + 1]);
+                x[j] = ex2(x[j]);
+                x[j + 1] = ex2(x[j + 1]);
+                sums = add2(sums, pack2(x[j], x[j + 1]));
+            }
+            float lo, hi;
+            unpack2(sums, lo, hi);
+            const float s = group_sum<G>(lo + hi);
+            if (lg == 0) row_sums[q] = make_float2(m, s);
+            if (pr.balance && s != 0.0f) {
+                const float inv = __frcp_rn(s);
+                const f32x2 of = pack2(inv, inv);
+#pragma unroll
+                for (int j = 0; j < V; j += 2)
+                    unpack2(fma2(pack2(x[j], x[j + 1]), of, pack2(sum_p[j], sum_p[j + 1])), sum_p[j], sum_p[j + 1]);
+            }
+        }
+        __syncwarp();
+        float inv = 0.0f;
+        if (lane < rows) {
+            const float2 v = row_sums[lane];
+            const float m = v.x, s = v.y, ref = m == neg_inf() ? 0.0f : m;
+            const bool live = s != 0.0f;  // (a NaN is live)
+            float all = 0.0f;
+            choose<Tag, G, V>(base + (r0 + lane) * pr.row_stride, E, wide, heads + lane, after + lane, k, [&](int i, int e, float x) {
+                const float w = ex2((x - ref) * kLog2E);  // (0 where nothing was chosen)
+                all += w;
+                weights[lane * k + i] = w;
+                ids[lane * k + i] = e;
+            });
+            inv = !live ? 0.0f : s != s ? quiet_nan() : 1.0f / (pr.normalize ? all : s);
+            pr.lse[r0 + lane] = live ? m + logf(s) : neg_inf();
             taken += live;
         }
         __syncwarp();
         for (int i0 = 0; i0 < rows * k; i0 += 32) {
-            const int i = i0 + lane, q = i < rows * k ? i / k : 0;  // row of the pass
-            const float scale = __shfl_sync(0xffffffffu, inv, q * LG);
+            const int i = i0 + lane, q = i < rows * k ? i / k : 0;
+            const float scale = __shfl_sync(0xffffffffu, inv, q);
             if (i < rows * k) {
                 const int id = ids[i];
                 pr.weights[r0 * k + i] = weights[i] * scale;
@@ -371,6 +321,7 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
 #pragma unroll
             for (int o = 16; o >= G; o >>= 1) sum_p[j] += __shfl_xor_sync(0xffffffffu, sum_p[j], o);
         }
+        __syncthreads();
         for (int h = kRouteWarps / 2; h >= 1; h >>= 1) {
             if (warp >= h && warp < 2 * h && sub == 0) {
 #pragma unroll
@@ -385,8 +336,10 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
         }
         if (warp == 0 && sub == 0) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (lg * V + j < E) acc[lg * V + j] = sum_p[j];
+            for (int j = 0; j < V; ++j) {
+                const int e = (j / 8 * G + lg) * 8 + j % 8;
+                if (e < E) acc[e] = sum_p[j];
+            }
         }
     }
     __syncthreads();
@@ -632,6 +585,16 @@ cudaError_t launch_route_grad_gv(const RouteProblem& pr, const argr_caps& caps) 
                           dim3(kRouteBlock), 1, smem, p, pr.stream, pr);
 }
 
+// Rows of 8 lanes for 33 to 256 experts, then more lanes, as the sums of p take a register per element of a lane.
+#define ARGR_ROUTE_FORWARD_GV(fn, Tag, pr, caps)        \
+    ((pr).experts <= 8     ? fn<Tag, 1, 8>(pr, caps)    \
+     : (pr).experts <= 16  ? fn<Tag, 2, 8>(pr, caps)    \
+     : (pr).experts <= 32  ? fn<Tag, 4, 8>(pr, caps)    \
+     : (pr).experts <= 64  ? fn<Tag, 8, 8>(pr, caps)    \
+     : (pr).experts <= 128 ? fn<Tag, 8, 16>(pr, caps)   \
+     : (pr).experts <= 256 ? fn<Tag, 8, 32>(pr, caps)   \
+     : (pr).experts <= 512 ? fn<Tag, 16, 32>(pr, caps)  \
+                           : fn<Tag, 32, 32>(pr, caps))
 #define ARGR_ROUTE_GV(fn, Tag, pr, caps)                \
     ((pr).experts <= 8     ? fn<Tag, 1, 8>(pr, caps)    \
      : (pr).experts <= 16  ? fn<Tag, 2, 8>(pr, caps)    \
@@ -644,7 +607,7 @@ cudaError_t launch_route_grad_gv(const RouteProblem& pr, const argr_caps& caps) 
 
 template <class Tag>
 cudaError_t launch_route_t(const RouteProblem& pr, const argr_caps& caps) {
-    return ARGR_ROUTE_GV(launch_route_gv, Tag, pr, caps);
+    return ARGR_ROUTE_FORWARD_GV(launch_route_gv, Tag, pr, caps);
 }
 template <class Tag>
 cudaError_t launch_route_grad_t(const RouteProblem& pr, const argr_caps& caps) {
