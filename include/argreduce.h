@@ -580,9 +580,9 @@ argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_
  *   taken      N, how many rows take part (one value)
  *   balance    experts * sum_e (counts[e] / (top_k N)) * (sum of p_e over the rows / N);
  *              1 when all is even, 0 when N = 0 (one value)
- * counts and taken may be NULL together, balance always; balance needs counts. They need
- * scratch (argreduce_route_scratch_bytes(), 16-byte aligned, no preparation), which
- * belongs to the call until it has finished on the stream.
+ * counts and taken may be NULL together, balance always; balance needs counts. For many
+ * rows they need scratch (argreduce_route_scratch_bytes(), 0 for the others; 16-byte aligned, no
+ * preparation), which belongs to the call until it has finished on the stream.
  * 1 <= experts <= ARGR_ROUTE_MAX_EXPERTS, 1 <= top_k <= min(experts, ARGR_ROUTE_MAX_TOP).
  * Results do not depend on timing.
  */

@@ -16,12 +16,13 @@ import torch
 from torch.autograd import forward_ad
 
 from . import _lib, _stream_ptr
-from ._lib import ARGR_OK, ArgreduceError
+from ._lib import ARGR_ESCRATCH, ARGR_OK, ArgreduceError
 from .logits import _arg, _current_device, _rows, _side, _under
 
 _LIB = _lib.load()  # looked up once: these calls are short
 _F32, _I64, _BOOL = torch.float32, torch.int64, torch.bool
 _empty = torch.empty
+_MAX_BEAMS, _MAX_COUNT = _lib.BEAM_MAX_BEAMS, _lib.LOGITS_MAX_TOP
 
 
 class BeamSelection(NamedTuple):
@@ -31,7 +32,11 @@ class BeamSelection(NamedTuple):
 
 
 def _no_gradient(what, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is None or not t.requires_grad:
+            continue
         raise RuntimeError(f"{what} has no gradient: call it under torch.no_grad(), or on detached tensors")
 
 
@@ -55,29 +60,28 @@ def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, s
                                      end_token=end_token, scale=scale, temperature=temperature, dtype=dtype))
     _no_gradient("beam_select", logits, scores, scale)
     rows, cols, stride, code = _rows(logits, dtype)
-    if logits.dim() < 2:
-        raise ValueError("logits must have the dimensions [..., beams, vocab]")
     lead, dev = logits.shape[:-1], logits.device
+    if not lead:
+        raise ValueError("logits must have the dimensions [..., beams, vocab]")
     beams = lead[-1]
-    if not 1 <= beams <= _lib.BEAM_MAX_BEAMS:
-        raise ValueError(f"between 1 and {_lib.BEAM_MAX_BEAMS} beams, got {beams}")
-    if not 1 <= count <= min(beams * cols, _lib.LOGITS_MAX_TOP):
-        raise ValueError(f"count must be in [1, {min(beams * cols, _lib.LOGITS_MAX_TOP)}], got {count}")
+    if not 1 <= beams <= _MAX_BEAMS:
+        raise ValueError(f"between 1 and {_MAX_BEAMS} beams, got {beams}")
+    if not 1 <= count <= min(beams * cols, _MAX_COUNT):
+        raise ValueError(f"count must be in [1, {min(beams * cols, _MAX_COUNT)}], got {count}")
     if scores is None:
         raise TypeError("scores must be a tensor of the beams' totals")
-    args = (_arg(scores, "scores", _F32, lead, dev), _arg(ended, "ended", _BOOL, lead, dev), end_token,
-            _arg(scale, "scale", _F32, lead, dev))
     out = (*lead[:-1], count)
     tokens, parents = _empty(out, dtype=_I64, device=dev), _empty(out, dtype=_I64, device=dev)
     totals = _empty(out, dtype=_F32, device=dev)
-    items = rows // beams
-    scratch = None
-    nbytes = _LIB.argreduce_beam_scratch_bytes(items, beams, cols, code, count)
-    if nbytes:  # this call's own: torch keeps it from others until the stream has passed the call
+    args = (logits.data_ptr(), code, rows // beams, beams, cols, stride, temperature, _arg(scores, "scores", _F32, lead, dev),
+            _arg(ended, "ended", _BOOL, lead, dev), end_token, _arg(scale, "scale", _F32, lead, dev), count,
+            tokens.data_ptr(), parents.data_ptr(), totals.data_ptr())
+    handle = _stream_ptr(None, dev.index) or None
+    st = _LIB.argreduce_beam_select(*args, None, 0, handle)
+    if st == ARGR_ESCRATCH:  # many rows; the scratch is this call's own: torch keeps it until the stream has passed the call
+        nbytes = _LIB.argreduce_beam_scratch_bytes(rows // beams, beams, cols, code, count)
         scratch = _empty(nbytes, dtype=torch.uint8, device=dev)
-    st = _LIB.argreduce_beam_select(logits.data_ptr(), code, items, beams, cols, stride, temperature, *args, count,
-                                    tokens.data_ptr(), parents.data_ptr(), totals.data_ptr(),
-                                    scratch.data_ptr() if nbytes else None, nbytes, _stream_ptr(None, dev.index) or None)
+        st = _LIB.argreduce_beam_select(*args, scratch.data_ptr(), nbytes, handle)
     if st != ARGR_OK:
         raise ArgreduceError(st, "argreduce_beam_select")
     return BeamSelection(tokens, parents, totals)
@@ -166,30 +170,30 @@ def beam_reorder(states, parents, lengths=None, *, dim: Optional[int] = None, st
     if parents.get_device() != _current_device():
         raise ValueError(f"parents are on cuda:{parents.get_device()}, but the current device is cuda:{_current_device()} "
                          "(the library launches there: enter torch.cuda.device(parents.device))")
-    if not 1 <= beams <= _lib.BEAM_MAX_BEAMS:
-        raise ValueError(f"between 1 and {_lib.BEAM_MAX_BEAMS} beams, got {beams}")
+    if not 1 <= beams <= _MAX_BEAMS:
+        raise ValueError(f"between 1 and {_MAX_BEAMS} beams, got {beams}")
     if lengths is not None and dim is None:
         raise ValueError("lengths need dim, the dimension of the positions")
     p_parents = _arg(parents, "parents", _I64, parents.shape, dev)
     p_lengths = _arg(lengths, "lengths", _I64, (items,), dev)
     _no_gradient("beam_reorder", *group)
-    plans = {}  # geometry: pointers; states of a kind are looked at once
-    kinds = {}
+    plans = {}  # geometry: pointers
+    shape = stride = kind = pointers = None  # of the state before: a list's are mostly alike
+    tangents = forward_ad._current_level >= 0
     for t in group:
-        key = (t.shape, t.stride(), t.dtype)
-        g = kinds.get(key)
-        if g is None:
-            if t.is_sparse or t.is_complex() and t.is_conj() or t.is_neg():
+        if t.shape != shape or t.stride() != stride or t.dtype is not kind:
+            shape, stride, kind = t.shape, t.stride(), t.dtype
+            if t.is_sparse or t.is_conj() or t.is_neg():
                 raise ValueError("states must be plain tensors")
-            g = kinds[key] = _geometry(t, items, beams, dim if lengths is not None else None)
+            g = _geometry(t, items, beams, dim if lengths is not None else None)
             if lengths is None and dim is not None:
                 _geometry(t, items, beams, dim)  # refuses what it would refuse with lengths
+            pointers = plans.setdefault(g, []) if t.numel() else []
         if t.device != dev:
             raise ValueError(f"states must be on {dev}, got one on {t.device}")
-        if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        if tangents and forward_ad.unpack_dual(t).tangent is not None:
             raise NotImplementedError("forward-mode differentiation of beam_reorder (the tangent would be lost)")
-        if t.numel():
-            plans.setdefault(g, []).append(t.data_ptr())
+        pointers.append(t.data_ptr())
     if items == 0 or not plans:
         return states
     if len(plans) > 1:
@@ -208,7 +212,6 @@ def beam_reorder(states, parents, lengths=None, *, dim: Optional[int] = None, st
                                          p_parents, p_lengths, handle)
         if st != ARGR_OK:
             raise ArgreduceError(st, "argreduce_beam_reorder (do states overlap, themselves or one another?)")
-    for t in group:
-        if not t.is_inference():
-            torch.autograd.graph.increment_version(t)  # written through its pointer: graphs that saved it have to know
+    # written through their pointers: graphs that saved them have to know
+    torch.autograd.graph.increment_version([t for t in group if not t.is_inference()])
     return states

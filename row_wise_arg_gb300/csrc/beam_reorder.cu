@@ -7,6 +7,10 @@
 // (but as a parent) nor written. A parent of several beams is read from memory once, its other
 // reads hit L1.
 //
+// The words of an item's live positions are numbered through, segment after segment, and cut into tiles; the tiles of
+// all items are dealt to as many CTAs as run at once. (With CTAs for each item, and for segments of the
+// longest, items of different lengths left them waiting in waves: 12 states of 9 items, 5 beams, 77 positions took 21 us.)
+//
 // Bound by memory: each distinct parent read once, each moving beam written once.
 #include "kernels_impl.cuh"
 #include "select.h"
@@ -14,6 +18,12 @@
 namespace argr {
 
 constexpr int kReorderBlock = 256;
+template <int BEAMS> constexpr int kReorderItems = BEAMS <= 16 ? 32 : 8;  // items at a time
+// CTAs of an SM, at least. What is in flight decides (45 KB an SM at the copy rate): words per thread against threads.
+// 32 bf16 caches of 16 items, lengths up to 1024, us: 4 beams 310, 335, 379 with 2, 4, 1 words of 16 bytes and 4, 2, 6
+// CTAs; 8 beams, 16 caches of 8 items, 208, 246 with 2, 1 words and 2, 4 CTAs; 5 beams of 4-byte words ([9, 5] states of
+// 119 KB, 12 of them) 15.6, 18.7 with 2, 4 words and 4, 2 CTAs. More CTAs than run at once, four times as many, took 299, 206, 21.3.
+template <int BEAMS, int W> constexpr int kReorderCtas = BEAMS <= 4 ? 4 : BEAMS <= 8 ? (W == 16 ? 2 : W == 8 ? 3 : 4) : BEAMS <= 16 ? 2 : 1;
 
 template <int W> struct WordOf;
 template <> struct WordOf<16> { using type = uint4; };
@@ -22,81 +32,133 @@ template <> struct WordOf<4> { using type = uint32_t; };
 template <> struct WordOf<2> { using type = uint16_t; };
 template <> struct WordOf<1> { using type = uint8_t; };
 
-// A tile: kReorderBlock words of a segment of one state. BEAMS: beams at most; U words per thread at a time.
+// a / b and what is left, in 32 bits where they fit.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t* left) {
+    int64_t q;
+    if (((a | b) >> 32) == 0) q = static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    else q = a / b;
+    *left = a - q * b;
+    return q;
+}
+
+template <int BEAMS>
+struct Moves {
+    int64_t to[kReorderItems<BEAMS>][BEAMS], from[kReorderItems<BEAMS>][BEAMS];  // bytes from beam 0
+    int n[32];
+    int64_t bytes[32];  // live in a segment
+    int64_t end[32];    // of the item's tiles
+};
+
+// U words of type Word at the offsets at[u] of beam 0 (negative: none), for all moves of an item.
+template <class Word, int BEAMS, int U>
+__device__ __forceinline__ void move_words(unsigned char* base, const int64_t (&at)[U], int n, const int64_t* to,
+                                           const int64_t* from) {
+    Word v[U][BEAMS];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < BEAMS; ++i)
+            if (i < n && at[u] >= 0) v[u][i] = *reinterpret_cast<const Word*>(base + at[u] + from[i]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < BEAMS; ++i)
+            if (i < n && at[u] >= 0) *reinterpret_cast<Word*>(base + at[u] + to[i]) = v[u][i];
+    }
+}
+
+// BEAMS: beams at most; a tile is kReorderBlock * U words of a state (or, of what is past the segments' last words, bytes).
 template <int W, int BEAMS, int U>
-__global__ void __launch_bounds__(kReorderBlock) beam_reorder_kernel(const ReorderProblem pr) {
+__global__ void __launch_bounds__(kReorderBlock, kReorderCtas<BEAMS, W>) beam_reorder_kernel(const ReorderProblem pr) {
     using Word = typename WordOf<W>::type;
-    __shared__ int move_to[BEAMS], move_from[BEAMS];
-    __shared__ int moves;
-    const int t = threadIdx.x;
+    constexpr int kTile = kReorderBlock * U, kItems = kReorderItems<BEAMS>;
+    __shared__ Moves<BEAMS> sh;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     allow_dependents();
     grid_dependency_wait();
-    for (int64_t item = blockIdx.y; item < pr.items; item += gridDim.y) {
+    for (int64_t item0 = 0; item0 < pr.items; item0 += kItems) {
+        const int items = pr.items - item0 < kItems ? static_cast<int>(pr.items - item0) : kItems;
         __syncthreads();
-        if (t < 32) {
-            // the beams that move, in order
+        for (int q = warp; q < 32; q += kReorderBlock / 32) {
+            // the beams of an item that move, in order
             int n = 0;
-            for (int j0 = 0; j0 < pr.beams; j0 += 32) {
-                const int j = j0 + t;
-                int64_t p = j < pr.beams ? pr.parents[item * pr.beams + j] : -1;
+            for (int j0 = 0; j0 < pr.beams && q < items; j0 += 32) {
+                const int j = j0 + lane;
+                const int64_t p = j < pr.beams ? pr.parents[(item0 + q) * pr.beams + j] : -1;
                 const bool in = p >= 0 && p < pr.beams && p != j;
                 const unsigned all = __ballot_sync(0xffffffffu, in);
                 if (in) {
-                    const int at = n + __popc(all & ((1u << t) - 1u));
-                    move_to[at] = j;
-                    move_from[at] = static_cast<int>(p);
+                    const int at = n + __popc(all & ((1u << lane) - 1u));
+                    sh.to[q][at] = j * pr.beam_stride;
+                    sh.from[q][at] = p * pr.beam_stride;
                 }
                 n += __popc(all);
             }
-            if (t == 0) moves = n;
+            if (lane == 0) {
+                int64_t live = pr.positions;
+                if (pr.lengths && q < items) {
+                    const int64_t len = pr.lengths[item0 + q];
+                    live = len < 0 ? 0 : len < live ? len : live;
+                }
+                const int64_t bytes = live * pr.pos_bytes, words = bytes / W, rest = bytes - words * W;
+                sh.n[q] = n;
+                sh.bytes[q] = bytes;
+                sh.end[q] = n ? ((words * pr.outer + kTile - 1) / kTile + (rest * pr.outer + kTile - 1) / kTile) * pr.n : 0;
+            }
         }
         __syncthreads();
-        const int n = moves;
-        if (n == 0) continue;
-        int64_t live = pr.positions;
-        if (pr.lengths) {
-            const int64_t len = pr.lengths[item];
-            live = len < 0 ? 0 : len < live ? len : live;
+        if (warp == 0) {
+            int64_t end = sh.end[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t d = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += d;
+            }
+            sh.end[lane] = end;
         }
-        const int64_t bytes = live * pr.pos_bytes, words = bytes / W;
-        const int rest = static_cast<int>(bytes - words * W);  // past the last word, byte by byte
-        const int64_t per_tile = static_cast<int64_t>(kReorderBlock) * U;
-        const int64_t chunks = (words + per_tile - 1) / per_tile + (rest > 0);
-        const int64_t tiles = chunks * pr.outer * pr.n;
-        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-            const int64_t seg = tile / chunks, chunk = tile - seg * chunks;
-            const int64_t state = seg / pr.outer, o = seg - state * pr.outer;
-            unsigned char* base = pr.states[state] + item * pr.item_stride + o * pr.outer_stride;
-            if (rest > 0 && chunk == chunks - 1) {
-                if (t < rest) {
-                    unsigned char* p = base + words * W + t;
-                    unsigned char v[BEAMS];
+        __syncthreads();
+        int q = 0;
+        for (int64_t tile = blockIdx.x; tile < sh.end[31]; tile += gridDim.x) {
+            while (tile >= sh.end[q]) ++q;
+            const int64_t bytes = sh.bytes[q], words = bytes / W, rest = bytes - words * W;
+            const int64_t word_tiles = (words * pr.outer + kTile - 1) / kTile;
+            const int64_t tiles = word_tiles + (rest * pr.outer + kTile - 1) / kTile;
+            int64_t in_state;
+            const int64_t state = divide(tile - (q ? sh.end[q - 1] : 0), tiles, &in_state);
+            unsigned char* base = pr.states[state] + (item0 + q) * pr.item_stride;
+            int64_t at[U];
+            if (in_state < word_tiles) {
+                // the tile's first word, and from it on: one division a tile where segments are longer than tiles
+                int64_t first = in_state * kTile, o0 = 0;
+                const int64_t left = words * pr.outer - first;
+                if (pr.outer > 1) o0 = divide(first, words, &first);
 #pragma unroll
-                    for (int i = 0; i < BEAMS; ++i)
-                        if (i < n) v[i] = p[move_from[i] * pr.beam_stride];
-#pragma unroll
-                    for (int i = 0; i < BEAMS; ++i)
-                        if (i < n) p[move_to[i] * pr.beam_stride] = v[i];
+                for (int u = 0; u < U; ++u) {
+                    int64_t w = first + (u * kReorderBlock + t), o = o0;
+                    if (w >= words) {
+                        if (words >= kTile) {
+                            w -= words;
+                            ++o;
+                        } else {
+                            o += divide(w, words, &w);
+                        }
+                    }
+                    at[u] = u * kReorderBlock + t < left ? o * pr.outer_stride + w * W : -1;
                 }
-                continue;
-            }
-            const int64_t w0 = chunk * per_tile + t;
-            Word v[U][BEAMS];
+                move_words<Word, BEAMS, U>(base, at, sh.n[q], sh.to[q], sh.from[q]);
+            } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (w0 + u * kReorderBlock >= words) break;
-                const unsigned char* p = base + (w0 + u * kReorderBlock) * W;
-#pragma unroll
-                for (int i = 0; i < BEAMS; ++i)
-                    if (i < n) v[u][i] = *reinterpret_cast<const Word*>(p + move_from[i] * pr.beam_stride);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (w0 + u * kReorderBlock >= words) break;
-                unsigned char* p = base + (w0 + u * kReorderBlock) * W;
-#pragma unroll
-                for (int i = 0; i < BEAMS; ++i)
-                    if (i < n) *reinterpret_cast<Word*>(p + move_to[i] * pr.beam_stride) = v[u][i];
+                for (int u = 0; u < U; ++u) {
+                    const int64_t b = (in_state - word_tiles) * kTile + u * kReorderBlock + t;
+                    at[u] = -1;
+                    if (b < rest * pr.outer) {
+                        int64_t in_segment;
+                        const int64_t o = divide(b, rest, &in_segment);
+                        at[u] = o * pr.outer_stride + words * W + in_segment;
+                    }
+                }
+                move_words<uint8_t, BEAMS, U>(base, at, sh.n[q], sh.to[q], sh.from[q]);
             }
         }
     }
@@ -104,24 +166,24 @@ __global__ void __launch_bounds__(kReorderBlock) beam_reorder_kernel(const Reord
 
 template <int W, int BEAMS, int U>
 cudaError_t launch_reorder_n(const ReorderProblem& pr, const argr_caps& caps) {
-    // about eight CTAs per SM; past that the tiles come in turns
-    const int64_t per_tile = static_cast<int64_t>(kReorderBlock) * U;
-    const int64_t words = pr.positions * pr.pos_bytes / W;
-    const int64_t tiles = ((words + per_tile - 1) / per_tile + 1) * pr.outer * pr.n;
-    const int64_t items = pr.items < 65535 ? pr.items : 65535;
-    int64_t x = (32 * static_cast<int64_t>(caps.sm_count) + items - 1) / items;
-    x = x < tiles ? x : tiles;
+    auto kern = beam_reorder_kernel<W, BEAMS, U>;
+    int per_sm = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kReorderBlock, 0);
+    if (e != cudaSuccess) return e;
+    const int64_t most = static_cast<int64_t>(per_sm > 0 ? per_sm : 1) * caps.sm_count;
+    // tiles, at most: every position of every item
+    const double tiles = (static_cast<double>(pr.positions) * pr.pos_bytes * pr.outer / (W * kReorderBlock * U) + 2) * pr.n * pr.items;
     argr_plan p = {};
     p.flags = ARGR_PLAN_PDL;
-    return launch_ex_smem(beam_reorder_kernel<W, BEAMS, U>, dim3(static_cast<unsigned>(x), static_cast<unsigned>(items)),
-                          dim3(kReorderBlock), 1, 0, p, pr.stream, pr);
+    return launch_ex_smem(kern, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kReorderBlock), 1, 0, p,
+                          pr.stream, pr);
 }
 
-// Words of all moving beams stay in registers: 64 beams of 16-byte words are 256 of them, so narrower
+// Words of all moving beams stay in registers, at most 64 of them (128 for 32 beams of 16 bytes), hence narrower
 // words from 33 beams on.
 template <int W>
 cudaError_t launch_reorder_w(const ReorderProblem& pr, const argr_caps& caps) {
-    if (pr.beams <= 4) return launch_reorder_n<W, 4, 4>(pr, caps);
+    if (pr.beams <= 4) return launch_reorder_n<W, 4, 2>(pr, caps);
     if (pr.beams <= 8) return launch_reorder_n<W, 8, 2>(pr, caps);
     if (pr.beams <= 16) return launch_reorder_n<W, 16, 1>(pr, caps);
     if (pr.beams <= 32) return launch_reorder_n<W, 32, 1>(pr, caps);

@@ -27,8 +27,6 @@
 
 namespace argr {
 
-constexpr int kRouteWarps = kRouteBlock / 32;
-
 // order32() of an element that can be chosen, 0 for -inf, NaN and what is past the row.
 __device__ __forceinline__ unsigned choice_key(float x) { return x > neg_inf() ? order32(x) : 0u; }
 
@@ -112,24 +110,24 @@ struct WarpShare {
 
 // Shared memory of the forward kernel: the CTA's choices and rows [E + 1], its sums of p [E]; per warp the rows' maxima and
 // sums, the heads of their blocks, from which element on a block's elements equal to its head are left, and
-// their choices (weights, then ids); at the end half the warps' sums.
+// their choices (weights, then ids); at the end the warps' sums.
 template <int G, int V>
 struct RouteLayout {
     static constexpr int BLOCKS = G * V / 8;                          // of a row
     static constexpr int ROWS = BLOCKS <= 32 ? 32 : 1024 / BLOCKS;    // of a batch
     static constexpr int PITCH = ROWS + 1;                            // of a block's heads: lanes and blocks in different banks
-    size_t hist, acc, half, warp, sums, heads, after, weights, ids, each, total;
+    size_t hist, acc, warp, sums, heads, after, weights, ids, each, total;
     __host__ __device__ RouteLayout(int E, int k) {
         hist = 0;
         acc = 4 * static_cast<size_t>((E + 1 + 3) / 4 * 4);
-        half = warp = acc + 4 * static_cast<size_t>((E + 3) / 4 * 4);
+        warp = acc + 4 * static_cast<size_t>((E + 3) / 4 * 4);
         sums = 0;  // (in a warp's part)
         heads = 8 * ROWS;
         after = heads + 4 * static_cast<size_t>(BLOCKS) * PITCH;
         weights = (after + static_cast<size_t>(BLOCKS) * PITCH + 15) / 16 * 16;
         ids = weights + 4 * static_cast<size_t>(ROWS) * k;
         each = (ids + 4 * static_cast<size_t>(ROWS) * k + 15) / 16 * 16;
-        const size_t a = kRouteWarps * each, b = 4 * static_cast<size_t>(kRouteWarps / 2) * G * V;
+        const size_t a = kRouteWarps * each, b = 4 * static_cast<size_t>(kRouteWarps) * G * V;
         total = warp + (a > b ? a : b);
     }
 };
@@ -314,32 +312,21 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
     if (!pr.counts) return;
     if (taken) atomicAdd(&hist[E], taken);
     if (pr.balance) {
-        // over the warp's rows, then half of the warps hand theirs to the other half
-        float* half = reinterpret_cast<float*>(dyn + lay.half);
+        // over the warp's rows, then over the warps, in order
+        float* lanes = reinterpret_cast<float*>(dyn + lay.warp);  // [warps][G * V]
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < V; ++j) {
 #pragma unroll
             for (int o = 16; o >= G; o >>= 1) sum_p[j] += __shfl_xor_sync(0xffffffffu, sum_p[j], o);
+            if (sub == 0) lanes[warp * G * V + (j / 8 * G + lg) * 8 + j % 8] = sum_p[j];
         }
         __syncthreads();
-        for (int h = kRouteWarps / 2; h >= 1; h >>= 1) {
-            if (warp >= h && warp < 2 * h && sub == 0) {
+        for (int e = threadIdx.x; e < E; e += kRouteBlock) {
+            float v = 0.0f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) half[((warp - h) * V + j) * G + lg] = sum_p[j];
-            }
-            __syncthreads();
-            if (warp < h) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) sum_p[j] += half[(warp * V + j) * G + lg];
-            }
-            __syncthreads();
-        }
-        if (warp == 0 && sub == 0) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int e = (j / 8 * G + lg) * 8 + j % 8;
-                if (e < E) acc[e] = sum_p[j];
-            }
+            for (int w = 0; w < kRouteWarps; ++w) v += lanes[w * G * V + e];
+            acc[e] = v;
         }
     }
     __syncthreads();
@@ -447,15 +434,22 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
     constexpr int U = G < 32 ? 32 / G : 1;
     const WarpShare share((pr.rows + U - 1) / U);
     const int64_t end = share.hi * U < pr.rows ? share.hi * U : pr.rows;
+    // lane q: of row q of the next pass, loaded a pass ahead. lse -inf: padding, or nothing above -inf: not read
+    float next_lse = neg_inf(), next_h = 0.0f;
+    const auto look_ahead = [&](int64_t r) {
+        const bool in = lane < RW && r + lane < end;
+        next_lse = in ? pr.lse[r + lane] : neg_inf();
+        next_h = in && pr.grad_lse ? pr.grad_lse[r + lane] : 0.0f;
+    };
+    look_ahead(share.lo * U);
     for (int64_t r0 = share.lo * U; r0 < end; r0 += RW) {
         const int rows = end - r0 < RW ? static_cast<int>(end - r0) : RW;
-        // lane q: of row q. lse -inf: padding, or nothing above -inf: not read
-        const float my_lse = lane < rows ? pr.lse[r0 + lane] : neg_inf();
-        const float my_h = lane < rows && pr.grad_lse ? pr.grad_lse[r0 + lane] : 0.0f;
+        const float my_lse = next_lse, my_h = next_h;
         const unsigned live = __ballot_sync(0xffffffffu, my_lse != neg_inf());
         LaneRow<Tag, V> raw;
         raw.clear();
         if (live >> sub & 1u) raw.load(base + (r0 + sub) * pr.row_stride, lg * V, E, wide);
+        look_ahead(r0 + RW);
         // the chosen elements: g w of each, their sums over a row, and what each gets
         float along = 0.0f;  // of row lane / LG
         if (pr.grad_weights) {
@@ -543,13 +537,6 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
     }
 }
 
-// CTAs of a problem: enough for a unit (32 / G rows) per warp, `per_sm` to an SM at most.
-inline int route_grid(int64_t rows, int unit, int per_sm, const argr_caps& caps) {
-    const int64_t each = static_cast<int64_t>(unit) * kRouteWarps;
-    const int64_t want = (rows + each - 1) / each, most = static_cast<int64_t>(per_sm) * caps.sm_count;
-    return static_cast<int>(want < most ? want : most);
-}
-
 template <class Tag, int G, int V>
 cudaError_t launch_route_gv(RouteProblem pr, const argr_caps& caps) {
     static KernelLaunchCache cache;
@@ -559,18 +546,11 @@ cudaError_t launch_route_gv(RouteProblem pr, const argr_caps& caps) {
     const size_t smem = RouteLayout<G, V>(pr.experts, pr.k).total;
     cudaError_t e = ensure_smem_limit(kern, smem + 1024, cache);  // with the static part
     if (e != cudaSuccess) return e;
-    pr.ctas = route_grid(pr.rows, 32 / G, V <= 8 ? 2 : 1, caps);
-    if (pr.ctas > kRouteMaxCtas) pr.ctas = kRouteMaxCtas;
-    // one cluster, without a second kernel, while its warps take few units each
-    int cluster = 0;
-    if (pr.counts && pr.ctas <= kRouteOneTurns * 8) {
-        cluster = 1;
-        while (cluster < 8 && cluster < pr.ctas) cluster *= 2;
-        if (cluster > caps.max_cluster) cluster = 0;
-    }
-    if (cluster) pr.ctas = cluster;
-    e = launch_ex_smem(kern, dim3(static_cast<unsigned>(pr.ctas)), dim3(kRouteBlock), cluster, smem, p, pr.stream, pr, cluster);
-    return e == cudaSuccess && pr.counts && !cluster ? launch_route_finish(pr) : e;
+    const RouteGrid grid = route_grid(pr.rows, pr.experts, pr.counts != nullptr, caps);
+    pr.ctas = grid.ctas;
+    e = launch_ex_smem(kern, dim3(static_cast<unsigned>(grid.ctas)), dim3(kRouteBlock), grid.cluster, smem, p, pr.stream, pr,
+                       grid.cluster);
+    return e == cudaSuccess && pr.counts && !grid.cluster ? launch_route_finish(pr) : e;
 }
 template <class Tag, int G, int V>
 cudaError_t launch_route_grad_gv(const RouteProblem& pr, const argr_caps& caps) {
@@ -581,20 +561,11 @@ cudaError_t launch_route_grad_gv(const RouteProblem& pr, const argr_caps& caps) 
     const size_t smem = kRouteWarps * RouteGradLayout<G, V>(pr.k).each;
     const cudaError_t e = ensure_smem_limit(kern, smem, cache);
     if (e != cudaSuccess) return e;
-    return launch_ex_smem(kern, dim3(static_cast<unsigned>(route_grid(pr.rows, 32 / G, V <= 8 ? 2 : 1, caps))),
-                          dim3(kRouteBlock), 1, smem, p, pr.stream, pr);
+    const int64_t each = 32 / G * kRouteWarps, want = (pr.rows + each - 1) / each, most = (V <= 8 ? 2 : 1) * caps.sm_count;
+    return launch_ex_smem(kern, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kRouteBlock), 1, smem, p,
+                          pr.stream, pr);
 }
 
-// Rows of 8 lanes for 33 to 256 experts, then more lanes, as the sums of p take a register per element of a lane.
-#define ARGR_ROUTE_FORWARD_GV(fn, Tag, pr, caps)        \
-    ((pr).experts <= 8     ? fn<Tag, 1, 8>(pr, caps)    \
-     : (pr).experts <= 16  ? fn<Tag, 2, 8>(pr, caps)    \
-     : (pr).experts <= 32  ? fn<Tag, 4, 8>(pr, caps)    \
-     : (pr).experts <= 64  ? fn<Tag, 8, 8>(pr, caps)    \
-     : (pr).experts <= 128 ? fn<Tag, 8, 16>(pr, caps)   \
-     : (pr).experts <= 256 ? fn<Tag, 8, 32>(pr, caps)   \
-     : (pr).experts <= 512 ? fn<Tag, 16, 32>(pr, caps)  \
-                           : fn<Tag, 32, 32>(pr, caps))
 #define ARGR_ROUTE_GV(fn, Tag, pr, caps)                \
     ((pr).experts <= 8     ? fn<Tag, 1, 8>(pr, caps)    \
      : (pr).experts <= 16  ? fn<Tag, 2, 8>(pr, caps)    \
@@ -607,7 +578,18 @@ cudaError_t launch_route_grad_gv(const RouteProblem& pr, const argr_caps& caps) 
 
 template <class Tag>
 cudaError_t launch_route_t(const RouteProblem& pr, const argr_caps& caps) {
-    return ARGR_ROUTE_FORWARD_GV(launch_route_gv, Tag, pr, caps);
+    const RouteShape s = route_shape(pr.experts);
+    switch (s.lanes) {
+        case 1: return launch_route_gv<Tag, 1, 8>(pr, caps);
+        case 2: return launch_route_gv<Tag, 2, 8>(pr, caps);
+        case 4: return launch_route_gv<Tag, 4, 8>(pr, caps);
+        case 8:
+            return s.elems == 8    ? launch_route_gv<Tag, 8, 8>(pr, caps)
+                   : s.elems == 16 ? launch_route_gv<Tag, 8, 16>(pr, caps)
+                                   : launch_route_gv<Tag, 8, 32>(pr, caps);
+        case 16: return launch_route_gv<Tag, 16, 32>(pr, caps);
+        default: return launch_route_gv<Tag, 32, 32>(pr, caps);
+    }
 }
 template <class Tag>
 cudaError_t launch_route_grad_t(const RouteProblem& pr, const argr_caps& caps) {

@@ -65,8 +65,38 @@ struct RouteProblem {
 };
 
 constexpr int kRouteBlock = 512;
+constexpr int kRouteWarps = kRouteBlock / 32;
 constexpr int kRouteMaxCtas = 512;  // CTAs that leave partial sums, at most
-constexpr int kRouteOneTurns = 2;   // turns of one cluster's CTAs over the rows, at most
+constexpr int kRouteOneTurns = 2;   // units of a warp where one cluster does it all, at most
+
+// How the forward kernel takes rows of so many experts: `lanes` to a row, `elems` elements to a lane. Rows of 8 lanes
+// for 33 to 256 experts, then more lanes, as the sums of p take a register per element of a lane.
+struct RouteShape {
+    int lanes, elems;
+};
+inline RouteShape route_shape(int64_t experts) {
+    if (experts <= 32) return {experts <= 8 ? 1 : experts <= 16 ? 2 : 4, 8};
+    if (experts <= 256) return {8, experts <= 64 ? 8 : experts <= 128 ? 16 : 32};
+    return {experts <= 512 ? 16 : 32, 32};
+}
+// The grid of the forward kernel: a unit (32 / lanes rows) per warp, up to two CTAs per SM (one where a lane's elements
+// take the registers). cluster: the CTAs are one cluster that joins its sums itself (counts alone need
+// that), while its warps take few units each; 0: they leave them in scratch.
+struct RouteGrid {
+    int ctas, cluster;
+};
+inline RouteGrid route_grid(int64_t rows, int64_t experts, bool counts, const argr_caps& caps) {
+    const RouteShape s = route_shape(experts);
+    const int64_t each = static_cast<int64_t>(32 / s.lanes) * kRouteWarps, want = (rows + each - 1) / each;
+    if (counts && want <= 8 * kRouteOneTurns) {
+        int c = 1;
+        while (c < 8 && c < want) c *= 2;
+        if (c <= caps.max_cluster) return {c, c};
+    }
+    int64_t most = static_cast<int64_t>(s.elems <= 8 ? 2 : 1) * caps.sm_count;
+    if (most > kRouteMaxCtas) most = kRouteMaxCtas;
+    return {static_cast<int>(want < most ? want : most), 0};
+}
 
 #ifdef __CUDACC__
 // The balance loss from sum_e counts_e (sum over the rows of p_e).

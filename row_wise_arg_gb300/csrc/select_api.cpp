@@ -65,14 +65,11 @@ argr_status check_route(const void* x, int dtype, int64_t rows, int64_t experts,
     return ARGR_OK;
 }
 
-// CTAs that leave sums and counts in a route's scratch, at most: two per SM (route.cuh), and a row to each.
-int64_t route_parts(int64_t rows, const argr_caps& caps) {
-    return std::min<int64_t>(rows, std::min<int64_t>(2 * static_cast<int64_t>(caps.sm_count), kRouteMaxCtas));
-}
-// Scratch of a route: the CTAs' sums, then their counts.
-size_t route_sums_bytes(int64_t parts, int64_t experts) { return align_up(4 * static_cast<size_t>(parts) * experts, 16); }
-size_t route_bytes(int64_t parts, int64_t experts) {
-    return route_sums_bytes(parts, experts) + 4 * static_cast<size_t>(parts) * (experts + 1);
+// Scratch of a route whose CTAs leave their sums and counts: the sums, then the counts.
+size_t route_sums_bytes(int64_t ctas, int64_t experts) { return align_up(4 * static_cast<size_t>(ctas) * experts, 16); }
+size_t route_scratch(int64_t rows, int64_t experts, const argr_caps& caps) {
+    const RouteGrid g = route_grid(rows, experts, true, caps);
+    return g.cluster ? 0 : route_sums_bytes(g.ctas, experts) + 4 * static_cast<size_t>(g.ctas) * (experts + 1);
 }
 
 }  // namespace
@@ -191,7 +188,7 @@ argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_
 size_t argreduce_route_scratch_bytes(int64_t rows, int64_t experts) {
     argr_caps caps;
     if (rows < 1 || experts < 1 || experts > ARGR_ROUTE_MAX_EXPERTS || current_caps(&caps) != ARGR_OK) return 0;
-    return route_bytes(route_parts(rows, caps), experts);
+    return route_scratch(rows, experts, caps);
 }
 
 argr_status argreduce_route(const void* x, argr_dtype dtype, int64_t rows, int64_t experts, int64_t row_stride,
@@ -224,11 +221,11 @@ argr_status argreduce_route(const void* x, argr_dtype dtype, int64_t rows, int64
     pr.taken = taken;
     pr.balance = balance;
     pr.stream = reinterpret_cast<cudaStream_t>(stream);
-    if (counts && rows > 0) {
-        const int64_t parts = route_parts(rows, caps);
-        if (!scratch || misaligned(scratch, 16) || scratch_bytes < route_bytes(parts, experts)) return ARGR_ESCRATCH;
+    if (const size_t need = counts && rows > 0 ? route_scratch(rows, experts, caps) : 0) {
+        if (!scratch || misaligned(scratch, 16) || scratch_bytes < need) return ARGR_ESCRATCH;
         pr.part_sums = static_cast<float*>(scratch);
-        pr.part_counts = reinterpret_cast<int*>(static_cast<char*>(scratch) + route_sums_bytes(parts, experts));
+        pr.part_counts = reinterpret_cast<int*>(static_cast<char*>(scratch) +
+                                                route_sums_bytes(route_grid(rows, experts, true, caps).ctas, experts));
     }
     if (rows == 0) return launched(launch_route_finish(pr));
     return ARGR_SELECT_DISPATCH(launch_route, dtype, pr, caps);

@@ -76,6 +76,8 @@ def _rows(x, dtype):
         return shape[0], cols, stride[0] if shape[0] > 1 else cols, code
     if n == 1:
         return 1, cols, cols, code
+    if n == 3 and stride[0] == shape[1] * stride[1] and shape[1] > 1:  # evenly spaced, without a view
+        return shape[0] * shape[1], cols, stride[1], code
     try:
         x = x.view(-1, cols)
     except RuntimeError:

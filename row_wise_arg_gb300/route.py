@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib, _stream_ptr
-from ._lib import ARGR_OK, ArgreduceError
+from ._lib import ARGR_ESCRATCH, ARGR_OK, ArgreduceError
 from .logits import _arg, _grad_out, _rows, _side, _under
 
 _LIB = _lib.load()  # looked up once: these calls are short
@@ -47,22 +47,21 @@ def _forward(x, top_k, valid, normalize, counts, balance, dtype):
     weights = _empty((*lead, top_k), dtype=_F32, device=dev)
     ids = _empty((*lead, top_k), dtype=_I64, device=dev)
     lse = _empty(lead, dtype=_F32, device=dev)
-    n = taken = loss = p_n = p_taken = p_loss = p_scratch = None
-    nbytes = 0
+    n = taken = loss = p_n = p_taken = p_loss = None
     if counts or balance:
         n, taken = _empty(experts, dtype=_I64, device=dev), _empty((), dtype=_I64, device=dev)
         p_n, p_taken = n.data_ptr(), taken.data_ptr()
         if balance:
             loss = _empty((), dtype=_F32, device=dev)
             p_loss = loss.data_ptr()
-        # this call's own: torch keeps it from others until the stream has passed the call
+    args = (x.data_ptr(), code, rows, experts, stride, top_k, bool(normalize), p_valid, weights.data_ptr(), ids.data_ptr(),
+            lse.data_ptr(), p_n, p_taken, p_loss)
+    handle = _stream_ptr(None, dev.index) or None
+    st = _LIB.argreduce_route(*args, None, 0, handle)
+    if st == ARGR_ESCRATCH:  # many rows; the scratch is this call's own: torch keeps it until the stream has passed the call
         nbytes = _LIB.argreduce_route_scratch_bytes(rows, experts)
-        if nbytes:
-            scratch = _empty(nbytes, dtype=torch.uint8, device=dev)
-            p_scratch = scratch.data_ptr()
-    st = _LIB.argreduce_route(x.data_ptr(), code, rows, experts, stride, top_k, bool(normalize), p_valid,
-                              weights.data_ptr(), ids.data_ptr(), lse.data_ptr(), p_n, p_taken, p_loss, p_scratch, nbytes,
-                              _stream_ptr(None, dev.index) or None)
+        scratch = _empty(nbytes, dtype=torch.uint8, device=dev)
+        st = _LIB.argreduce_route(*args, scratch.data_ptr(), nbytes, handle)
     if st != ARGR_OK:
         raise ArgreduceError(st, "argreduce_route")
     return weights, ids, lse, n, taken, loss
