@@ -11,7 +11,7 @@
 // in 64 bits (a handful of operations per list entry; the 64-bit unit is slow), S is the
 // binary32 sum of the pass.
 //
-// Few rows: one cluster per item, `groups` beams at a time, `ranks` CTAs to a beam. Every CTA hands
+// Few rows: one cluster per item, `ranks` CTAs to a beam. Every CTA hands
 // its sums and its list to CTA 0 through distributed shared memory, which merges: no
 // scratch, one launch. Many rows: a CTA per row, or the persistent kernel of long rows
 // (logits_stream.cuh), leaves lists and sums in scratch, and a second kernel merges them.
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) beam_select_kernel(const BeamPr
     __shared__ MergeShared merge;
     const int t = threadIdx.x;
     const int cta = static_cast<int>(blockIdx.x % cluster), ranks = 1 << shift, rank = cta & (ranks - 1);
-    const int first = cta >> shift, groups = cluster >> shift;
+    const int b = cta >> shift;
     const int64_t item = blockIdx.x / cluster;
     const int k = pr.rows.top_k;
     const BeamLayout lay(k, pr.beams << shift, seg_slots, kGroupElems<Tag>);
@@ -335,30 +335,27 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) beam_select_kernel(const BeamPr
     float2* sums = reinterpret_cast<float2*>(dyn + lay.sums);
     allow_dependents();
     if (cluster > 1) cluster_ready();
-    prefetch_part<Tag>(pr.rows, item * pr.beams + first, rank, ranks);
+    const int64_t r = item * pr.beams + b;
+    prefetch_part<Tag>(pr.rows, r, rank, ranks);
     grid_dependency_wait();
     if (cta == 0) load_beams(pr, item, merge);
     if (cluster > 1) cluster_wait();
     const unsigned to_lists = cluster > 1 ? cluster_addr(smem_u32(gathered), 0) : 0;
     const unsigned to_sums = cluster > 1 ? cluster_addr(smem_u32(sums), 0) : 0;
-    for (int b = first; b < pr.beams; b += groups) {
-        const int64_t r = item * pr.beams + b;
-        if (!beam_looks(pr.rows, r)) continue;  // (alike in every thread)
+    if (beam_looks(pr.rows, r)) {  // (alike in every thread)
         const R* row = static_cast<const R*>(pr.rows.x) + r * pr.rows.row_stride;
         SoftSum c;
         const int have = scan_beam<Tag>(row, Part<Tag>(row, pr.rows.cols, rank, ranks), k, scale2, sh, red, c);
-        const int l = (b << shift) + rank;
         if (cluster > 1) {
             if (t == 0) {
-                st_cluster(to_sums + 8 * l, c.m);
-                st_cluster(to_sums + 8 * l + 4, c.s);
+                st_cluster(to_sums + 8 * cta, c.m);
+                st_cluster(to_sums + 8 * cta + 4, c.s);
             }
-            for (int i = t; i < k; i += blockDim.x) st_cluster(to_lists + 8 * (l * k + i), i < have ? sh.best[i] : 0ull);
+            for (int i = t; i < k; i += blockDim.x) st_cluster(to_lists + 8 * (cta * k + i), i < have ? sh.best[i] : 0ull);
         } else {
-            if (t == 0) sums[l] = make_float2(c.m, c.s);
-            for (int i = t; i < k; i += blockDim.x) gathered[l * k + i] = i < have ? sh.best[i] : 0ull;
+            if (t == 0) sums[0] = make_float2(c.m, c.s);
+            for (int i = t; i < k; i += blockDim.x) gathered[i] = i < have ? sh.best[i] : 0ull;
         }
-        __syncthreads();  // `red` and the best have been read
     }
     if (cluster > 1) {
         cluster_arrive();
@@ -395,13 +392,14 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) beam_rows_kernel(const LogitsPr
 // (one instance, in select_f32.cu)
 cudaError_t launch_beam_merge(const BeamProblem& pr);
 
-// The plan of a step: one cluster of 1 << shift CTAs to a beam per item, or (cluster == 0) rows and merge.
+// The plan of a step: one cluster per item, 1 << shift CTAs to a beam, or (cluster == 0) rows and merge.
 struct BeamPlan {
     int cluster, shift, block;
     bool stream;
 };
 
-// Whether rows go to the persistent kernel, and its plan.
+// Whether rows go to the persistent kernel, and its plan: those that the planner of token_logprobs streams, and last rounds
+// that three quarters of the CTAs take part in (it asks for 85%; without entropies a round is shorter).
 inline bool beam_stream_plan(int64_t rows, int64_t cols, int dtype, int k, const argr_caps& caps, argr_plan* p) {
     const int64_t ctas = 2 * static_cast<int64_t>(caps.sm_count), rounds = (rows + ctas - 1) / ctas;
     if (rows * 100 < rounds * ctas * 75) return false;
@@ -409,16 +407,24 @@ inline bool beam_stream_plan(int64_t rows, int64_t cols, int dtype, int k, const
            p->path == ARGR_PATH_LOGITS_STREAM;
 }
 
-// PLAN COMMENT
+// A cluster's CTAs start together, wait for one another, and hold their SMs while CTA 0 merges, which costs little while
+// the grid leaves room for the next one's clusters. So, for up to 16 beams: a CTA per beam, and several to a beam while
+// they are two thirds of the SMs at most and have 64 KB each. Of 4 beams with 1, 2, 4
+// CTAs each, 8 continuations, us in a graph of calls: [1, 4, 32000] f32 7.9, 8.0, 9.3; [1, 4, 202048] bf16 13.3, 10.9, 11.0;
+// [4, 4, 128000] bf16 11.0, 9.6, 10.3; [16, 4, 202048] bf16 14.8, 20.7, 26.6. Clusters of up to 8 CTAs are kept up to two
+// waves, those of 16 up to one (they find few places): cluster against a CTA per row and a merge,
+// [64, 4, 128000] bf16 17.5 / 22.3 (streaming 24.6), [60, 4, 32000] 9.8 / 11.7, [30, 8, 32000] 10.7 / 12.7, but [19, 16, 202048], 32
+// continuations, 60.6 / 53.3 (streaming 49.2), [19, 16, 32000] 25.8 / 24.6 (21.2 with 128 threads). Past that long rows are
+// streamed ([64, 16, 202048], 32: 98.6, against 107.8 with a CTA per row).
 inline BeamPlan plan_beams(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps) {
     BeamPlan p = {};
     const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32), rows = items * beams;
     const int most = caps.max_cluster < 16 ? caps.max_cluster : 16;
     int64_t per_cta = groups, n = rows;
     argr_plan q;
-    if (rows <= (beams <= 8 ? 2 : 1) * static_cast<int64_t>(caps.sm_count)) {
-        p.cluster = beams < most ? beams : most;
-        while (beams <= most && 2 * p.cluster <= most && 3 * items * p.cluster <= caps.sm_count && (groups >> (p.shift + 1)) >= 1024) {
+    if (beams <= most && rows <= (beams <= 8 ? 2 : 1) * static_cast<int64_t>(caps.sm_count)) {
+        p.cluster = beams;
+        while (2 * p.cluster <= most && 3 * items * p.cluster <= caps.sm_count && (groups >> (p.shift + 1)) >= 1024) {
             p.cluster *= 2;
             ++p.shift;
         }
@@ -427,7 +433,7 @@ inline BeamPlan plan_beams(int64_t items, int beams, int64_t cols, int dtype, in
     } else {
         p.stream = beam_stream_plan(rows, cols, dtype, k, caps, &q);
     }
-    p.block = 512;
+    p.block = p.cluster ? 512 : 256;
     if (n > caps.sm_count) {
         p.block = 256;
         while (p.block > 32 && per_cta <= 8 * p.block &&

@@ -54,9 +54,16 @@ struct LaneRow {
     static constexpr int P = 16 / static_cast<int>(sizeof(R));  // elements of 16 bytes
     uint32_t w[N * sizeof(R) / 4];
 
-    // `wide`: rows begin at 16-byte boundaries.
-    __device__ __forceinline__ void load(const R* row, int lo, int E, bool wide) {
-        if (wide && lo + N <= E) {
+    // `align`: rows begin at boundaries of so many bytes. (Eight binary32 elements come in one load where they may: in two,
+    // 32 bytes from lane to lane, they take the L1 twice as long.)
+    __device__ __forceinline__ void load(const R* row, int lo, int E, int align) {
+        if (sizeof(R) == 4 && N == 8 && align == 32 && lo + N <= E) {
+            if constexpr (sizeof(R) == 4 && N == 8)
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                             : "l"(row + lo)
+                             : "memory");
+        } else if (align >= 16 && lo + N <= E) {
 #pragma unroll
             for (int i = 0; i < N / P; ++i) {
                 const uint4 v = *reinterpret_cast<const uint4*>(row + lo + i * P);
@@ -92,6 +99,13 @@ struct LaneRow {
         }
     }
 };
+
+// The boundaries that rows begin at: 32 bytes, 16, or less (0).
+template <class R>
+__device__ __forceinline__ int rows_aligned(const void* x, int64_t stride) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(x) | static_cast<uintptr_t>(stride) * sizeof(R);
+    return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
+}
 
 // Gradient: rows of a warp at a time, one after the other, where a row takes all its lanes (by the registers of a lane and the
 // shared memory).
@@ -136,7 +150,7 @@ struct RouteLayout {
 // Of the blocks' heads the largest of every 8 are kept in registers. A block's elements are taken in order, so what is left
 // of it is what is below the element taken last, or equals it further on.
 template <class Tag, int G, int V, class Put>
-__device__ __forceinline__ void choose(const typename Tag::raw* row, int E, bool wide, float* heads, unsigned char* after, int k,
+__device__ __forceinline__ void choose(const typename Tag::raw* row, int E, int align, float* heads, unsigned char* after, int k,
                                        Put put) {
     constexpr int BLOCKS = RouteLayout<G, V>::BLOCKS, PITCH = RouteLayout<G, V>::PITCH;
     constexpr int S = BLOCKS < 8 ? BLOCKS : 8, M = BLOCKS / S;  // M sets of S blocks
@@ -166,7 +180,7 @@ __device__ __forceinline__ void choose(const typename Tag::raw* row, int E, bool
         }
         const int block = set * S + at, from = after[block * PITCH];
         LaneRow<Tag, 8> raw;
-        raw.load(row, block * 8, E, wide);
+        raw.load(row, block * 8, E, align);
         float x[8];
         raw.widen(x);
         int j = 8, again = 8;
@@ -218,7 +232,7 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
     float* weights = reinterpret_cast<float*>(part + lay.weights);  // [ROWS][k]
     int* ids = reinterpret_cast<int*>(part + lay.ids);
     const R* base = static_cast<const R*>(pr.x);
-    const bool wide = (reinterpret_cast<uintptr_t>(pr.x) | static_cast<uintptr_t>(pr.row_stride) * sizeof(R)) % 16 == 0;
+    const int align = rows_aligned<R>(pr.x, pr.row_stride);
     const WarpShare share((pr.rows + U - 1) / U);
     const int64_t end = share.hi * U < pr.rows ? share.hi * U : pr.rows;
     allow_dependents();
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
             for (int b = 0; b < B; ++b) {
                 LaneRow<Tag, 8> raw;
                 raw.clear();
-                if (on) raw.load(row, (b * G + lg) * 8, E, wide);
+                if (on) raw.load(row, (b * G + lg) * 8, E, align);
                 raw.widen(x + 8 * b);
             }
 #pragma unroll
@@ -286,7 +300,7 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
             const float m = v.x, s = v.y, ref = m == neg_inf() ? 0.0f : m;
             const bool live = s != 0.0f;  // (a NaN is live)
             float all = 0.0f;
-            choose<Tag, G, V>(base + (r0 + lane) * pr.row_stride, E, wide, heads + lane, after + lane, k, [&](int i, int e, float x) {
+            choose<Tag, G, V>(base + (r0 + lane) * pr.row_stride, E, align, heads + lane, after + lane, k, [&](int i, int e, float x) {
                 const float w = ex2((x - ref) * kLog2E);  // (0 where nothing was chosen)
                 all += w;
                 weights[lane * k + i] = w;
@@ -388,6 +402,18 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_kernel(cons
     }
 }
 
+// A lane's elements in the gradient's kernel: chunks of 16 bytes, dealt to the lanes in turns, so that a warp's loads and
+// stores are of contiguous memory. (32 contiguous bytes to a lane took 30 us for [65536, 256] f32, the L1 66% busy.)
+template <class Tag, int G>
+struct Dealt {
+    static constexpr int P = 16 / static_cast<int>(sizeof(typename Tag::raw));
+    static __device__ __forceinline__ int first(int chunk, int lg) { return (chunk * G + lg) * P; }
+    // The place of element e of a row of `elems` in shared memory: a lane reads 4 at a time, next to its neighbours'.
+    static __device__ __forceinline__ int place(int e, int elems) {
+        return P == 4 ? e : (e >> 3) * 4 + (e & 3) + (e >> 2 & 1) * (elems / 2);
+    }
+};
+
 // Shared memory of the gradient's kernel, per warp: what the chosen elements of its RW rows get, 0 elsewhere, and the
 // products of their weights and gradients [RW][k].
 template <int G, int V>
@@ -403,17 +429,31 @@ struct RouteGradLayout {
 template <class Tag, int G, int V>
 __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel(const RouteProblem pr) {
     using R = typename Tag::raw;
-    constexpr int T = kTurns<G, V>, RW = 32 / G * T, LG = 32 / RW, P = 16 / static_cast<int>(sizeof(R));
+    using D = Dealt<Tag, G>;
+    constexpr int T = kTurns<G, V>, RW = 32 / G * T, LG = 32 / RW, P = D::P, C = V / P;  // C: chunks of a lane
     extern __shared__ __align__(16) unsigned char dyn[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), sub = lane / G;
     const int E = pr.experts, k = pr.k;
     const RouteGradLayout<G, V> lay(k);
     float* at = reinterpret_cast<float*>(dyn + warp * lay.each);  // [RW][G * V]
     float* prods = reinterpret_cast<float*>(dyn + warp * lay.each + lay.prods);
+    const R* base = static_cast<const R*>(pr.x);
+    constexpr int U = G < 32 ? 32 / G : 1;
+    const WarpShare share((pr.rows + U - 1) / U);
+    const int64_t end = share.hi * U < pr.rows ? share.hi * U : pr.rows;
     allow_dependents();
     for (int i = lane; i < RW * G * V; i += 32) at[i] = 0.0f;
     grid_dependency_wait();
     __syncwarp();
+    const int align = rows_aligned<R>(pr.x, pr.row_stride), align_out = rows_aligned<R>(pr.grad, pr.grad_stride);
+    // lane q: of row q of the next pass, loaded a pass ahead. lse -inf: padding, or nothing above -inf: not read
+    float next_lse = neg_inf(), next_h = 0.0f;
+    const auto look_ahead = [&](int64_t r) {
+        const bool in = lane < RW && r + lane < end;
+        next_lse = in ? pr.lse[r + lane] : neg_inf();
+        next_h = in && pr.grad_lse ? pr.grad_lse[r + lane] : 0.0f;
+    };
+    look_ahead(share.lo * U);
     float c[V];
     {
         float per = 0.0f;
@@ -424,31 +464,23 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int e = lg * V + j;
+            const int e = D::first(j / P, lg) + j % P;
             c[j] = pr.grad_balance && e < E ? per * static_cast<float>(pr.counts[e]) : 0.0f;
         }
     }
-    const bool wide = (reinterpret_cast<uintptr_t>(pr.x) | static_cast<uintptr_t>(pr.row_stride) * sizeof(R)) % 16 == 0;
-    const bool wide_out = (reinterpret_cast<uintptr_t>(pr.grad) | static_cast<uintptr_t>(pr.grad_stride) * sizeof(R)) % 16 == 0;
-    const R* base = static_cast<const R*>(pr.x);
-    constexpr int U = G < 32 ? 32 / G : 1;
-    const WarpShare share((pr.rows + U - 1) / U);
-    const int64_t end = share.hi * U < pr.rows ? share.hi * U : pr.rows;
-    // lane q: of row q of the next pass, loaded a pass ahead. lse -inf: padding, or nothing above -inf: not read
-    float next_lse = neg_inf(), next_h = 0.0f;
-    const auto look_ahead = [&](int64_t r) {
-        const bool in = lane < RW && r + lane < end;
-        next_lse = in ? pr.lse[r + lane] : neg_inf();
-        next_h = in && pr.grad_lse ? pr.grad_lse[r + lane] : 0.0f;
+    LaneRow<Tag, P> raw[C];
+    const auto load = [&](int64_t row, bool on) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            raw[i].clear();
+            if (on) raw[i].load(base + row * pr.row_stride, D::first(i, lg), E, align);
+        }
     };
-    look_ahead(share.lo * U);
     for (int64_t r0 = share.lo * U; r0 < end; r0 += RW) {
         const int rows = end - r0 < RW ? static_cast<int>(end - r0) : RW;
         const float my_lse = next_lse, my_h = next_h;
         const unsigned live = __ballot_sync(0xffffffffu, my_lse != neg_inf());
-        LaneRow<Tag, V> raw;
-        raw.clear();
-        if (live >> sub & 1u) raw.load(base + (r0 + sub) * pr.row_stride, lg * V, E, wide);
+        load(r0 + sub, live >> sub & 1u);
         look_ahead(r0 + RW);
         // the chosen elements: g w of each, their sums over a row, and what each gets
         float along = 0.0f;  // of row lane / LG
@@ -467,7 +499,7 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
                 if (i < rows * k && (live >> q & 1u)) {
                     const int64_t e = pr.ids[r0 * k + i];
                     if (e >= 0 && e < E)
-                        at[q * G * V + e] = pr.normalize ? prods[i] - pr.weights[r0 * k + i] * a : prods[i];
+                        at[q * G * V + D::place(static_cast<int>(e), G * V)] = pr.normalize ? prods[i] - pr.weights[r0 * k + i] * a : prods[i];
                 }
             }
             __syncwarp();
@@ -477,11 +509,9 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
             const int row = G < 32 ? sub : q;
             if (G == 32 && q >= rows) break;
             float d[V];
-            raw.widen(d);
-            if (G == 32 && q + 1 < T) {
-                raw.clear();
-                if (live >> 1 >> q & 1u) raw.load(base + (r0 + q + 1) * pr.row_stride, lg * V, E, wide);
-            }
+#pragma unroll
+            for (int i = 0; i < C; ++i) raw[i].widen(d + P * i);
+            if (G == 32 && q + 1 < T) load(r0 + q + 1, live >> 1 >> q & 1u);
             const float lse = __shfl_sync(0xffffffffu, my_lse, row), h = __shfl_sync(0xffffffffu, my_h, row);
             const float a = __shfl_sync(0xffffffffu, along, row * LG);
             const bool on = live >> row & 1u;
@@ -493,13 +523,13 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
             }
             dot = pr.grad_balance ? group_sum<G>(dot) : 0.0f;
             const float rest = h - dot - (pr.normalize ? 0.0f : a);
-            float4* mine = reinterpret_cast<float4*>(at + row * G * V + lg * V);
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (pr.grad_weights && on) {
-                    v = mine[j / 4];
-                    mine[j / 4] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float4* mine = reinterpret_cast<float4*>(at + row * G * V + D::place(D::first(j / P, lg) + j % P, G * V));
+                    v = *mine;
+                    *mine = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
                 d[j] = d[j] * (c[j] + rest) + v.x;
                 d[j + 1] = d[j + 1] * (c[j + 1] + rest) + v.y;
@@ -511,26 +541,25 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
                 for (int j = 0; j < V; ++j) d[j] = 0.0f;
             }
             if (row >= rows) continue;  // (the last pass)
-            R* out = static_cast<R*>(pr.grad) + (r0 + row) * pr.grad_stride + lg * V;
-            if (wide_out && lg * V + V <= E) {
+            R* out = static_cast<R*>(pr.grad) + (r0 + row) * pr.grad_stride;
 #pragma unroll
-                for (int i = 0; i < V / P; ++i) {
+            for (int i = 0; i < C; ++i) {
+                const int e = D::first(i, lg);
+                if (align_out >= 16 && e + P <= E) {
                     uint32_t w[4];
-                    if constexpr (P == 4) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) w[u] = __float_as_uint(d[4 * i + u]);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < 4; ++u) {
+                        if constexpr (P == 4) w[u] = __float_as_uint(d[4 * i + u]);
+                        else
                             w[u] = static_cast<uint32_t>(narrow_elem<Tag>(d[8 * i + 2 * u])) |
                                    static_cast<uint32_t>(narrow_elem<Tag>(d[8 * i + 2 * u + 1])) << 16;
                     }
-                    *reinterpret_cast<uint4*>(out + i * P) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
+                    *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (lg * V + j < E) out[j] = narrow_elem<Tag>(d[j]);
+                    for (int j = 0; j < P; ++j)
+                        if (e + j < E) out[e + j] = narrow_elem<Tag>(d[P * i + j]);
+                }
             }
         }
         __syncwarp();
