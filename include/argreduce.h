@@ -536,7 +536,7 @@ argr_status argreduce_logits_plan(argr_logits_op what, int64_t rows, int64_t col
  * continuations of different beams whose totals differ by less than about 1e-6
  * may come in either order (and equal ones, where the beams' rows do not begin
  * at the same place between two 32-byte boundaries). Within a beam the order is exact.
- * 1 <= beams <= ARGR_BEAM_MAX_BEAMS, 1 <= count <= ARGR_LOGITS_MAX_TOP. Steps of many
+ * 1 <= beams <= ARGR_BEAM_MAX_BEAMS, items < 2^25, 1 <= count <= ARGR_LOGITS_MAX_TOP. Steps of many
  * rows need scratch (argreduce_beam_scratch_bytes(), 0 for the others; 16-byte aligned, no
  * preparation), which belongs to the call until it has finished on the stream. Errors as
  * for argreduce_logprobs(); ARGR_ESCRATCH.
@@ -560,12 +560,17 @@ size_t argreduce_beam_scratch_bytes(int64_t items, int32_t beams, int64_t cols, 
  *   - Several beams may have the same parent, and beams may exchange places.
  * No state may overlap itself (its dimensions have to nest: no stride smaller than what lies within it),
  * another one, parents or lengths: ARGR_EINVAL. At most ARGR_REORDER_MAX_STATES of them.
+ * argreduce_beam_reorder_check() makes these checks alone, before the first of several calls.
  */
 #define ARGR_REORDER_MAX_STATES 1024
 argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_t items, int32_t beams,
                                    int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
                                    int64_t positions, int64_t position_bytes, const int64_t* parents,
                                    const int64_t* lengths, argr_stream stream);
+argr_status argreduce_beam_reorder_check(void* const* states, int32_t n_states, int64_t items, int32_t beams,
+                                         int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
+                                         int64_t positions, int64_t position_bytes, const int64_t* parents,
+                                         const int64_t* lengths);
 
 /*
  * A router's choice of experts. x is [rows, experts] logits (types, strides and

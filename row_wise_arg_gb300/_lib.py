@@ -55,7 +55,7 @@ EXPORTS = (
     "argreduce_cum_with_plan", "argreduce_cum_scratch_bytes", "argreduce_plan_check",
     "argreduce_logprobs", "argreduce_logprobs_backward", "argreduce_distill", "argreduce_distill_backward",
     "argreduce_distill_step", "argreduce_logits_plan", "argreduce_beam_select", "argreduce_beam_scratch_bytes",
-    "argreduce_beam_reorder",
+    "argreduce_beam_reorder", "argreduce_beam_reorder_check",
     "argreduce_route", "argreduce_route_backward", "argreduce_route_scratch_bytes",
 )
 
@@ -158,8 +158,9 @@ def load() -> ctypes.CDLL:
         lib.argreduce_beam_reorder.argtypes = [vp, i32, i64, i32, i64, i64, i64, i64, i64, i64, vp, vp, vp]
         lib.argreduce_route.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         lib.argreduce_route_backward.argtypes = [vp, i32, i64, i64, i64, i32, i32] + [vp] * 9 + [i64, vp]
-        for f in (lib.argreduce_beam_select, lib.argreduce_beam_reorder, lib.argreduce_route,
-                  lib.argreduce_route_backward):
+        lib.argreduce_beam_reorder_check.argtypes = [vp, i32, i64, i32, i64, i64, i64, i64, i64, i64, vp, vp]
+        for f in (lib.argreduce_beam_select, lib.argreduce_beam_reorder, lib.argreduce_beam_reorder_check,
+                  lib.argreduce_route, lib.argreduce_route_backward):
             f.restype = i32
         lib.argreduce_route_scratch_bytes.argtypes = [i64, i64]
         lib.argreduce_route_scratch_bytes.restype = sz

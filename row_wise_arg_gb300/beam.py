@@ -16,7 +16,7 @@ import torch
 from torch.autograd import forward_ad
 
 from . import _lib, _stream_ptr
-from ._lib import ARGR_ESCRATCH, ARGR_OK, ArgreduceError
+from ._lib import ARGR_OK, ArgreduceError
 from .logits import _arg, _current_device, _rows, _side, _under
 
 _LIB = _lib.load()  # looked up once: these calls are short
@@ -77,11 +77,10 @@ def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, s
             _arg(ended, "ended", _BOOL, lead, dev), end_token, _arg(scale, "scale", _F32, lead, dev), count,
             tokens.data_ptr(), parents.data_ptr(), totals.data_ptr())
     handle = _stream_ptr(None, dev.index) or None
-    st = _LIB.argreduce_beam_select(*args, None, 0, handle)
-    if st == ARGR_ESCRATCH:  # many rows; the scratch is this call's own: torch keeps it until the stream has passed the call
-        nbytes = _LIB.argreduce_beam_scratch_bytes(rows // beams, beams, cols, code, count)
-        scratch = _empty(nbytes, dtype=torch.uint8, device=dev)
-        st = _LIB.argreduce_beam_select(*args, scratch.data_ptr(), nbytes, handle)
+    # many rows need scratch; it is this call's own: torch keeps it until the stream has passed the call
+    nbytes = _LIB.argreduce_beam_scratch_bytes(rows // beams, beams, cols, code, count) if rows > 16 else 0
+    scratch = _empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    st = _LIB.argreduce_beam_select(*args, scratch.data_ptr() if nbytes else None, nbytes, handle)
     if st != ARGR_OK:
         raise ArgreduceError(st, "argreduce_beam_select")
     return BeamSelection(tokens, parents, totals)
@@ -120,6 +119,8 @@ def _geometry(t, items, beams, dim):
         while at > lead and (shape[at - 1] == 1 or stride[at - 1] == size):
             size *= shape[at - 1]
             at -= 1
+    if t.numel() == 0:
+        return (0, 0, 0, 0, 0, es)
     inner = _even(shape[at + (dim is not None):], stride[at + (dim is not None):])
     outer = _even(shape[lead:at], stride[lead:at])
     if inner is None or outer is None or (inner[0] > 1 and inner[1] != 1):
@@ -145,6 +146,11 @@ def _apart(a, ga, b, gb, items, beams):
         return False
     na, nb = _span(ga, 1, 1), _span(gb, 1, 1)
     return (b - a) % row >= na and (b - a) % row + nb <= row
+
+
+def _reordered(st):
+    if st != ARGR_OK:
+        raise ArgreduceError(st, "argreduce_beam_reorder (do states overlap, themselves or one another?)")
 
 
 def beam_reorder(states, parents, lengths=None, *, dim: Optional[int] = None, stream=None):
@@ -188,7 +194,7 @@ def beam_reorder(states, parents, lengths=None, *, dim: Optional[int] = None, st
             g = _geometry(t, items, beams, dim if lengths is not None else None)
             if lengths is None and dim is not None:
                 _geometry(t, items, beams, dim)  # refuses what it would refuse with lengths
-            pointers = plans.setdefault(g, []) if t.numel() else []
+            pointers = plans.setdefault(g, []) if t.numel() else []  # (nothing moves in an empty one)
         if t.device != dev:
             raise ValueError(f"states must be on {dev}, got one on {t.device}")
         if tangents and forward_ad.unpack_dual(t).tangent is not None:
@@ -196,22 +202,25 @@ def beam_reorder(states, parents, lengths=None, *, dim: Optional[int] = None, st
         pointers.append(t.data_ptr())
     if items == 0 or not plans:
         return states
-    if len(plans) > 1:
-        spans = sorted((p, g) for g, pointers in plans.items() for p in pointers)
-        for i, (p, g) in enumerate(spans):
-            for q, h in spans[i + 1:]:
-                if q >= p + max(_span(k, items, beams) for k in plans):
-                    break
-                if h != g and not _apart(p, g, q, h, items, beams):
-                    raise ValueError("states must not overlap")
-    handle = _stream_ptr(None, dev.index) or None
+    calls = []
     for g, pointers in plans.items():
         if len(pointers) > _lib.REORDER_MAX_STATES:
             raise ValueError(f"at most {_lib.REORDER_MAX_STATES} states of a kind, got {len(pointers)}")
-        st = _LIB.argreduce_beam_reorder((ctypes.c_void_p * len(pointers))(*pointers), len(pointers), items, beams, *g,
-                                         p_parents, p_lengths, handle)
-        if st != ARGR_OK:
-            raise ArgreduceError(st, "argreduce_beam_reorder (do states overlap, themselves or one another?)")
+        calls.append(((ctypes.c_void_p * len(pointers))(*pointers), len(pointers), items, beams, *g, p_parents, p_lengths))
+    if len(calls) > 1:  # every check before the first launch
+        spans = sorted((p, g) for g, pointers in plans.items() for p in pointers)
+        longest = max(_span(g, items, beams) for g in plans)
+        for i, (p, g) in enumerate(spans):
+            for q, h in spans[i + 1:]:
+                if q >= p + longest:
+                    break
+                if h != g and not _apart(p, g, q, h, items, beams):
+                    raise ValueError("states must not overlap")
+        for call in calls:
+            _reordered(_LIB.argreduce_beam_reorder_check(*call))
+    handle = _stream_ptr(None, dev.index) or None
+    for call in calls:
+        _reordered(_LIB.argreduce_beam_reorder(*call, handle))
     # written through their pointers: graphs that saved them have to know
     torch.autograd.graph.increment_version([t for t in group if not t.is_inference()])
     return states

@@ -167,9 +167,15 @@ __global__ void __launch_bounds__(kReorderBlock, kReorderCtas<BEAMS, W>) beam_re
 template <int W, int BEAMS, int U>
 cudaError_t launch_reorder_n(const ReorderProblem& pr, const argr_caps& caps) {
     auto kern = beam_reorder_kernel<W, BEAMS, U>;
-    int per_sm = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kReorderBlock, 0);
+    static std::atomic<int> known[kLaunchCacheDevices];  // CTAs of an SM, by device
+    int dev = 0, per_sm = 0;
+    cudaError_t e = launch_device(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 0) per_sm = known[dev].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kReorderBlock, 0)) != cudaSuccess) return e;
+        if (dev >= 0) known[dev].store(per_sm, std::memory_order_relaxed);
+    }
     const int64_t most = static_cast<int64_t>(per_sm > 0 ? per_sm : 1) * caps.sm_count;
     // tiles, at most: every position of every item
     const double tiles = (static_cast<double>(pr.positions) * pr.pos_bytes * pr.outer / (W * kReorderBlock * U) + 2) * pr.n * pr.items;

@@ -53,6 +53,14 @@ struct Layout {
     }
 };
 
+bool reorder_layout(int64_t items, int beams, int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
+                    int64_t segment, Layout* lay) {
+    lay->add(item_stride, items);
+    lay->add(beam_stride, beams);
+    lay->add(outer_stride, outer);
+    return lay->nest(segment);
+}
+
 bool touches(const void* a, int64_t na, const void* b, int64_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
@@ -84,7 +92,7 @@ argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items
                                   int64_t end_token, const float* scale, int32_t count, int64_t* tokens,
                                   int64_t* parents, float* out_scores, void* scratch, size_t scratch_bytes,
                                   argr_stream stream) {
-    if (beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items < 0 || items > INT_MAX / 16) return ARGR_EINVAL;
+    if (beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items < 0 || items > INT_MAX / 64) return ARGR_EINVAL;
     argr_status s = check_rows(x, dtype, items * beams, cols, row_stride, temperature);
     if (s != ARGR_OK) return s;
     if (count < 1 || count > ARGR_LOGITS_MAX_TOP) return ARGR_EINVAL;
@@ -125,16 +133,16 @@ argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items
 
 size_t argreduce_beam_scratch_bytes(int64_t items, int32_t beams, int64_t cols, argr_dtype dtype, int32_t count) {
     argr_caps caps;
-    if (items < 1 || beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items > INT_MAX / 16 || cols < 1 || cols > INT_MAX || count < 1 ||
+    if (items < 1 || beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items > INT_MAX / 64 || cols < 1 || cols > INT_MAX || count < 1 ||
         count > ARGR_LOGITS_MAX_TOP || (dtype != ARGR_F32 && dtype != ARGR_F16 && dtype != ARGR_BF16) || current_caps(&caps) != ARGR_OK)
         return 0;
     return beam_scratch_bytes(items, beams, cols, dtype, static_cast<int>(std::min<int64_t>(count, cols)), caps);
 }
 
-argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_t items, int32_t beams,
-                                   int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
-                                   int64_t positions, int64_t position_bytes, const int64_t* parents,
-                                   const int64_t* lengths, argr_stream stream) {
+argr_status argreduce_beam_reorder_check(void* const* states, int32_t n_states, int64_t items, int32_t beams,
+                                         int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
+                                         int64_t positions, int64_t position_bytes, const int64_t* parents,
+                                         const int64_t* lengths) {
     if (n_states < 0 || n_states > ARGR_REORDER_MAX_STATES || items < 0 || beams < 1 || beams > ARGR_BEAM_MAX_BEAMS ||
         outer < 0 || positions < 0 || position_bytes < 1 || item_stride < 0 || beam_stride < 0 || outer_stride < 0)
         return ARGR_EINVAL;
@@ -142,27 +150,37 @@ argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_
     if (n_states == 0 || items == 0 || outer == 0 || positions == 0) return ARGR_OK;
     if (!states || !parents || positions > INT64_MAX / position_bytes || items > INT64_MAX / 8 / beams) return ARGR_EINVAL;
     Layout lay;
-    lay.add(item_stride, items);
-    lay.add(beam_stride, beams);
-    lay.add(outer_stride, outer);
-    if (!lay.nest(positions * position_bytes)) return ARGR_EINVAL;
-    uintptr_t at[ARGR_REORDER_MAX_STATES], low = 0;
+    if (!reorder_layout(items, beams, item_stride, beam_stride, outer, outer_stride, positions * position_bytes, &lay))
+        return ARGR_EINVAL;
+    uintptr_t at[ARGR_REORDER_MAX_STATES];
     for (int i = 0; i < n_states; ++i) {
         if (!states[i]) return ARGR_EINVAL;
         if (touches(states[i], lay.extent, parents, 8 * items * beams) ||
             (lengths && touches(states[i], lay.extent, lengths, 8 * items)))
             return ARGR_EINVAL;
         at[i] = reinterpret_cast<uintptr_t>(states[i]);
-        low |= at[i];
     }
     std::sort(at, at + n_states);
     for (int i = 0; i < n_states; ++i)
         for (int j = i + 1; j < n_states && at[j] - at[i] < static_cast<uintptr_t>(lay.extent); ++j)
             if (lay.meets(static_cast<int64_t>(at[j] - at[i]))) return ARGR_EINVAL;
+    return ARGR_OK;
+}
+
+argr_status argreduce_beam_reorder(void* const* states, int32_t n_states, int64_t items, int32_t beams,
+                                   int64_t item_stride, int64_t beam_stride, int64_t outer, int64_t outer_stride,
+                                   int64_t positions, int64_t position_bytes, const int64_t* parents,
+                                   const int64_t* lengths, argr_stream stream) {
+    argr_status s = argreduce_beam_reorder_check(states, n_states, items, beams, item_stride, beam_stride, outer, outer_stride,
+                                                 positions, position_bytes, parents, lengths);
+    if (s != ARGR_OK || n_states == 0 || items == 0 || outer == 0 || positions == 0) return s;
+    Layout lay;
+    reorder_layout(items, beams, item_stride, beam_stride, outer, outer_stride, positions * position_bytes, &lay);
+    uintptr_t low = 0;
+    for (int i = 0; i < n_states; ++i) low |= reinterpret_cast<uintptr_t>(states[i]);
     if (beams == 1) return ARGR_OK;  // nothing can move
     argr_caps caps;
-    argr_status s = current_caps(&caps);
-    if (s != ARGR_OK) return s;
+    if ((s = current_caps(&caps)) != ARGR_OK) return s;
     ReorderProblem pr = {};
     pr.items = items;
     pr.beams = beams;

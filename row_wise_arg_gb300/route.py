@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib, _stream_ptr
-from ._lib import ARGR_ESCRATCH, ARGR_OK, ArgreduceError
+from ._lib import ARGR_OK, ArgreduceError
 from .logits import _arg, _grad_out, _rows, _side, _under
 
 _LIB = _lib.load()  # looked up once: these calls are short
@@ -57,11 +57,10 @@ def _forward(x, top_k, valid, normalize, counts, balance, dtype):
     args = (x.data_ptr(), code, rows, experts, stride, top_k, bool(normalize), p_valid, weights.data_ptr(), ids.data_ptr(),
             lse.data_ptr(), p_n, p_taken, p_loss)
     handle = _stream_ptr(None, dev.index) or None
-    st = _LIB.argreduce_route(*args, None, 0, handle)
-    if st == ARGR_ESCRATCH:  # many rows; the scratch is this call's own: torch keeps it until the stream has passed the call
-        nbytes = _LIB.argreduce_route_scratch_bytes(rows, experts)
-        scratch = _empty(nbytes, dtype=torch.uint8, device=dev)
-        st = _LIB.argreduce_route(*args, scratch.data_ptr(), nbytes, handle)
+    # many rows need scratch for the counts; it is this call's own: torch keeps it until the stream has passed the call
+    nbytes = _LIB.argreduce_route_scratch_bytes(rows, experts) if n is not None and rows > 256 else 0
+    scratch = _empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    st = _LIB.argreduce_route(*args, scratch.data_ptr() if nbytes else None, nbytes, handle)
     if st != ARGR_OK:
         raise ArgreduceError(st, "argreduce_route")
     return weights, ids, lse, n, taken, loss

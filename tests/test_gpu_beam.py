@@ -102,6 +102,35 @@ def test_long_rows():
     check(x, "bf16", scores, 8)
 
 
+@pytest.mark.parametrize("dtype,cols", [("f32", 45001), ("bf16", 90000), ("f16", 82001)])
+@pytest.mark.parametrize("items,beams,count", [(15, 16, 20), (14, 17, 9), (20, 32, 128)])
+def test_many_long_rows(dtype, cols, items, beams, count):
+    """Rows that a persistent kernel reads, some of them not to be looked at (and full of NaN)."""
+    rng, x, scores = data(items, beams, cols, items)
+    ended = rng.random((items, beams)) < 0.2
+    x[ended] = np.nan
+    scores[3, 4:] = -np.inf
+    x[3, 4:] = np.nan
+    scores[5] = -np.inf
+    x[6][rng.random((beams, cols)) < 0.9999] = -np.inf
+    x[7] = np.round(x[7])  # ties
+    check(x, dtype, scores, count, ended=ended, end_token=1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_ties_than_are_ranked(dtype):
+    """Beams that all go on alike: more entries tie for the last places than the merge ranks by counting."""
+    items, beams, cols, count = 3, 64, 512, 100
+    x = torch.zeros(items, beams, cols, device="cuda", dtype=DT[dtype])
+    x[1, :, 100:] = -20.0
+    r = A.beam_select(x, torch.full((items, beams), -2.0, device="cuda"), count)
+    assert r.tokens[0].tolist() == list(range(100)) and r.parents[0].tolist() == [0] * 100
+    assert r.tokens[1].tolist() == list(range(100)) and r.parents[1].tolist() == [0] * 100
+    scores = torch.linspace(0, -1e-3, beams, device="cuda").expand(items, beams).contiguous()
+    r = A.beam_select(x, scores, count)  # and where their totals lie between
+    assert r.tokens[0].tolist() == list(range(100)) and r.parents[2].tolist() == [0] * 100
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_options(dtype):
     rng, x, scores = data(6, 5, 3001, 7)
@@ -295,6 +324,39 @@ def test_reorder_views():
     A.beam_reorder([group[3]], p, n, dim=3)
     for got, want in zip(tensors, host):
         assert (bits(got) == bits(want)).all()
+
+
+def test_reorder_nothing():
+    """No items, no states, empty states, one beam; and what is refused is refused before anything has moved."""
+    p = torch.tensor([[1, 0]], device="cuda")
+    assert A.beam_reorder([], p) == []
+    empty = torch.zeros(2, 0, 5, device="cuda")
+    assert A.beam_reorder(empty, p, torch.tensor([3], device="cuda"), dim=1) is empty
+    A.beam_reorder(torch.zeros(0, 3, device="cuda"), p[:0])
+    one = torch.arange(6.0, device="cuda").view(3, 2)
+    A.beam_reorder(one, torch.tensor([[0], [-1], [5]], device="cuda"))
+    assert one.tolist() == [[0, 1], [2, 3], [4, 5]]
+    a, b = torch.arange(4.0, device="cuda").view(2, 2), torch.arange(12.0, device="cuda").view(2, 6)
+    with pytest.raises(RuntimeError):
+        A.beam_reorder([a, b, b[:, :]], p)
+    with pytest.raises(ValueError):
+        A.beam_reorder([a, b, b[:, 2:5]], p)
+    assert a.tolist() == [[0, 1], [2, 3]]
+    A.beam_reorder([a, b[:, :2], b[:, 4:]], p)
+    assert a.tolist() == [[2, 3], [0, 1]] and b.tolist() == [[6, 7, 2, 3, 10, 11], [0, 1, 8, 9, 4, 5]]
+
+
+def test_reorder_many_items():
+    """More items than a CTA plans at once, lengths of every size, short segments."""
+    rng = np.random.Generator(np.random.PCG64(8))
+    for items, beams in ((100, 3), (77, 20)):
+        parents = rng.integers(-1, beams, (items, beams))
+        lengths = rng.integers(0, 8, items)
+        host = filled((items * beams, 9, 7, 3), torch.bfloat16, 2)
+        t = host.cuda()
+        A.beam_reorder(t, torch.from_numpy(parents).cuda(), torch.from_numpy(lengths).cuda(), dim=-2)
+        want = reference(host, parents, lengths, 2, items, beams)
+        assert (bits(t).reshape(want.shape) == want).all()
 
 
 def test_reorder_many_states():
