@@ -19,11 +19,16 @@ namespace argr {
 
 constexpr int kReorderBlock = 256;
 template <int BEAMS> constexpr int kReorderItems = BEAMS <= 16 ? 32 : 8;  // items at a time
-// CTAs of an SM, at least. What is in flight decides (45 KB an SM at the copy rate): words per thread against threads.
-// 32 bf16 caches of 16 items, lengths up to 1024, us: 4 beams 310, 335, 379 with 2, 4, 1 words of 16 bytes and 4, 2, 6
-// CTAs; 8 beams, 16 caches of 8 items, 208, 246 with 2, 1 words and 2, 4 CTAs; 5 beams of 4-byte words ([9, 5] states of
-// 119 KB, 12 of them) 15.6, 18.7 with 2, 4 words and 4, 2 CTAs. More CTAs than run at once, four times as many, took 299, 206, 21.3.
-template <int BEAMS, int W> constexpr int kReorderCtas = BEAMS <= 4 ? 4 : BEAMS <= 8 ? (W == 16 ? 2 : W == 8 ? 3 : 4) : BEAMS <= 16 ? 2 : 1;
+// CTAs of an SM, at least. What is in flight decides (45 KB an SM at the copy rate), words per thread against threads; for
+// words of 4 bytes and less it is the instructions (addresses, above all). us:
+//   32 bf16 caches of [16, 4, 8, 1024, 128], ragged lengths, words of 16 bytes: 309, 335, 379 with 2, 4, 1 of them to a thread
+//   and 4, 2, 6 CTAs (four times as many CTAs as run at once: 299); 16 of [8, 8, 8, 1024, 128]: 208, 246 with 2, 1 and 2, 4 CTAs;
+//   words of 4 bytes: 12 states of [9, 5, 3, 77, 129] f32 13.2, 4 of [6, 13, 5, 401, 77] 37; of 2: 8 of [16, 4, 7, 701, 33] 34. Two
+//   words to a thread, an address each: 15.6, 55, 59.
+template <int BEAMS, int W> constexpr int kReorderCtas = BEAMS <= 4 ? 4 : BEAMS <= 8 ? (W == 16 ? 2 : 3) : BEAMS <= 16 ? 2 : 1;
+// Words per thread at a time.
+template <int BEAMS, int W>
+constexpr int kReorderWords = BEAMS <= 8 ? (W >= 8 ? 2 : 4) : BEAMS <= 16 ? (W >= 8 ? 1 : 4) : BEAMS <= 32 && W <= 4 ? 2 : 1;
 
 template <int W> struct WordOf;
 template <> struct WordOf<16> { using type = uint4; };
@@ -65,6 +70,29 @@ __device__ __forceinline__ void move_words(unsigned char* base, const int64_t (&
 #pragma unroll
         for (int i = 0; i < BEAMS; ++i)
             if (i < n && at[u] >= 0) *reinterpret_cast<Word*>(base + at[u] + to[i]) = v[u][i];
+    }
+}
+
+// The same for U words kReorderBlock apart from `first` (of beam 0) on: one address to a beam, where the addresses of narrow
+// words would cost more than the words do.
+template <class Word, int BEAMS, int U>
+__device__ __forceinline__ void move_run(unsigned char* first, int n, const int64_t* to, const int64_t* from) {
+    Word v[BEAMS][U];
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i) {
+        if (i < n) {
+            const Word* p = reinterpret_cast<const Word*>(first + from[i]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[i][u] = p[u * kReorderBlock];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < BEAMS; ++i) {
+        if (i < n) {
+            Word* p = reinterpret_cast<Word*>(first + to[i]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) p[u * kReorderBlock] = v[i][u];
+        }
     }
 }
 
@@ -127,27 +155,51 @@ __global__ void __launch_bounds__(kReorderBlock, kReorderCtas<BEAMS, W>) beam_re
             int64_t in_state;
             const int64_t state = divide(tile - (q ? sh.end[q - 1] : 0), tiles, &in_state);
             unsigned char* base = pr.states[state] + (item0 + q) * pr.item_stride;
-            int64_t at[U];
+            [[maybe_unused]] int64_t at[U];  // (of wide words)
             if (in_state < word_tiles) {
                 // the tile's first word, and from it on: one division a tile where segments are longer than tiles
                 int64_t first = in_state * kTile, o0 = 0;
                 const int64_t left = words * pr.outer - first;
                 if (pr.outer > 1) o0 = divide(first, words, &first);
+                if constexpr (W >= 8) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    int64_t w = first + (u * kReorderBlock + t), o = o0;
-                    if (w >= words) {
-                        if (words >= kTile) {
-                            w -= words;
-                            ++o;
-                        } else {
-                            o += divide(w, words, &w);
+                    for (int u = 0; u < U; ++u) {
+                        int64_t w = first + (u * kReorderBlock + t), o = o0;
+                        if (w >= words) {
+                            if (words >= kTile) {
+                                w -= words;
+                                ++o;
+                            } else {
+                                o += divide(w, words, &w);
+                            }
                         }
+                        at[u] = u * kReorderBlock + t < left ? o * pr.outer_stride + w * W : -1;
                     }
-                    at[u] = u * kReorderBlock + t < left ? o * pr.outer_stride + w * W : -1;
+                    move_words<Word, BEAMS, U>(base, at, sh.n[q], sh.to[q], sh.from[q]);
+                } else if (first + kTile <= words) {
+                    move_run<Word, BEAMS, U>(base + o0 * pr.outer_stride + (first + t) * W, sh.n[q], sh.to[q], sh.from[q]);
+                } else {  // a tile over several segments, in smaller steps
+                    constexpr int A = U < 2 ? 1 : 2;
+#pragma unroll 1
+                    for (int u0 = 0; u0 < kTile && u0 < left; u0 += kReorderBlock * A) {
+                        int64_t some[A];
+#pragma unroll
+                        for (int u = 0; u < A; ++u) {
+                            int64_t w = first + (u0 + u * kReorderBlock + t), o = o0;
+                            if (w >= words) {
+                                if (words >= kTile) {
+                                    w -= words;
+                                    ++o;
+                                } else {
+                                    o += divide(w, words, &w);
+                                }
+                            }
+                            some[u] = u0 + u * kReorderBlock + t < left ? o * pr.outer_stride + w * W : -1;
+                        }
+                        move_words<Word, BEAMS, A>(base, some, sh.n[q], sh.to[q], sh.from[q]);
+                    }
                 }
-                move_words<Word, BEAMS, U>(base, at, sh.n[q], sh.to[q], sh.from[q]);
-            } else {
+            } else if constexpr (W >= 8) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t b = (in_state - word_tiles) * kTile + u * kReorderBlock + t;
@@ -159,13 +211,24 @@ __global__ void __launch_bounds__(kReorderBlock, kReorderCtas<BEAMS, W>) beam_re
                     }
                 }
                 move_words<uint8_t, BEAMS, U>(base, at, sh.n[q], sh.to[q], sh.from[q]);
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    const int64_t b = (in_state - word_tiles) * kTile + u * kReorderBlock + t;
+                    if (b >= rest * pr.outer) break;
+                    int64_t in_segment;
+                    const int64_t o = divide(b, rest, &in_segment);
+                    const int64_t one[1] = {o * pr.outer_stride + words * W + in_segment};
+                    move_words<uint8_t, BEAMS, 1>(base, one, sh.n[q], sh.to[q], sh.from[q]);
+                }
             }
         }
     }
 }
 
-template <int W, int BEAMS, int U>
+template <int W, int BEAMS>
 cudaError_t launch_reorder_n(const ReorderProblem& pr, const argr_caps& caps) {
+    constexpr int U = kReorderWords<BEAMS, W>;
     auto kern = beam_reorder_kernel<W, BEAMS, U>;
     static std::atomic<int> known[kLaunchCacheDevices];  // CTAs of an SM, by device
     int dev = 0, per_sm = 0;
@@ -189,11 +252,11 @@ cudaError_t launch_reorder_n(const ReorderProblem& pr, const argr_caps& caps) {
 // words from 33 beams on.
 template <int W>
 cudaError_t launch_reorder_w(const ReorderProblem& pr, const argr_caps& caps) {
-    if (pr.beams <= 4) return launch_reorder_n<W, 4, 2>(pr, caps);
-    if (pr.beams <= 8) return launch_reorder_n<W, 8, 2>(pr, caps);
-    if (pr.beams <= 16) return launch_reorder_n<W, 16, 1>(pr, caps);
-    if (pr.beams <= 32) return launch_reorder_n<W, 32, 1>(pr, caps);
-    return launch_reorder_n<(W < 8 ? W : 8), 64, 1>(pr, caps);
+    if (pr.beams <= 4) return launch_reorder_n<W, 4>(pr, caps);
+    if (pr.beams <= 8) return launch_reorder_n<W, 8>(pr, caps);
+    if (pr.beams <= 16) return launch_reorder_n<W, 16>(pr, caps);
+    if (pr.beams <= 32) return launch_reorder_n<W, 32>(pr, caps);
+    return launch_reorder_n<(W < 8 ? W : 8), 64>(pr, caps);
 }
 
 cudaError_t launch_beam_reorder(const ReorderProblem& pr, const argr_caps& caps) {
