@@ -23,14 +23,14 @@
 namespace argr {
 
 constexpr int kMaxBeams = ARGR_BEAM_MAX_BEAMS;
-constexpr int kMergeBlock = 256;
+constexpr int kMergeBlock = 512;
 constexpr int kMergeMax = 256;  // entries ranked by counting, at most
 
 // What the merge knows of a beam.
 struct BeamSum {
     double base;   // s_b - ln S
     double scale;  // of the rank
-    float m;
+    double m;
     int state;     // kBeamGone, kBeamEnded or kBeamLive
 };
 constexpr int kBeamGone = 0, kBeamEnded = 1, kBeamLive = 2;
@@ -41,6 +41,9 @@ __device__ __forceinline__ unsigned long long rank_key(double rank) {
     if ((hi & 0x7ff00000u) == 0x7ff00000u) return 0ull;
     const unsigned long long b = static_cast<unsigned long long>(hi) << 32 | lo;
     return (hi >> 31) ? 0ull - b : b | 0x8000000000000000ull;  // (-0, 1 << 63, maps to itself, as +0 does)
+}
+__device__ __forceinline__ double key_rank(unsigned long long key) {
+    return __longlong_as_double(static_cast<long long>((key >> 63) ? key & 0x7fffffffffffffffull : 0ull - key));
 }
 
 // base - ln s for a binary32 s >= 1/2, off by less than 3e-9: with s = 2^e f, f in [2/3, 4/3), ln f = 2 artanh u,
@@ -80,7 +83,7 @@ __device__ __forceinline__ bool load_beam(const BeamProblem& pr, int64_t r, Beam
     const float w = pr.scale ? pr.scale[r] : 1.0f;
     v.base = s;
     v.scale = w;
-    v.m = 0.0f;
+    v.m = 0.0;
     v.state = s == neg_inf() ? kBeamGone : pr.rows.beam_ended && pr.rows.beam_ended[r] ? kBeamEnded : kBeamLive;
     return v.state == kBeamGone || (fabsf(s) <= FLT_MAX && w > 0.0f && w <= FLT_MAX);
 }
@@ -97,7 +100,7 @@ __device__ __forceinline__ void load_beams(const BeamProblem& pr, int64_t item, 
 }
 
 // The merge of an item's lists, ranks (a power of two, 1 << shift) of k keys to a beam, each in order and filled up
-// with 0; load_beams() has been called. `keys` and `totals`: room for as many. The entries become ranks in 64 bits; a
+// with 0; load_beams() has been called. `keys` and `totals` (where there are scales): room for as many. The entries become ranks in 64 bits; a
 // value that at least `count` of them reach, and not many more, is found bit by bit in their
 // upper 32 bits, a barrier each, from the first bit on in which they differ; what reaches it is ranked by counting.
 // Where too many do (ties), one warp takes the best of the lists' heads `count` times.
@@ -143,15 +146,15 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
             if (v.state == kBeamLive) {
                 const unsigned long long g = gathered[l * k + i];
                 if (g) {
-                    total = v.base + (static_cast<double>(order_value(static_cast<unsigned>(g >> 32))) - static_cast<double>(v.m)) * pr.inv_t;
-                    key = rank_key(total * v.scale);
+                    total = v.base + (static_cast<double>(order_value(static_cast<unsigned>(g >> 32))) - v.m) * pr.inv_t;
+                    key = rank_key(pr.scale ? total * v.scale : total);
                 }
             } else if (v.state == kBeamEnded && (l & (ranks - 1)) == 0 && i == 0) {
-                key = rank_key(total * v.scale);
+                key = rank_key(pr.scale ? total * v.scale : total);
             }
             if (poisoned) key = 0;
             keys[l * k + i] = key;
-            totals[l * k + i] = static_cast<float>(total);
+            if (pr.scale) totals[l * k + i] = static_cast<float>(total);
             const unsigned hi = static_cast<unsigned>(key >> 32);
             if (key) low = min(low, hi);
             high = max(high, hi);
@@ -197,11 +200,11 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
     }
     __syncthreads();
     const int n = sh.n;
-    const auto put = [&](int r, int i) {
+    const auto put = [&](int r, int i, unsigned long long key) {
         const int parent = i / k >> shift;
         pr.tokens[item * count + r] = sh.beam[parent].state == kBeamEnded ? pr.end_token : key_index(gathered[i]);
         pr.parents[item * count + r] = parent;
-        pr.out_scores[item * count + r] = totals[i];
+        pr.out_scores[item * count + r] = pr.scale ? totals[i] : static_cast<float>(key_rank(key));
     };
     if (n <= kMergeMax) {
         // four lanes to an entry
@@ -217,7 +220,7 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
             }
             r += __shfl_xor_sync(0xffffffffu, r, 1);
             r += __shfl_xor_sync(0xffffffffu, r, 2);
-            if (q < n && (t & 3) == 0 && r < count) put(r, i);
+            if (q < n && (t & 3) == 0 && r < count) put(r, i, key);
         }
         for (int r = n + t; r < count; r += nt) {
             pr.tokens[item * count + r] = -1;
@@ -255,7 +258,7 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
         }
     }
     __syncthreads();
-    for (int r = t; r < count; r += nt) put(r, sh.win[r]);
+    for (int r = t; r < count; r += nt) put(r, sh.win[r], keys[sh.win[r]]);
 }
 
 // Shared memory of a CTA that reads rows: a segment's slots, the list so far, and, where it merges too, `lists` lists.
