@@ -11,7 +11,8 @@
 // all items are dealt to as many CTAs as run at once. (With CTAs for each item, and for segments of the
 // longest, items of different lengths left them waiting in waves: 12 states of 9 items, 5 beams, 77 positions took 21 us.)
 //
-// Bound by memory: each distinct parent read once, each moving beam written once.
+// Bound by memory: each distinct parent read once, each moving beam written once. 32 caches of [16 x 4, 8, 1024, 128] bf16, ragged, 289 to 309 us,
+// 5.9 TB/s of the bytes that move.
 #include "kernels_impl.cuh"
 #include "select.h"
 

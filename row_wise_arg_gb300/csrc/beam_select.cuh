@@ -15,6 +15,10 @@
 // its sums and its list to CTA 0 through distributed shared memory, which merges: no
 // scratch, one launch. Many rows: a CTA per row, or the persistent kernel of long rows
 // (logits_stream.cuh), leaves lists and sums in scratch, and a second kernel merges them.
+//
+// Bound by latency for few rows: in a graph of calls whose inputs rotate past L2, [1, 4, 32000] f32, 8 continuations, 7.6 us: read
+// 1.5, threshold and alternatives 2.2, hand-over 0.6, merge 2 (sums and logarithms 0.5, ranks 0.7, threshold and places
+// 1); [16, 4, 202048] bf16 14.6 us. [64, 16, 202048] bf16, 32 continuations, 95 us, 4.1 TB/s: 1024 rows in 3.4 rounds.
 #pragma once
 
 #include "logits_stream.cuh"

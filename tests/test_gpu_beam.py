@@ -368,6 +368,31 @@ def test_reorder_many_states():
         assert s.tolist() == [[2.0 + i, 3.0 + i], [i, 1.0 + i], [i, 1.0 + i]]
 
 
+def test_reorder_on_another_stream():
+    side = torch.cuda.Stream()
+    host = filled((12, 3, 50, 8), torch.float32, 4)
+    parents = np.array([[1, 0, 3, 3], [2, 2, 2, 2], [0, -1, 1, 9]])
+    t, p = host.cuda(), torch.from_numpy(parents).cuda()
+    side.wait_stream(torch.cuda.current_stream())
+    assert A.beam_reorder([t], p, stream=side)[0] is t
+    side.synchronize()
+    want = reference(host, parents, None, None, 3, 4)
+    assert (bits(t).reshape(want.shape) == want).all()
+
+
+def test_reorder_counts_as_a_change():
+    """What automatic differentiation saved of a state is not what it holds any more."""
+    t = torch.randn(4, 6, device="cuda")
+    leaf = torch.randn(4, 6, device="cuda", requires_grad=True)
+    loss = (leaf * t).sum()
+    A.beam_reorder(t, torch.tensor([[1, 0, 2, 3]], device="cuda"))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        u = torch.ones(2, 3, device="cuda")
+        A.beam_reorder([u], torch.tensor([[1, 1]], device="cuda"))
+
+
 def test_reorder_refuses():
     t = torch.zeros(6, 4, 8, device="cuda")
     p = torch.zeros(2, 3, dtype=torch.int64, device="cuda")

@@ -276,6 +276,46 @@ def test_backward_in_a_graph():
     assert torch.equal(got, want)
 
 
+def test_backward_on_another_stream():
+    side = torch.cuda.Stream()
+    x = torch.randn(700, 48, device="cuda", requires_grad=True)
+    want = torch.autograd.grad(A.route_topk(x, 4, balance=True).balance * 5, x)[0]
+    side.wait_stream(torch.cuda.current_stream())
+    r = A.route_topk(x, 4, balance=True, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(torch.autograd.grad(r.balance * 5, x)[0], want)
+    d = x.detach()
+    side.wait_stream(torch.cuda.current_stream())
+    got = A.route_topk_backward(d, None, r.ids, r.lse.detach(), r.counts, r.rows, grad_balance=torch.tensor(5.0, device="cuda"),
+                                stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_weights_changed_in_place_are_noticed():
+    x = torch.randn(20, 16, device="cuda", requires_grad=True)
+    r = A.route_topk(x, 3)
+    loss = r.weights.sum()
+    with torch.no_grad():
+        r.weights.mul_(2.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_only_some_outputs_are_used():
+    """Gradients of the outputs that a loss leaves out are not asked for; counts and ids have none."""
+    x = torch.randn(50, 16, device="cuda", requires_grad=True)
+    r = A.route_topk(x, 3, counts=True, balance=True)
+    assert not r.ids.requires_grad and not r.counts.requires_grad and not r.rows.requires_grad
+    one = torch.autograd.grad(r.lse.sum(), x, retain_graph=True)[0]
+    assert torch.allclose(one, torch.softmax(x.detach(), -1), atol=1e-6)
+    two = torch.autograd.grad(r.weights[:, 0].sum(), x)[0]  # gradients that are not contiguous
+    w = r.weights.detach()
+    want = torch.zeros_like(x).scatter_(1, r.ids, -w[:, :1] * w)
+    want.scatter_add_(1, r.ids[:, :1], w[:, :1])
+    assert torch.allclose(two, want, atol=1e-6)
+
+
 def test_refuses():
     x = torch.zeros(4, 10, device="cuda")
     r = A.route_topk(x, 2, balance=True)
