@@ -87,7 +87,8 @@ def check(x, dtype, k, normalize=True, valid=None, pad=0, offset=0, seed=1, grad
     (1, 1, 1, True, 0, 0), (1, 8, 2, True, 0, 0), (3, 2, 2, False, 0, 1), (7, 60, 6, True, 0, 0), (300, 64, 8, False, 0, 0),
     (1000, 129, 5, True, 0, 0), (257, 256, 8, True, 0, 0), (33, 1024, 32, True, 0, 0), (5, 1023, 17, False, 3, 1),
     (2000, 8, 2, True, 0, 0), (3, 33, 32, False, 0, 0), (64, 31, 31, True, 5, 3), (100, 500, 4, True, 0, 0), (9, 4, 4, True, 12, 1),
-    (501, 16, 1, False, 0, 0), (130, 384, 8, True, 8, 0), (40, 160, 6, True, 0, 8)])
+    (501, 16, 1, False, 0, 0), (130, 384, 8, True, 8, 0), (40, 160, 6, True, 0, 8),
+    (700, 256, 32, True, 0, 0), (90, 200, 20, False, 0, 0), (50, 512, 32, True, 0, 0), (333, 12, 12, True, 4, 0), (70, 32, 32, False, 0, 0)])
 def test_sizes(dtype, rows, experts, k, normalize, pad, offset):
     rng = np.random.Generator(np.random.PCG64(rows + experts))
     x = rng.normal(size=(rows, experts)) + rng.normal(size=experts) * 0.5
