@@ -106,7 +106,7 @@ def _geometry(t, items, beams, dim):
     if len(shape) >= 1 and shape[0] == items * beams:
         lead, strides = 1, (beams * stride[0], stride[0])
     elif len(shape) >= 2 and shape[0] == items and shape[1] == beams:
-        lead, strides = 2, stride[:2]
+        lead, strides = 2, (stride[0] if items > 1 else beams * stride[1], stride[1])
     else:
         raise ValueError(f"a state must have the leading dimensions [{items}, {beams}] or [{items * beams}], got {tuple(shape)}")
     if dim is not None:

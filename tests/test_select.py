@@ -150,6 +150,49 @@ def test_geometry():
             _geometry(bad, 2, 3, dim)
 
 
+def test_geometry_of_one_item():
+    """A lone item's stride says nothing: columns of the same rows are apart whatever it is."""
+    torch = pytest.importorskip("torch")
+    from row_wise_arg_gb300.beam import _apart, _geometry
+    rows = torch.empty(4, 10)
+    a = rows.as_strided((1, 4, 3), (7, 10, 1))
+    b = rows.as_strided((1, 4, 5), (1, 10, 1), 3)
+    ga, gb = _geometry(a, 1, 4, None), _geometry(b, 1, 4, None)
+    assert ga == (160, 40, 1, 0, 1, 12) and gb == (160, 40, 1, 0, 1, 20)
+    assert _apart(a.data_ptr(), ga, b.data_ptr(), gb, 1, 4)
+
+
+class Elsewhere:
+    """What the binding looks at of logits that lie on another GPU than the current one."""
+    is_cuda, requires_grad, shape = True, False, (4, 100)
+
+    def get_device(self):
+        return 1
+
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was used of logits on another device")
+
+
+def test_logits_of_another_device_are_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = Elsewhere()
+    for call in (lambda: A.beam_select(x, None, 3), lambda: A.route_topk(x, 2),
+                 lambda: A.route_topk_backward(x, None, None, None)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+def test_what_lies_on_the_cpu_is_refused():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 10)
+    p = torch.zeros(1, 4, dtype=torch.int64)
+    for call in (lambda: A.beam_select(x, x[:, 0], 3), lambda: A.route_topk(x, 2), lambda: A.beam_reorder(x, p),
+                 lambda: A.beam_reorder([x], p)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
 def test_apart():
     pytest.importorskip("torch")
     from row_wise_arg_gb300.beam import _apart
