@@ -138,14 +138,16 @@ def _span(g, items, beams):
 
 def _apart(a, ga, b, gb, items, beams):
     """Whether two states of different geometry, at the addresses a <= b, certainly share no byte:
-    one ends before the other begins, or they are columns of the same rows."""
+    one ends before the other begins, or they are columns of the same rows, a beam's or the segments'."""
     if a + _span(ga, items, beams) <= b:
         return True
-    row = ga[1]
-    if ga[:2] != gb[:2] or ga[0] != beams * row or row == 0:
+    if ga[:2] != gb[:2]:
         return False
-    na, nb = _span(ga, 1, 1), _span(gb, 1, 1)
-    return (b - a) % row >= na and (b - a) % row + nb <= row
+    for row, na, nb, fit in ((ga[1], _span(ga, 1, 1), _span(gb, 1, 1), True),
+                             (ga[3], ga[4] * ga[5], gb[4] * gb[5], ga[3] == gb[3] and ga[3] and ga[1] % ga[3] == 0)):
+        if fit and row and ga[0] % row == 0 and (b - a) % row >= na and (b - a) % row + nb <= row:
+            return True
+    return False
 
 
 def _reordered(st):

@@ -45,10 +45,15 @@ struct Layout {
     bool meets(int64_t d, int level = 0) const {
         if (level == n) return d > -segment && d < segment;
         const Dim& m = dim[level];
-        int64_t q = d / m.stride;
-        if (d % m.stride < 0) --q;
-        for (int64_t k = q; k <= q + 1; ++k)
-            if (k > -m.count && k < m.count && meets(d - k * m.stride, level + 1)) return true;
+        int64_t q = 0;
+        if (d < 0 || d >= m.stride) {
+            q = d / m.stride;
+            if (d % m.stride < 0) --q;
+        }
+        for (int64_t k = q; k <= q + 1; ++k) {
+            const int64_t left = d - k * m.stride;
+            if (k > -m.count && k < m.count && left > -m.inner && left < m.inner && meets(left, level + 1)) return true;
+        }
         return false;
     }
 };

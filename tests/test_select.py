@@ -202,6 +202,43 @@ def test_apart():
     assert not _apart(1000, a, 1040, (600, 200, 1, 0, 5, 12), 2, 3)
 
 
+@pytest.mark.parametrize("seed", range(20))
+def test_apart_is_never_wrong(seed):
+    """Against the bytes themselves: states that share one are never taken to be apart."""
+    pytest.importorskip("torch")
+    from row_wise_arg_gb300.beam import _apart
+    rng = np.random.Generator(np.random.PCG64(seed))
+    seen = set()
+    for _ in range(300):
+        unit = int(rng.integers(6, 13))  # what segments lie apart, one item and beam of which take `per` or more
+        per = int(rng.integers(1, 4))
+        items, beams = int(rng.integers(1, 3)), int(rng.integers(1, 3))
+
+        def geometry():
+            outer, size = int(rng.integers(1, per + 1)), int(rng.integers(1, 7))
+            beam = unit * (per + int(rng.integers(0, 2)) if rng.random() < 0.3 else per) + (int(rng.integers(0, 2)) if rng.random() < 0.3 else 0)
+            item = beam * beams + (unit * int(rng.integers(0, 3)) if rng.random() < 0.3 else 0)
+            return (item, beam, outer, unit if outer > 1 else 0, size, 1)
+
+        def touched(at, g):
+            return {at + i * g[0] + j * g[1] + o * g[3] + p for i in range(items) for j in range(beams) for o in range(g[2])
+                    for p in range(g[4])}
+        ga, gb, d = geometry(), geometry(), int(rng.integers(0, 40))
+        apart, meet = _apart(1000, ga, 1000 + d, gb, items, beams), not touched(1000, ga).isdisjoint(touched(1000 + d, gb))
+        assert not (apart and meet), (ga, gb, d, items, beams)
+        seen.add((apart, meet))
+    assert seen == {(True, False), (False, True), (False, False)}
+
+
+def test_apart_by_segments():
+    """[2, 3, 5, 10 | 6] int8 cut along the last dimension: segments of 10 and of 6 bytes, 16 apart."""
+    pytest.importorskip("torch")
+    from row_wise_arg_gb300.beam import _apart
+    a, b = (240, 80, 5, 16, 1, 10), (240, 80, 5, 16, 1, 6)
+    assert _apart(1000, a, 1010, b, 2, 3) and not _apart(1000, a, 1009, b, 2, 3) and not _apart(1000, a, 1011, b, 2, 3)
+    assert not _apart(1000, a, 1010, (240, 80, 5, 15, 1, 5), 2, 3)
+
+
 def test_beam_definition():
     """The 64-bit step against sorting every continuation by hand."""
     x = np.log(np.array([[0.5, 0.3, 0.2], [0.1, 0.8, 0.1]]))
