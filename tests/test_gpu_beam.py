@@ -243,6 +243,47 @@ def test_other_stream_and_graph():
         assert torch.equal(state.cpu(), torch.from_numpy(ref.reorder(first.view(4, 4, 3, 50).cpu().numpy(), parents.cpu().numpy())).view(16, 3, 50))
 
 
+def test_calls_at_once():
+    """Two steps with scratch and two without, on two streams at a time, are each as they are alone."""
+    work = [(20, 17, 30000, 24), (400, 3, 500, 6), (2, 4, 32000, 8), (15, 16, 90000, 20)]
+    given = []
+    for i, (items, beams, cols, count) in enumerate(work):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        given.append((torch.randn(items, beams, cols, device="cuda", generator=g).bfloat16(),
+                      torch.randn(items, beams, device="cuda", generator=g), count))
+    want = [A.beam_select(*a) for a in given]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for turn in range(8):
+        for i, a in enumerate(given):
+            got.append((i, A.beam_select(*a, stream=streams[(i + turn) % 2])))
+    torch.cuda.synchronize()
+    for i, r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i])), i
+
+
+def test_offsets_past_32_bits():
+    """Rows and states whose parts begin beyond 2^31 elements."""
+    stride = (1 << 30) + 64
+    buf = torch.empty(3 * stride + 4096, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((2, 2, 2000), (2 * stride, stride, 1))
+    near = torch.randn(2, 2, 2000, device="cuda").bfloat16()
+    x.copy_(near)
+    scores = torch.tensor([[-1.0, -1.5], [-2.0, -1.9]], device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(A.beam_select(x, scores, 9), A.beam_select(near, scores, 9)))
+    parents = torch.tensor([[1, 0], [1, 1]], device="cuda")
+    A.beam_reorder(x, parents)
+    assert torch.equal(x, torch.stack([near[0].flip(0), near[1][[1, 1]]]))
+    x.copy_(near)
+    cut = x[:, :, 3:1996]  # unaligned
+    A.beam_reorder(cut, parents, torch.tensor([1993, 1000], device="cuda"), dim=2)
+    want = near.clone()
+    want[0, :, 3:1996] = near[0].flip(0)[:, 3:1996]
+    want[1, 0, 3:1003] = near[1, 1, 3:1003]
+    assert torch.equal(x, want)
+
+
 # -- reordering -------------------------------------------------------------------------------
 PARENTS = {
     "stay": lambda rng, i, b: np.tile(np.arange(b), (i, 1)),

@@ -169,6 +169,41 @@ def test_many_rows():
         assert torch.equal(again.balance, r.balance)
 
 
+def test_offsets_past_32_bits():
+    """Rows that begin beyond 2^31 elements, and their gradient over them."""
+    stride = (1 << 30) + 64
+    buf = torch.empty(3 * stride + 64, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((4, 60), (stride, 1))
+    near = torch.randn(4, 60, device="cuda").bfloat16()
+    x.copy_(near)
+    r, want = (A.route_topk(t, 5, counts=True, balance=True) for t in (x, near))
+    assert all(torch.equal(a, b) for a, b in zip(r, want))
+    g = dict(grad_weights=torch.randn(4, 5, device="cuda"), grad_lse=torch.randn(4, device="cuda"),
+             grad_balance=torch.tensor(2.0, device="cuda"))
+    want = A.route_topk_backward(near, *want[:5], **g)
+    A.route_topk_backward(x, *r[:5], grad=x, **g)
+    assert torch.equal(x, want)
+
+
+def test_calls_at_once():
+    """Routes of many rows (with scratch) and of few, and gradients, on two streams at a time."""
+    given = [torch.randn(n, e, device="cuda") for n, e in ((60000, 64), (5000, 256), (30, 64), (20001, 60))]
+    want = [A.route_topk(x, 6, counts=True, balance=True) for x in given]
+    g = [torch.randn(x.shape[0], 6, device="cuda") for x in given]
+    grads = [A.route_topk_backward(x, *r[:5], grad_weights=w) for x, r, w in zip(given, want, g)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for turn in range(8):
+        for i, x in enumerate(given):
+            s = streams[(i + turn) % 2]
+            r = A.route_topk(x, 6, counts=True, balance=True, stream=s)
+            got.append((i, r, A.route_topk_backward(x, *r[:5], grad_weights=g[i], stream=s)))
+    torch.cuda.synchronize()
+    for i, r, d in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i])) and torch.equal(d, grads[i]), i
+
+
 def test_gradient_against_differences():
     """The 64-bit formula that the kernel is held to, against differences of the definition (the choice fixed)."""
     rng = np.random.Generator(np.random.PCG64(9))
