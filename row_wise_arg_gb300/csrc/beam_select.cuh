@@ -18,7 +18,7 @@
 //
 // Bound by latency for few rows: in a graph of calls whose inputs rotate past L2, [1, 4, 32000] f32, 8 continuations, 7.6 us: read
 // 1.5, threshold and alternatives 2.2, hand-over 0.6, merge 2 (sums and logarithms 0.5, ranks 0.7, threshold and places
-// 1); [16, 4, 202048] bf16 14.6 us. [64, 16, 202048] bf16, 32 continuations, 95 us, 4.1 TB/s: 1024 rows in 3.4 rounds.
+// 1); [16, 4, 202048] bf16 14.6 us. [64, 16, 202048] bf16, 32 continuations, 92 us, 4.3 TB/s: 1024 rows in 3.4 rounds.
 #pragma once
 
 #include "logits_stream.cuh"
@@ -422,7 +422,7 @@ inline bool beam_stream_plan(int64_t rows, int64_t cols, int dtype, int k, const
 // waves, those of 16 up to one (they find few places): cluster against a CTA per row and a merge,
 // [64, 4, 128000] bf16 17.5 / 22.3 (streaming 24.6), [60, 4, 32000] 9.8 / 11.7, [30, 8, 32000] 10.7 / 12.7, but [19, 16, 202048], 32
 // continuations, 60.6 / 53.3 (streaming 49.2), [19, 16, 32000] 25.8 / 24.6 (21.2 with 128 threads). Past that long rows are
-// streamed ([64, 16, 202048], 32: 98.6, against 107.8 with a CTA per row).
+// streamed ([64, 16, 202048], 32: 92, against 107.8 with a CTA per row).
 inline BeamPlan plan_beams(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps) {
     BeamPlan p = {};
     const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32), rows = items * beams;

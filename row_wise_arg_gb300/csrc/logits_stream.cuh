@@ -22,7 +22,7 @@
 // reference for the exponentials that moves only when a group exceeds it by more
 // than 2^kSlack.
 //
-// [2048, 202048] bf16: 138 us, 6.0 TB/s; 147, 157, 171 us with the top 1, 20, 64 (the finishing warps
+// [2048, 202048] bf16: 134 us in a graph of calls, 6.2 TB/s; 143, 151, 160 us with the top 1, 20, 64 (the finishing warps
 // take issue slots, and the last rows' finish is not hidden); distillation, 64 slots and a tail,
 // 145 us. [2048, 100000] f32 138 us, 6.0 TB/s; [1500, 65537] f32, top 1, 70 us, 5.6 TB/s. A CTA of 256
 // threads and twice as many of them, and picked groups staged in shared memory for the finisher,
@@ -330,16 +330,32 @@ __device__ __forceinline__ unsigned long long warp_prune(unsigned long long* key
     return least;
 }
 
+__device__ __forceinline__ uint32_t at4(const uint4& w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+
 // A value (order32) that at least k of a warp's V * 32 values reach, or 0.
 template <int V>
 __device__ __forceinline__ unsigned warp_threshold(const unsigned (&v)[V], int k) {
-    unsigned at = 0;
-    for (int b = 31; b >= 0; --b) {
-        const unsigned trial = at | 1u << b;
+    const auto reach = [&](unsigned trial) {
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) mine += v[i] >= trial;
-        const int n = __reduce_add_sync(0xffffffffu, mine);
+        return __reduce_add_sync(0xffffffffu, mine);
+    };
+    // from the first bit on in which those that are not 0 differ
+    unsigned low = ~0u, high = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        low = min(low, v[i] - 1u);
+        high = max(high, v[i]);
+    }
+    low = __reduce_min_sync(0xffffffffu, low) + 1u;
+    high = __reduce_max_sync(0xffffffffu, high);
+    int b = 31 - __clz(low ^ high);  // -1: none
+    unsigned at = b < 0 ? high : b < 31 ? high & ~((2u << b) - 1u) : 0u;
+    if (high == 0 || reach(at > 1u ? at : 1u) < k) return 0;
+    for (; b >= 0; --b) {
+        const unsigned trial = at | 1u << b;
+        const int n = reach(trial);
         if (n >= k) {
             at = trial;
             if (n <= k + k / 8 + 2) break;
@@ -393,8 +409,12 @@ __device__ __forceinline__ void rank_lane_keys(const unsigned long long* keys, i
 // The row's k first alternatives, in order, as keys in cand[kStreamCands, + k),
 // from the largest elements of its slots (big), of its tiles of 32 groups (tile)
 // and of the streaming threads (most). The finisher shares its scheduler with
-// streaming warps and works alone, so its chains of dependent instructions count: 128 slots or 32
-// units of 16 bytes are looked at side by side, several at a time.
+// streaming warps and works alone, so its chains of dependent instructions count, and branches, whose code is
+// mostly not at hand: a tile's 32 slots are compared by one lane without any, 128 units of 16 bytes are looked at
+// side by side, and their hits get places together. A last row's finish, 36 slots picked for the top 32 of
+// [., 202048]: threshold 1.0 us, slots 2.8, units 3.7, order 0.7. (128 slots at a time, with a ballot for each, and
+// units of 32 lanes with places of their own took 4.9 and 4.1, 7.7 and 18 for the top 128, now 4 and 15; picked slots
+// prefetched in bulk, each by its lane, 9 in place of 2.8.)
 template <class Tag>
 __device__ __forceinline__ void warp_top(const WideRow<Tag>& row, int k, const unsigned* big, const unsigned* tile,
                                          const unsigned* most, int streamers, unsigned long long* cand,
@@ -457,31 +477,44 @@ __device__ __forceinline__ void warp_top(const WideRow<Tag>& row, int k, const u
                 lo[u] = i < 8 * picked ? row.slot_begin(list[i >> 3]) + (i & 7) * P : -1;
                 w[u] = lo[u] >= 0 ? ld_stream16(row.p + lo[u]) : make_uint4(0, 0, 0, 0);
             }
+            // bit u * P + e: element e of unit u may matter
+            unsigned hits = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (i0 + 32 * u >= 8 * picked) break;  // (of the whole warp)
-                __syncwarp();
-                room_for(32 * P);
-                unsigned hits = 0;
                 const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
                 for (int e = 0; e < P; ++e) {
                     float x;
                     if constexpr (P == 4) x = __uint_as_float(word[e]);
                     else x = Tag::widen(static_cast<uint16_t>(e & 1 ? word[e >> 1] >> 16 : word[e >> 1] & 0xffffu));
-                    if (x >= least || nans) hits |= 1u << e;
+                    if ((x >= least || nans) && lo[u] >= 0) hits |= 1u << (u * P + e);
                 }
-                if (lo[u] < 0) hits = 0;
-                int p = warp_places(__popc(hits), &n);
-                for (; hits; hits &= hits - 1) {
-                    const int e = __ffs(hits) - 1;
+            }
+            const auto put = [&](unsigned in, int p) {
+                for (; in; in &= in - 1) {
+                    const int b = __ffs(in) - 1, i = b / (P / 4), u = b / P;  // the word, the unit
+                    uint32_t v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = i & 8 ? (i & 4 ? at4(w[3], q) : at4(w[2], q)) : (i & 4 ? at4(w[1], q) : at4(w[0], q));
+                    v[0] = i & 2 ? (i & 1 ? v[3] : v[2]) : (i & 1 ? v[1] : v[0]);
+                    const int j = (u & 2 ? (u & 1 ? lo[3] : lo[2]) : (u & 1 ? lo[1] : lo[0])) + b % P;
                     float x;
-                    const uint32_t v = P == 4 ? (e == 0 ? word[0] : e == 1 ? word[1] : e == 2 ? word[2] : word[3])
-                                              : (e < 2 ? word[0] : e < 4 ? word[1] : e < 6 ? word[2] : word[3]);
-                    if constexpr (P == 4) x = __uint_as_float(v);
-                    else x = Tag::widen(static_cast<uint16_t>(e & 1 ? v >> 16 : v & 0xffffu));
-                    const unsigned long long key = order_key(x, lo[u] + e);
+                    if constexpr (P == 4) x = __uint_as_float(v[0]);
+                    else x = Tag::widen(static_cast<uint16_t>(b & 1 ? v[0] >> 16 : v[0] & 0xffffu));
+                    const unsigned long long key = order_key(x, j);
                     cand[p++] = key > above ? key : 0;
+                }
+            };
+            const int more = __reduce_add_sync(0xffffffffu, __popc(hits));
+            if (n + more <= kStreamCands) {
+                put(hits, warp_places(__popc(hits), &n));
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    __syncwarp();
+                    room_for(32 * P);
+                    const unsigned in = hits & ((1u << P) - 1u) << (u * P);
+                    put(in, warp_places(__popc(in), &n));
                 }
             }
             __syncwarp();
@@ -490,22 +523,47 @@ __device__ __forceinline__ void warp_top(const WideRow<Tag>& row, int k, const u
     };
     const int tiles = (row.body + 31) / 32;
     for (int t0 = 0; t0 < tiles; t0 += 32) {
-        const unsigned mine = t0 + lane < tiles ? tile[t0 + lane] : 0u;
-        const unsigned hit = __ballot_sync(0xffffffffu, mine != 0 && mine >= at);
-        for (int q = 0; q < 8; ++q) {  // four tiles, 128 slots at a time
-            if ((hit >> (4 * q) & 15u) == 0) continue;
-            const int s = 1 + (t0 + 4 * q) * 32 + lane;
+        // a lane to a tile, each from another slot on: 32 banks
+        const int s0 = 1 + (t0 + lane) * 32;
+        const unsigned big_tile = t0 + lane < tiles ? tile[t0 + lane] : 0u;
+        const auto scan = [&]() {
             unsigned in = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const unsigned o = s + 32 * u <= row.body ? big[s + 32 * u] : 0u;
-                const unsigned long long first = static_cast<unsigned long long>(o) << 32 |
-                                                 (0xffffffffu - static_cast<unsigned>(row.slot_begin(s + 32 * u)));
-                if (o != 0 && first > above) in |= 1u << u;
+            if (big_tile == 0 || big_tile < at) return in;
+            const unsigned least_big = at > 0 ? at : 1u;
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+                const unsigned o = big[min(s0 + ((i + lane) & 31), row.body)];
+                in |= static_cast<unsigned>(o >= least_big) << i;
             }
+            in = __funnelshift_l(in, in, lane);
+            if (row.body - s0 < 31) in &= (2u << (row.body - s0)) - 1u;
+            if (const unsigned kept = static_cast<unsigned>(above)) {
+                // a largest element that equals `at` has to come before the last of those that were kept
+                for (unsigned rest = in; rest; rest &= rest - 1) {
+                    const int q = __ffs(rest) - 1;
+                    if (big[s0 + q] == at && 0xffffffffu - static_cast<unsigned>(row.slot_begin(s0 + q)) <= kept) in ^= 1u << q;
+                }
+            }
+            return in;
+        };
+        const auto pick = [&](unsigned in) {
             int p = warp_places(__popc(in), &picked);
-            for (; in; in &= in - 1) list[p++] = static_cast<unsigned short>(s + 32 * (__ffs(in) - 1));
-            if (picked > kStreamList - 128) look();
+            for (; in; in &= in - 1) list[p++] = static_cast<unsigned short>(s0 + __ffs(in) - 1);
+        };
+        const bool any = __any_sync(0xffffffffu, big_tile != 0 && big_tile >= at);
+        if (!any) continue;  // (of the whole warp)
+        const unsigned in = scan();
+        const int more = __reduce_add_sync(0xffffffffu, __popc(in));
+        if (picked + more > kStreamList) look();
+        if (more <= kStreamList) {
+            pick(in);
+        } else {  // (ties) a quarter at a time, as what was kept by then allows
+#pragma unroll 1
+            for (int part = 0; part < 32; part += 8) {
+                if (picked > kStreamList - 8 * 32) look();
+                __syncwarp();
+                pick(scan() & 255u << part);
+            }
         }
     }
     look();

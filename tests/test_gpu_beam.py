@@ -131,6 +131,28 @@ def test_more_ties_than_are_ranked(dtype):
     assert r.tokens[0].tolist() == list(range(100)) and r.parents[2].tolist() == [0] * 100
 
 
+@pytest.mark.parametrize("dtype,cols", [("f32", 45003), ("bf16", 90007)])
+def test_ties_in_masses(dtype, cols):
+    """Long rows of one value, of few, and of few near the end: first alternatives, ties by the index."""
+    items, beams, k = 19, 16, 40
+    x = torch.zeros(items, beams, cols, device="cuda", dtype=DT[dtype])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[1::3] = torch.randint(0, 3, x[1::3].shape, device="cuda", generator=g).to(x.dtype)
+    x[2::3, :, cols - 5000:] = torch.randint(0, 2, (6, beams, 5000), device="cuda", generator=g).to(x.dtype)
+    x[4, 3] = -float("inf")
+    x[4, 3, ::700] = 1.0
+    want = torch.stack([torch.sort(x[i], dim=-1, descending=True, stable=True).indices[:, :k] for i in range(items)])
+    got = A.token_logprobs(x.view(-1, cols), None, top_k=k)
+    assert torch.equal(got.top_ids.view(items, beams, k), want)
+    # one beam of each item has begun
+    scores = torch.full((items, beams), -float("inf"), device="cuda")
+    begun = torch.arange(items, device="cuda") % beams
+    scores[torch.arange(items, device="cuda"), begun] = -1.0
+    r = A.beam_select(x, scores, k)
+    assert torch.equal(r.tokens, want[torch.arange(items, device="cuda"), begun])
+    assert torch.equal(r.parents, begun[:, None].expand(items, k))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_options(dtype):
     rng, x, scores = data(6, 5, 3001, 7)
