@@ -604,7 +604,8 @@ argr_status argreduce_route(const void* x, argr_dtype dtype, int64_t rows, int64
  * balance with respect to x, choice and counts held fixed; each of the three may be NULL (zero). ids,
  * weights, lse, counts and taken as argreduce_route() wrote them for the same x
  * (ids and weights are needed with grad_weights, counts and taken with
- * grad_balance). Rows with lse -inf are not looked at and get 0. grad as in
+ * grad_balance). Rows with lse -inf are not looked at and get 0; p is divided by the
+ * row's own sum, so it is as exact far from zero as near it. grad as in
  * argreduce_logprobs_backward().
  */
 argr_status argreduce_route_backward(const void* x, argr_dtype dtype, int64_t rows, int64_t experts,

@@ -9,6 +9,9 @@
 // and with c_e = g_balance E counts_e / (k N^2), g the weights' gradients, h the log-sum-exp's
 //     dx_e = p_e (c_e - sum_j c_j p_j + h [- sum_i g_i w_i where not normalised])
 //            + [e is chosen i] w_i (g_i [- sum_j g_j w_j where normalised]).
+// The gradient sums e = exp(x - lse) of a row again and takes p = e / sum e. With a binary32 lse, e itself is off by |lse| 2^-24, and by a
+// factor of E where a row is the type's lowest value throughout (lse = m + ln s has lost ln s); what lse is off by is
+// common to a row's e, and at most about ln s, so the quotient is as exact far from zero as near it.
 //
 // Two phases. A row is read once, by G lanes of a warp, in blocks of 8 elements dealt to the lanes in turns, the warp's
 // 32 / G rows side by side: sums, p, and the largest element of each block, which goes to shared memory. Then, for
@@ -37,6 +40,20 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = G / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+// Both sums in every lane: each half of the group takes on one of them, so that two cost one exchange more than one does.
+template <int G>
+__device__ __forceinline__ void group_sums(float& a, float& b) {
+    if constexpr (G > 1) {
+        const bool upper = threadIdx.x & (G / 2);
+        const float away = upper ? a : b, stays = upper ? b : a;
+        float v = stays + __shfl_xor_sync(0xffffffffu, away, G / 2);
+#pragma unroll
+        for (int o = G / 4; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const float w = __shfl_xor_sync(0xffffffffu, v, G / 2);
+        a = upper ? w : v;
+        b = upper ? v : w;
+    }
 }
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
@@ -517,14 +534,16 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
             const float lse = __shfl_sync(0xffffffffu, my_lse, row), h = __shfl_sync(0xffffffffu, my_h, row);
             const float a = __shfl_sync(0xffffffffu, along, row * LG);
             const bool on = live >> row & 1u;
-            float dot = 0.0f;
+            float s = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 d[j] = on ? ex2((d[j] - lse) * kLog2E) : 0.0f;
+                s += d[j];
                 dot += d[j] * c[j];
             }
-            dot = pr.grad_balance ? group_sum<G>(dot) : 0.0f;
-            const float rest = h - dot - (pr.normalize ? 0.0f : a);
+            group_sums<G>(s, dot);
+            const float inv = on ? __fdividef(1.0f, s) : 0.0f;  // (s is near 1, or E; off by two units at most)
+            const float rest = (h - dot * inv - (pr.normalize ? 0.0f : a)) * inv;
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -533,10 +552,10 @@ __global__ void __launch_bounds__(kRouteBlock, V <= 8 ? 2 : 1) route_grad_kernel
                     v = *mine;
                     *mine = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
-                d[j] = d[j] * (c[j] + rest) + v.x;
-                d[j + 1] = d[j + 1] * (c[j + 1] + rest) + v.y;
-                d[j + 2] = d[j + 2] * (c[j + 2] + rest) + v.z;
-                d[j + 3] = d[j + 3] * (c[j + 3] + rest) + v.w;
+                d[j] = d[j] * fmaf(c[j], inv, rest) + v.x;
+                d[j + 1] = d[j + 1] * fmaf(c[j + 1], inv, rest) + v.y;
+                d[j + 2] = d[j + 2] * fmaf(c[j + 2], inv, rest) + v.z;
+                d[j + 3] = d[j + 3] * fmaf(c[j + 3], inv, rest) + v.w;
             }
             if (!on) {
 #pragma unroll

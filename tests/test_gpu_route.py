@@ -115,6 +115,36 @@ def test_masks(dtype, normalize, experts, k):
     check(x[5:13], dtype, k, normalize, np.zeros(8, bool))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("experts,k", [(8, 2), (16, 3), (20, 6), (60, 4), (100, 5), (200, 12), (500, 8), (1000, 4)])
+def test_gradient_of_rows_far_from_zero(dtype, normalize, experts, k):
+    """Rows whose lse, a binary32 number, says little or nothing of their sum: a large common offset, the type's
+    lowest value throughout, its largest. Each p is still exp(x - m) / s, so the bound has no part that grows with lse."""
+    rng = np.random.Generator(np.random.PCG64(experts))
+    high = {"f32": 3e7, "f16": 60000.0, "bf16": 1e5}[dtype]
+    offsets = np.array([0.0, 1000.0, -1000.0, 30000.0, -30000.0, high, -high])
+    x = rng.normal(size=(40, experts)) + offsets[np.arange(40) % len(offsets)][:, None]
+    x[5] = LOWEST[dtype]
+    x[6] = -LOWEST[dtype]
+    x[7, 1:] = LOWEST[dtype]
+    x[8] = LOWEST[dtype]
+    x[8, experts // 2:] = -np.inf
+    xd, x64 = on_gpu(x, dtype)
+    r = A.route_topk(xd, k, normalize=normalize, balance=True)
+    w, ids, lse, counts, n, _ = ref.route(x64, k, normalize)
+    assert (r.ids.cpu().numpy() == ids).all() and (r.counts.cpu().numpy() == counts).all() and r.rows.item() == n
+    for on in ("w", "h", "b", "whb"):
+        g = rng.normal(size=(40, k)).astype(np.float32) * ("w" in on)
+        h = rng.normal(size=40).astype(np.float32) * ("h" in on)
+        b = np.float32(rng.normal() * 40 * ("b" in on))
+        want, size = ref.route_grad(x64, ids, counts, n, k, g.astype(np.float64), h.astype(np.float64), float(b), normalize)
+        cuda = lambda a, name: torch.from_numpy(np.asarray(a)).cuda() if name in on else None  # noqa: E731
+        got = A.route_topk_backward(xd, r.weights, r.ids, r.lse, r.counts, r.rows, normalize=normalize,
+                                    grad_weights=cuda(g, "w"), grad_lse=cuda(h, "h"), grad_balance=cuda(b, "b"))
+        close(got, want, logits_ref.grad_bound(want, 2 * size, experts, dtype), f"gradient of {on}")
+
+
 @pytest.mark.parametrize("what", [np.nan, np.inf])
 def test_rows_with_a_mistake(what):
     rng = np.random.Generator(np.random.PCG64(4))
