@@ -29,6 +29,7 @@ namespace argr {
 constexpr int kMaxBeams = ARGR_BEAM_MAX_BEAMS;
 constexpr int kMergeBlock = 512;
 constexpr int kMergeMax = 256;  // entries ranked by counting, at most
+constexpr int kMergeEntries = kMaxBeams * ARGR_LOGITS_MAX_TOP;  // of all lists
 
 // What the merge knows of a beam.
 struct BeamSum {
@@ -75,7 +76,7 @@ __device__ __forceinline__ double minus_log(double base, float s) {
 struct MergeShared {
     BeamSum beam[kMaxBeams];
     unsigned long long key[kMergeMax];
-    int from[kMergeMax];
+    unsigned long long place[kMergeMax];
     int win[ARGR_LOGITS_MAX_TOP];
     unsigned low[32], high[32];
     int poisoned, n;
@@ -193,13 +194,21 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
             if (n <= slack) break;
         }
     }
+    // Which of two entries of the same rank is first: the lower beam's, within a beam the larger logit, then the lower index. A list
+    // is in this order (and there are kMergeEntries at most); the parts of a beam's row are lists of their own, in which
+    // different logits may have totals that round to one binary64 value.
+    const auto place_of = [&](int i) {
+        if (shift == 0) return static_cast<unsigned long long>(i);
+        const unsigned later = ~static_cast<unsigned>(gathered[i] >> 32);
+        return (static_cast<unsigned long long>(i / (k << shift)) << 32 | later) * kMergeEntries + i;
+    };
     for (int i = t; i < all; i += nt) {
         const unsigned long long key = keys[i];
         if (key == 0 || static_cast<unsigned>(key >> 32) < at) continue;
         const int p = atomicAdd(&sh.n, 1);
         if (p < kMergeMax) {
             sh.key[p] = key;
-            sh.from[p] = i;
+            sh.place[p] = place_of(i);
         }
     }
     __syncthreads();
@@ -215,16 +224,16 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
         for (int q0 = 0; q0 < n; q0 += nt / 4) {
             const int q = q0 + (t >> 2);
             const unsigned long long key = q < n ? sh.key[q] : 0ull;
-            const int i = q < n ? sh.from[q] : 0;
+            const unsigned long long place = q < n ? sh.place[q] : 0ull;
             int r = 0;
 #pragma unroll 4
             for (int j = t & 3; j < n; j += 4) {
                 const unsigned long long other = sh.key[j];
-                r += other > key || (other == key && sh.from[j] < i);
+                r += other > key || (other == key && sh.place[j] < place);
             }
             r += __shfl_xor_sync(0xffffffffu, r, 1);
             r += __shfl_xor_sync(0xffffffffu, r, 2);
-            if (q < n && (t & 3) == 0 && r < count) put(r, i, key);
+            if (q < n && (t & 3) == 0 && r < count) put(r, static_cast<int>(place % kMergeEntries), key);
         }
         for (int r = n + t; r < count; r += nt) {
             pr.tokens[item * count + r] = -1;
@@ -240,13 +249,26 @@ __device__ __forceinline__ void merge_beams(const BeamProblem& pr, int64_t item,
 #pragma unroll
         for (int j = 0; j < 2; ++j) head[j] = 2 * lane + j < lists ? keys[(2 * lane + j) * k] : 0ull;
         for (int r = 0; r < count; ++r) {  // (more than kMergeMax entries are there)
-            const int j = head[1] > head[0];
+            int j = head[1] > head[0];
+            if (shift > 0 && head[1] == head[0] && head[1] != 0)  // two lists of one beam
+                j = gathered[(2 * lane + 1) * k + p[1]] > gathered[2 * lane * k + p[0]];
             const unsigned long long h = j ? head[1] : head[0];
             const unsigned hi = static_cast<unsigned>(h >> 32), top = __reduce_max_sync(0xffffffffu, hi);
             const unsigned lo = hi == top ? static_cast<unsigned>(h) : 0u;
             const unsigned least = __reduce_max_sync(0xffffffffu, lo);
             const bool best = hi == top && lo == least;
-            const unsigned holds = __ballot_sync(0xffffffffu, best);
+            unsigned holds = __ballot_sync(0xffffffffu, best);
+            if (shift > 0) {
+                // of the lowest of these beams, the largest logit
+                const int l = 2 * lane + j, beam = 2 * (__ffs(holds) - 1) >> shift;
+                const bool in = best && l >> shift == beam;
+                const unsigned long long g = in ? gathered[l * k + (j ? p[1] : p[0])] : 0ull;
+                const unsigned g_hi = static_cast<unsigned>(g >> 32), g_top = __reduce_max_sync(0xffffffffu, g_hi);
+                const unsigned g_lo = g_hi == g_top ? static_cast<unsigned>(g) : 0u;
+                const unsigned g_least = __reduce_max_sync(0xffffffffu, g_lo);
+                const bool first = in && g_hi == g_top && g_lo == g_least;
+                holds = __ballot_sync(0xffffffffu, first);
+            }
             if (lane == __ffs(holds) - 1) {
                 const int l = 2 * lane + j, i = j ? p[1] : p[0];
                 sh.win[r] = l * k + i;

@@ -153,6 +153,30 @@ def test_ties_in_masses(dtype, cols):
     assert torch.equal(r.parents, begun[:, None].expand(items, k))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("beams,cols,count", [(1, 200003, 5), (2, 131072, 8), (2, 131072, 32), (2, 131080, 64), (4, 80001, 128), (3, 40000, 20)])
+def test_order_within_a_beam_read_by_several_ctas(dtype, beams, cols, count):
+    """Different logits whose totals round to the same binary64 value: the larger logit is first, wherever it lies."""
+    g = torch.Generator(device="cuda").manual_seed(count)
+    x = torch.randn(2, beams, cols, device="cuda", generator=g).to(DT[dtype])
+    x[1, 0, cols // 3] = 1e30  # beside it, the other logits vanish
+    scores = -torch.arange(2.0 * beams, device="cuda").view(2, beams)
+    best = torch.sort(x.float(), dim=-1, descending=True, stable=True).indices[..., :count]
+    r = A.beam_select(x, scores, count, temperature=1e30)  # all totals of a beam are alike
+    assert torch.equal(r.tokens[0], best[0, 0]) and (r.parents[0] == 0).all()
+    first = torch.full_like(scores, -np.inf)
+    first[:, 0] = -1.0
+    r = A.beam_select(x, first, count)
+    assert torch.equal(r.tokens, best[:, 0]) and (r.parents == 0).all()
+    # where the lists of other beams lie between
+    for temperature in (1.0, 1e30):
+        r = A.beam_select(x, scores, count, temperature=temperature)
+        for i in range(2):
+            for b in range(beams):
+                mine = r.tokens[i][r.parents[i] == b]
+                assert torch.equal(mine, best[i, b, :len(mine)]), (temperature, i, b)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_options(dtype):
     rng, x, scores = data(6, 5, 3001, 7)
