@@ -51,6 +51,11 @@ class DistillLoss(NamedTuple):
 _CODES = {torch.float32: _lib.ARGR_F32, torch.float16: _lib.ARGR_F16, torch.bfloat16: _lib.ARGR_BF16}
 
 
+def _no_tangent(t):
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise NotImplementedError("forward-mode differentiation of operators over rows of scores (the tangent would be lost)")
+
+
 def _rows(x, dtype):
     """(rows, cols, row stride, type code) of logits."""
     if not x.is_cuda:
@@ -58,8 +63,7 @@ def _rows(x, dtype):
     if x.get_device() != _current_device():
         raise ValueError(f"logits are on cuda:{x.get_device()}, but the current device is cuda:{_current_device()} "
                          "(the library plans and launches there: enter torch.cuda.device(logits.device))")
-    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(x).tangent is not None:
-        raise NotImplementedError("forward-mode differentiation of the vocabulary rows (the tangent would be lost)")
+    _no_tangent(x)
     code = _CODES.get(x.dtype) if dtype is None else dtype_code(x, dtype)
     if code is None or code > _lib.ARGR_BF16:
         raise TypeError("logits must be float32, float16 or bfloat16")
@@ -90,6 +94,8 @@ def _arg(t, what, dtype, shape, device):
     if t is None:
         return None
     if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if dtype is _F32:
+            _no_tangent(t)
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")

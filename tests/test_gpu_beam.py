@@ -505,6 +505,29 @@ def test_select_refuses():
             call()
 
 
+def test_tangents_of_the_other_arguments_are_refused():
+    import torch.autograd.forward_ad as fwd
+    x, s = torch.randn(2, 3, 20, device="cuda"), torch.zeros(2, 3, device="cuda")
+    ones = torch.ones(2, 3, device="cuda")
+    y = torch.randn(6, 20, device="cuda")
+    r = A.route_topk(y, 2, balance=True)
+    t = A.token_logprobs(y, torch.zeros(6, dtype=torch.int64, device="cuda"), with_stats=True)
+    one, two, loss = torch.ones(6, device="cuda"), torch.ones(6, 2, device="cuda"), torch.ones((), device="cuda")
+    with fwd.dual_level():
+        dual = lambda v: fwd.make_dual(v, torch.ones_like(v))  # noqa: E731
+        back = lambda weights=r.weights, lse=r.lse, **g: A.route_topk_backward(y, weights, r.ids, lse, r.counts, r.rows, **g)  # noqa: E731
+        for call in (lambda: A.beam_select(x, dual(s), 2), lambda: A.beam_select(x, s, 2, scale=dual(ones)),
+                     lambda: back(weights=dual(r.weights), grad_weights=two), lambda: back(lse=dual(r.lse), grad_lse=one),
+                     lambda: back(grad_weights=dual(two)), lambda: back(grad_lse=dual(one)), lambda: back(grad_balance=dual(loss)),
+                     lambda: A.token_logprobs_backward(y, None, t.stats, grad_lse=dual(one)),
+                     lambda: A.distill_topk(y, r.ids, dual(two))):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        # and without a tangent all is as ever
+        A.beam_select(x, s, 2, scale=ones)
+        assert torch.equal(back(grad_lse=one), A.route_topk_backward(y, r.weights, r.ids, r.lse, grad_lse=one))
+
+
 @pytest.mark.parametrize("graph", [False, True])
 def test_search(graph):
     """A whole search: a model whose logits are a function of the last two tokens, its states reordered and

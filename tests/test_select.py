@@ -193,6 +193,20 @@ def test_what_lies_on_the_cpu_is_refused():
             call()
 
 
+def test_an_argument_with_a_tangent_is_refused():
+    torch = pytest.importorskip("torch")
+    from torch.autograd import forward_ad
+    from row_wise_arg_gb300.logits import _arg
+    t = torch.ones(3, 2)
+    arg = lambda v, dtype: _arg(v, "scores", dtype, (3, 2), t.device)  # noqa: E731
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(t, torch.ones(3, 2))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            arg(dual, torch.float32)
+        assert arg(t, torch.float32) == t.data_ptr() and arg(t > 0, torch.bool)
+    assert arg(t, torch.float32) == t.data_ptr() and arg(None, torch.float32) is None
+
+
 def test_apart():
     pytest.importorskip("torch")
     from row_wise_arg_gb300.beam import _apart
