@@ -10,6 +10,7 @@ semantics stand).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -38,6 +39,12 @@ def _no_gradient(what, *tensors):
         if t is None or not t.requires_grad:
             continue
         raise RuntimeError(f"{what} has no gradient: call it under torch.no_grad(), or on detached tensors")
+
+
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(device, items, beams, cols, code, count):
+    """What the library's plan for such a step on the current device, `device`, asks for (kept: the call into it takes 1 us)."""
+    return _LIB.argreduce_beam_scratch_bytes(items, beams, cols, code, count)
 
 
 def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, scale=None, temperature: float = 1.0,
@@ -78,7 +85,7 @@ def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, s
             tokens.data_ptr(), parents.data_ptr(), totals.data_ptr())
     handle = _stream_ptr(None, dev.index) or None
     # many rows need scratch; it is this call's own: torch keeps it until the stream has passed the call
-    nbytes = _LIB.argreduce_beam_scratch_bytes(rows // beams, beams, cols, code, count) if rows > 16 else 0
+    nbytes = _scratch_bytes(dev.index, rows // beams, beams, cols, code, count)
     scratch = _empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     st = _LIB.argreduce_beam_select(*args, scratch.data_ptr() if nbytes else None, nbytes, handle)
     if st != ARGR_OK:

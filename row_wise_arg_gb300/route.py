@@ -8,6 +8,7 @@ automatic differentiation: weights, lse and balance have gradients to the logits
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -38,6 +39,12 @@ def _shape_of(x, dtype):
     return rows, experts, stride, code
 
 
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(device, rows, experts):
+    """What the library's plan for counts of such a route on the current device, `device`, asks for (kept: the call into it takes 1 us)."""
+    return _LIB.argreduce_route_scratch_bytes(rows, experts)
+
+
 def _forward(x, top_k, valid, normalize, counts, balance, dtype):
     rows, experts, stride, code = _shape_of(x, dtype)
     lead, dev = x.shape[:-1], x.device
@@ -58,7 +65,7 @@ def _forward(x, top_k, valid, normalize, counts, balance, dtype):
             lse.data_ptr(), p_n, p_taken, p_loss)
     handle = _stream_ptr(None, dev.index) or None
     # many rows need scratch for the counts; it is this call's own: torch keeps it until the stream has passed the call
-    nbytes = _LIB.argreduce_route_scratch_bytes(rows, experts) if n is not None and rows > 256 else 0
+    nbytes = _scratch_bytes(dev.index, rows, experts) if n is not None else 0
     scratch = _empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     st = _LIB.argreduce_route(*args, scratch.data_ptr() if nbytes else None, nbytes, handle)
     if st != ARGR_OK:

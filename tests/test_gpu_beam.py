@@ -528,6 +528,36 @@ def test_tangents_of_the_other_arguments_are_refused():
         assert torch.equal(back(grad_lse=one), A.route_topk_backward(y, r.weights, r.ids, r.lse, grad_lse=one))
 
 
+@pytest.mark.parametrize("items,beams", [(1, 2), (4, 4), (1, 16), (20, 17)])
+def test_scratch_is_what_the_library_asks_for(monkeypatch, items, beams):
+    """Also for few rows: which steps need scratch is the library's plan alone."""
+    from row_wise_arg_gb300 import beam
+    asked, given = [], []
+
+    class Library:
+        def __getattr__(self, name):
+            return getattr(beam_lib, name)
+
+        def argreduce_beam_scratch_bytes(self, *a):
+            asked.append(a)
+            return beam_lib.argreduce_beam_scratch_bytes(*a) + 4096
+
+        def argreduce_beam_select(self, *a):
+            given.append(a[-3:-1])
+            return beam_lib.argreduce_beam_select(*a)
+
+    beam_lib = beam._LIB
+    x, s = torch.randn(items, beams, 700, device="cuda"), -torch.rand(items, beams, device="cuda")
+    want = A.beam_select(x, s, 4)
+    beam._scratch_bytes.cache_clear()
+    monkeypatch.setattr(beam, "_LIB", Library())
+    got = A.beam_select(x, s, 4)
+    beam._scratch_bytes.cache_clear()
+    need = beam_lib.argreduce_beam_scratch_bytes(items, beams, 700, 0, 4) + 4096
+    assert asked and given[0][0] and given[0][1] == need
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("graph", [False, True])
 def test_search(graph):
     """A whole search: a model whose logits are a function of the last two tokens, its states reordered and

@@ -284,6 +284,35 @@ def test_shapes_streams_and_graphs():
         assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("rows,experts", [(1, 8), (256, 1024), (257, 1024), (5000, 64)])
+def test_scratch_is_what_the_library_asks_for(monkeypatch, rows, experts):
+    """Also for few rows: which routes need scratch is the library's plan alone."""
+    from row_wise_arg_gb300 import route
+    given = []
+
+    class Library:
+        def __getattr__(self, name):
+            return getattr(lib, name)
+
+        def argreduce_route_scratch_bytes(self, *a):
+            return lib.argreduce_route_scratch_bytes(*a) + 4096
+
+        def argreduce_route(self, *a):
+            given.append(a[-3:-1])
+            return lib.argreduce_route(*a)
+
+    lib = route._LIB
+    x = torch.randn(rows, experts, device="cuda")
+    want = A.route_topk(x, 4, balance=True)
+    route._scratch_bytes.cache_clear()
+    monkeypatch.setattr(route, "_LIB", Library())
+    got, plain = A.route_topk(x, 4, balance=True), A.route_topk(x, 4)
+    route._scratch_bytes.cache_clear()
+    assert given[0][0] and given[0][1] == lib.argreduce_route_scratch_bytes(rows, experts) + 4096
+    assert given[1] == (None, 0)  # nothing is counted
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(plain.ids, want.ids)
+
+
 def test_training_step():
     """A layer of experts: routed, balanced, trained; against the same in 64 bits, automatic differentiation of both."""
     torch.manual_seed(1)
