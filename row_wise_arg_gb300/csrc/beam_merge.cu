@@ -28,9 +28,4 @@ cudaError_t launch_beam_merge(const BeamProblem& pr) {
                           pr.rows.stream, pr, kLog2E / pr.rows.temperature);
 }
 
-size_t beam_scratch_bytes(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps) {
-    const BeamPlan b = plan_beams(items, beams, cols, dtype, k, caps);
-    return b.cluster ? 0 : 8 * static_cast<size_t>(items) * beams * (k + 1);
-}
-
 }  // namespace argr

@@ -418,62 +418,8 @@ __global__ void __launch_bounds__(BLOCK, PER_SM) beam_rows_kernel(const LogitsPr
     for (int i = t; i < k; i += blockDim.x) pr.beam_keys[r * k + i] = i < have ? sh.best[i] : 0ull;
 }
 
-// (one instance, in select_f32.cu)
+// (beam_merge.cu)
 cudaError_t launch_beam_merge(const BeamProblem& pr);
-
-// The plan of a step: one cluster per item, 1 << shift CTAs to a beam, or (cluster == 0) rows and merge.
-struct BeamPlan {
-    int cluster, shift, block;
-    bool stream;
-};
-
-// Whether rows go to the persistent kernel, and its plan: those that the planner of token_logprobs streams, and last rounds
-// that three quarters of the CTAs take part in (it asks for 85%; without entropies a round is shorter).
-inline bool beam_stream_plan(int64_t rows, int64_t cols, int dtype, int k, const argr_caps& caps, argr_plan* p) {
-    const int64_t ctas = 2 * static_cast<int64_t>(caps.sm_count), rounds = (rows + ctas - 1) / ctas;
-    if (rows * 100 < rounds * ctas * 75) return false;
-    return make_logits_plan(ARGR_LOGITS_LOGPROBS, rounds * ctas, cols, dtype, k, caps, p) == ARGR_OK &&
-           p->path == ARGR_PATH_LOGITS_STREAM;
-}
-
-// A cluster's CTAs start together, wait for one another, and hold their SMs while CTA 0 merges, which costs little while
-// the grid leaves room for the next one's clusters. So, for up to 16 beams: a CTA per beam, and several to a beam while
-// they are two thirds of the SMs at most and have 64 KB each. Of 4 beams with 1, 2, 4
-// CTAs each, 8 continuations, us in a graph of calls: [1, 4, 32000] f32 7.9, 8.0, 9.3; [1, 4, 202048] bf16 13.3, 10.9, 11.0;
-// [4, 4, 128000] bf16 11.0, 9.6, 10.3; [16, 4, 202048] bf16 14.8, 20.7, 26.6. Clusters of up to 8 CTAs are kept up to two
-// waves, those of 16 up to one (they find few places): cluster against a CTA per row and a merge,
-// [64, 4, 128000] bf16 17.5 / 22.3 (streaming 24.6), [60, 4, 32000] 9.8 / 11.7, [30, 8, 32000] 10.7 / 12.7, but [19, 16, 202048], 32
-// continuations, 60.6 / 53.3 (streaming 49.2), [19, 16, 32000] 25.8 / 24.6 (21.2 with 128 threads). Past that long rows are
-// streamed ([64, 16, 202048], 32: 92, against 107.8 with a CTA per row).
-inline BeamPlan plan_beams(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps) {
-    BeamPlan p = {};
-    const int64_t groups = cols / (dtype == ARGR_F32 ? 16 : 32), rows = items * beams;
-    const int most = caps.max_cluster < 16 ? caps.max_cluster : 16;
-    int64_t per_cta = groups, n = rows;
-    argr_plan q;
-    if (beams <= most && rows <= (beams <= 8 ? 2 : 1) * static_cast<int64_t>(caps.sm_count)) {
-        p.cluster = beams;
-        while (2 * p.cluster <= most && 3 * items * p.cluster <= caps.sm_count && (groups >> (p.shift + 1)) >= 1024) {
-            p.cluster *= 2;
-            ++p.shift;
-        }
-        per_cta = groups >> p.shift;
-        n = items * p.cluster;
-    } else {
-        p.stream = beam_stream_plan(rows, cols, dtype, k, caps, &q);
-    }
-    p.block = p.cluster ? 512 : 256;
-    if (n > caps.sm_count) {
-        p.block = 256;
-        while (p.block > 32 && per_cta <= 8 * p.block &&
-               n > (p.block == 256 ? 3 : 640 / p.block) * static_cast<int64_t>(caps.sm_count))
-            p.block /= 2;
-        while (p.block < 256 && p.block < 2 * k) p.block *= 2;
-    } else {
-        while (p.block > 32 && p.block / 2 >= per_cta && p.block > 2 * k) p.block /= 2;
-    }
-    return p;
-}
 
 template <class Tag>
 int beam_seg_slots(int cols, int shift) {
@@ -481,25 +427,50 @@ int beam_seg_slots(int cols, int shift) {
     return static_cast<int>((parts < kSegGroups ? parts : kSegGroups) + 2 + 3) / 4 * 4;
 }
 
-template <class Tag, int BLOCK, int PER_SM>
-cudaError_t launch_beam_cluster(const BeamProblem& pr, const BeamPlan& b) {
-    auto kern = beam_select_kernel<Tag, BLOCK, PER_SM>;
-    static KernelLaunchCache cache;
-    const int seg_slots = beam_seg_slots<Tag>(pr.rows.cols, b.shift);
-    const size_t smem = BeamLayout(pr.rows.top_k, pr.beams << b.shift, seg_slots, kGroupElems<Tag>).total;
-    cudaError_t e = ensure_smem_limit(kern, smem + sizeof(MergeShared) + 1024, cache);  // with the static part
-    if (e != cudaSuccess) return e;
-    if (b.cluster > 1) {
-        bool ok = false;
-        if (b.cluster > 8 && (e = allow_big_cluster(kern, cache)) != cudaSuccess) return e;
-        if ((e = cluster_fits(kern, dim3(static_cast<unsigned>(b.cluster)), b.block, b.cluster, smem, cache, &ok)) != cudaSuccess)
-            return e;
-        if (!ok) return cudaErrorInvalidClusterSize;
+// The kernel of a cluster per item: its launch's cache and shared memory.
+template <class Tag>
+struct BeamCluster {
+    static constexpr auto kernel() { return beam_select_kernel<Tag, 512, 1>; }
+    static KernelLaunchCache& cache() {
+        static KernelLaunchCache c;
+        return c;
     }
+    int seg_slots;
+    size_t smem;
+    BeamCluster(int beams, int cols, int k, const BeamPlan& b)
+        : seg_slots(beam_seg_slots<Tag>(cols, b.shift)), smem(BeamLayout(k, beams << b.shift, seg_slots, kGroupElems<Tag>).total) {}
+
+    cudaError_t allow(const BeamPlan& b) const {
+        const cudaError_t e = ensure_smem_limit(kernel(), smem + sizeof(MergeShared) + 1024, cache());  // with the static part
+        return e == cudaSuccess && b.cluster > 8 ? allow_big_cluster(kernel(), cache()) : e;
+    }
+    // Whether the current device places such clusters.
+    cudaError_t fits(const BeamPlan& b, bool* ok) const {
+        cudaError_t e = allow(b);
+        if (e == cudaSuccess)
+            e = cluster_fits(kernel(), dim3(static_cast<unsigned>(b.cluster)), b.block, b.cluster, smem, cache(), ok);
+        if (e != cudaErrorInvalidClusterSize) return e;
+        cudaGetLastError();
+        *ok = false;
+        return cudaSuccess;
+    }
+};
+
+template <class Tag>
+cudaError_t beam_plan_t(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps, BeamPlan* p) {
+    const auto fits = [&](const BeamPlan& b, bool* ok) { return BeamCluster<Tag>(beams, static_cast<int>(cols), k, b).fits(b, ok); };
+    return fitting_beam_plan(items, beams, cols, dtype, k, caps, fits, p);
+}
+
+template <class Tag>
+cudaError_t launch_beam_cluster(const BeamProblem& pr, const BeamPlan& b) {
+    const BeamCluster<Tag> c(pr.beams, pr.rows.cols, pr.rows.top_k, b);
+    const cudaError_t e = c.allow(b);
+    if (e != cudaSuccess) return e;
     argr_plan p = {};
     p.flags = ARGR_PLAN_PDL;
-    return launch_ex_smem(kern, dim3(static_cast<unsigned>(pr.items * b.cluster)), dim3(b.block), b.cluster, smem, p,
-                          pr.rows.stream, pr, kLog2E / pr.rows.temperature, b.cluster, b.shift, seg_slots);
+    return launch_ex_smem(c.kernel(), dim3(static_cast<unsigned>(pr.items * b.cluster)), dim3(b.block), b.cluster, c.smem, p,
+                          pr.rows.stream, pr, kLog2E / pr.rows.temperature, b.cluster, b.shift, c.seg_slots);
 }
 
 template <class Tag, int BLOCK, int PER_SM>
@@ -530,11 +501,8 @@ cudaError_t launch_beam_stream(const BeamProblem& pr, const argr_caps& caps) {
 }
 
 template <class Tag>
-cudaError_t launch_beam_select_t(const BeamProblem& pr, const argr_caps& caps) {
-    const BeamPlan b = plan_beams(pr.items, pr.beams, pr.rows.cols, pr.rows.dtype, pr.rows.top_k, caps);
-    if (b.cluster) {
-        return launch_beam_cluster<Tag, 512, 1>(pr, b);
-    }
+cudaError_t launch_beam_select_t(const BeamProblem& pr, const BeamPlan& b, const argr_caps& caps) {
+    if (b.cluster) return launch_beam_cluster<Tag>(pr, b);
     const cudaError_t e = b.stream        ? launch_beam_stream<Tag>(pr, caps)
                           : b.block > 128 ? launch_beam_rows<Tag, 256, 3>(pr, b)
                                           : launch_beam_rows<Tag, 128, 5>(pr, b);

@@ -646,17 +646,20 @@ cudaError_t launch_route_grad_t(const RouteProblem& pr, const argr_caps& caps) {
     return ARGR_ROUTE_GV(launch_route_grad_gv, Tag, pr, caps);
 }
 
-#define ARGR_DEFINE_SELECT(sfx, Tag)                                                          \
-    namespace argr {                                                                          \
-    cudaError_t launch_beam_select_##sfx(const BeamProblem& pr, const argr_caps& caps) {      \
-        return launch_beam_select_t<Tag>(pr, caps);                                           \
-    }                                                                                         \
-    cudaError_t launch_route_##sfx(const RouteProblem& pr, const argr_caps& caps) {           \
-        return launch_route_t<Tag>(pr, caps);                                                 \
-    }                                                                                         \
-    cudaError_t launch_route_grad_##sfx(const RouteProblem& pr, const argr_caps& caps) {      \
-        return launch_route_grad_t<Tag>(pr, caps);                                            \
-    }                                                                                         \
+#define ARGR_DEFINE_SELECT(sfx, Tag, dtype)                                                                           \
+    namespace argr {                                                                                                  \
+    cudaError_t beam_plan_##sfx(int64_t items, int beams, int64_t cols, int k, const argr_caps& caps, BeamPlan* p) {  \
+        return beam_plan_t<Tag>(items, beams, cols, dtype, k, caps, p);                                               \
+    }                                                                                                                 \
+    cudaError_t launch_beam_select_##sfx(const BeamProblem& pr, const BeamPlan& b, const argr_caps& caps) {           \
+        return launch_beam_select_t<Tag>(pr, b, caps);                                                                \
+    }                                                                                                                 \
+    cudaError_t launch_route_##sfx(const RouteProblem& pr, const argr_caps& caps) {                                   \
+        return launch_route_t<Tag>(pr, caps);                                                                         \
+    }                                                                                                                 \
+    cudaError_t launch_route_grad_##sfx(const RouteProblem& pr, const argr_caps& caps) {                              \
+        return launch_route_grad_t<Tag>(pr, caps);                                                                    \
+    }                                                                                                                 \
     }
 
 }  // namespace argr

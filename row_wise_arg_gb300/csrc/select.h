@@ -20,6 +20,29 @@ struct BeamProblem {
     float* out_scores;
 };
 
+// The plan of a step: one cluster per item, 1 << shift CTAs to a beam, or (cluster == 0) rows and merge.
+struct BeamPlan {
+    int cluster, shift, block;
+    bool stream;
+};
+// By the figures of a device that places clusters of up to caps.max_cluster CTAs (plan_beams.cpp).
+BeamPlan plan_beams(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps);
+// Whether rows are streamed, and their plan.
+bool beam_stream_plan(int64_t rows, int64_t cols, int dtype, int k, const argr_caps& caps, argr_plan* p);
+// The plan for a device of which fits(plan, &ok) says whether it places a plan's clusters: with smaller ones, or without, where it
+// does not (a part of a GPU).
+template <class Fits>
+cudaError_t fitting_beam_plan(int64_t items, int beams, int64_t cols, int dtype, int k, argr_caps caps, Fits fits, BeamPlan* p) {
+    for (;;) {
+        *p = plan_beams(items, beams, cols, dtype, k, caps);
+        if (p->cluster <= 1) return cudaSuccess;
+        bool ok = false;
+        const cudaError_t e = fits(*p, &ok);
+        if (e != cudaSuccess || ok) return e;
+        caps.max_cluster = p->cluster - 1;
+    }
+}
+
 constexpr int kReorderStates = 128;  // tensors of one launch
 
 struct ReorderProblem {
@@ -106,13 +129,12 @@ __device__ __forceinline__ float route_balance(double sum, long long rows, int e
 }
 #endif
 
-// Scratch of a step, 0 where it is one launch.
-size_t beam_scratch_bytes(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps);
 cudaError_t launch_beam_reorder(const ReorderProblem& pr, const argr_caps& caps);
 cudaError_t launch_route_finish(const RouteProblem& pr);
-#define ARGR_DECLARE_SELECT(sfx)                                                         \
-    cudaError_t launch_beam_select_##sfx(const BeamProblem& pr, const argr_caps& caps);  \
-    cudaError_t launch_route_##sfx(const RouteProblem& pr, const argr_caps& caps);       \
+#define ARGR_DECLARE_SELECT(sfx)                                                                                    \
+    cudaError_t beam_plan_##sfx(int64_t items, int beams, int64_t cols, int k, const argr_caps& caps, BeamPlan* p); \
+    cudaError_t launch_beam_select_##sfx(const BeamProblem& pr, const BeamPlan& b, const argr_caps& caps);          \
+    cudaError_t launch_route_##sfx(const RouteProblem& pr, const argr_caps& caps);                                  \
     cudaError_t launch_route_grad_##sfx(const RouteProblem& pr, const argr_caps& caps);
 ARGR_DECLARE_SELECT(f32)
 ARGR_DECLARE_SELECT(f16)

@@ -85,6 +85,14 @@ size_t route_scratch(int64_t rows, int64_t experts, const argr_caps& caps) {
     return g.cluster ? 0 : route_sums_bytes(g.ctas, experts) + 4 * static_cast<size_t>(g.ctas) * (experts + 1);
 }
 
+// Scratch of a step, 0 where it is one launch: a list and sums for every row.
+size_t beam_scratch(const BeamPlan& b, int64_t rows, int k) { return b.cluster ? 0 : 8 * static_cast<size_t>(rows) * (k + 1); }
+argr_status beam_plan(int64_t items, int beams, int64_t cols, int dtype, int k, const argr_caps& caps, BeamPlan* b) {
+    return launched(dtype == ARGR_F32   ? beam_plan_f32(items, beams, cols, k, caps, b)
+                    : dtype == ARGR_F16 ? beam_plan_f16(items, beams, cols, k, caps, b)
+                                        : beam_plan_bf16(items, beams, cols, k, caps, b));
+}
+
 }  // namespace
 }  // namespace argr
 
@@ -128,20 +136,27 @@ argr_status argreduce_beam_select(const void* x, argr_dtype dtype, int64_t items
     pr.tokens = tokens;
     pr.parents = parents;
     pr.out_scores = out_scores;
-    if (const size_t need = beam_scratch_bytes(items, beams, cols, dtype, pr.rows.top_k, caps)) {
+    BeamPlan plan;
+    if ((s = beam_plan(items, beams, cols, dtype, pr.rows.top_k, caps, &plan)) != ARGR_OK) return s;
+    if (const size_t need = beam_scratch(plan, pr.rows.rows, pr.rows.top_k)) {
         if (!scratch || misaligned(scratch, 16) || scratch_bytes < need) return ARGR_ESCRATCH;
         pr.rows.beam_keys = static_cast<unsigned long long*>(scratch);
         pr.rows.beam_sums = reinterpret_cast<float2*>(pr.rows.beam_keys + pr.rows.rows * pr.rows.top_k);
     }
-    return ARGR_SELECT_DISPATCH(launch_beam_select, dtype, pr, caps);
+    return launched(dtype == ARGR_F32   ? launch_beam_select_f32(pr, plan, caps)
+                    : dtype == ARGR_F16 ? launch_beam_select_f16(pr, plan, caps)
+                                        : launch_beam_select_bf16(pr, plan, caps));
 }
 
 size_t argreduce_beam_scratch_bytes(int64_t items, int32_t beams, int64_t cols, argr_dtype dtype, int32_t count) {
     argr_caps caps;
+    BeamPlan plan;
     if (items < 1 || beams < 1 || beams > ARGR_BEAM_MAX_BEAMS || items > INT_MAX / 64 || cols < 1 || cols > INT_MAX || count < 1 ||
         count > ARGR_LOGITS_MAX_TOP || (dtype != ARGR_F32 && dtype != ARGR_F16 && dtype != ARGR_BF16) || current_caps(&caps) != ARGR_OK)
         return 0;
-    return beam_scratch_bytes(items, beams, cols, dtype, static_cast<int>(std::min<int64_t>(count, cols)), caps);
+    const int k = static_cast<int>(std::min<int64_t>(count, cols));
+    if (beam_plan(items, beams, cols, dtype, k, caps, &plan) != ARGR_OK) return 0;
+    return beam_scratch(plan, items * beams, k);
 }
 
 argr_status argreduce_beam_reorder_check(void* const* states, int32_t n_states, int64_t items, int32_t beams,

@@ -2,4 +2,4 @@
 #include "beam_select.cuh"
 #include "route.cuh"
 
-ARGR_DEFINE_SELECT(bf16, argr::TagBF16)
+ARGR_DEFINE_SELECT(bf16, argr::TagBF16, ARGR_BF16)

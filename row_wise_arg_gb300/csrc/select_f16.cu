@@ -2,4 +2,4 @@
 #include "beam_select.cuh"
 #include "route.cuh"
 
-ARGR_DEFINE_SELECT(f16, argr::TagF16)
+ARGR_DEFINE_SELECT(f16, argr::TagF16, ARGR_F16)

@@ -2,4 +2,4 @@
 #include "beam_select.cuh"
 #include "route.cuh"
 
-ARGR_DEFINE_SELECT(f32, argr::TagF32)
+ARGR_DEFINE_SELECT(f32, argr::TagF32, ARGR_F32)

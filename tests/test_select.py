@@ -1,6 +1,8 @@
 """Beam selection, reordering and routing without a GPU: refusals before any device
 work, the geometry of states, and the definitions that the GPU tests hold the kernels to."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -129,6 +131,74 @@ def test_route_nothing_to_do():
     assert route(rows=0, x=None, weights=None, ids=None, lse=None) == OK
     assert route(rows=0, x=None, dtype=3) == _lib.ARGR_EUNSUPPORTED
     assert route_backward(rows=0, x=None, grad=None, lse=None) == OK
+
+
+# -- the plan of a step ------------------------------------------------------------------------
+PLANNER = """
+#include "select.h"
+extern "C" int plan(int64_t items, int beams, int64_t cols, int dtype, int k, int max_cluster, int placed, int* out) {
+    argr_caps caps = {};
+    caps.sm_count = 152;
+    caps.max_threads_per_sm = 2048;
+    caps.max_cluster = max_cluster;
+    argr::BeamPlan p;
+    int asked = 0;
+    const auto fits = [&](const argr::BeamPlan& b, bool* ok) {
+        ++asked;
+        *ok = b.cluster <= placed;
+        return placed < 0 ? cudaErrorInvalidValue : cudaSuccess;
+    };
+    const cudaError_t e = argr::fitting_beam_plan(items, beams, cols, dtype, k, caps, fits, &p);
+    out[0] = p.cluster;
+    out[1] = p.shift;
+    out[2] = p.block;
+    out[3] = p.stream;
+    out[4] = asked;
+    return e;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def planner(tmp_path_factory):
+    """The planner, with a device of which the caller says what clusters it places."""
+    from row_wise_arg_gb300 import build as b
+    at = tmp_path_factory.mktemp("planner")
+    (at / "planner.cpp").write_text(PLANNER)
+    so = str(at / "planner.so")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(b.nvcc()))), "include")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I" + b.INCLUDE, "-I" + b.CSRC, "-I" + cuda, str(at / "planner.cpp"),
+                    _lib.LIB_PATH, "-Wl,-rpath," + os.path.dirname(_lib.LIB_PATH), "-o", so], check=True)
+    lib = ctypes.CDLL(so)
+
+    def plan(items, beams, cols, dtype=0, k=8, max_cluster=16, placed=16):
+        out = (ctypes.c_int * 5)()
+        st = lib.plan(ctypes.c_int64(items), beams, ctypes.c_int64(cols), dtype, k, max_cluster, placed, out)
+        return (st, *out)
+    return plan
+
+
+def test_a_step_without_room_for_its_cluster(planner):
+    """Clusters that a device does not place are made smaller, then done without (rows, and a merge that needs scratch)."""
+    assert planner(1, 4, 202048, 2)[:3] == (0, 16, 2) and planner(1, 4, 202048, 2, placed=8)[:3] == (0, 8, 1)
+    assert planner(1, 1, 202048, 2)[:3] == (0, 4, 2)
+    assert planner(1, 1, 202048, 2, placed=2)[:3] == (0, 2, 1)
+    assert planner(1, 1, 202048, 2, placed=1)[:3] == (0, 1, 0)
+    assert planner(1, 4, 202048, 2, placed=4)[:3] == (0, 4, 0)
+    for beams in range(1, 17):
+        for items, cols in ((1, 1000), (2, 300000), (9, 32000)):
+            for placed in (1, 2, 3, 4, 7, 8, 12, 15, 16):
+                st, cluster, shift, block, stream, asked = planner(items, beams, cols, placed=placed)
+                assert st == 0 and asked <= 5 and 32 <= block <= 512 and not stream
+                if beams <= placed:
+                    assert cluster == beams << shift and cluster <= placed
+                    assert planner(items, beams, cols, placed=16)[1] <= placed or cluster * 2 > placed
+                else:
+                    assert cluster == 0 and shift == 0
+                # a device that says so by itself gives the same plan
+                assert planner(items, beams, cols, max_cluster=placed)[:5] == (0, cluster, shift, block, stream)
+    assert planner(1, 17, 1000)[1] == 0 and planner(1, 17, 1000)[5] == 0
+    assert planner(1, 4, 1000, placed=-1)[0] != 0  # an error is handed on
 
 
 # -- the geometry of states ------------------------------------------------------------------
