@@ -532,7 +532,8 @@ argr_status argreduce_logits_plan(argr_logits_op what, int64_t rows, int64_t col
  *   - An item with a total that is NaN or +inf, a scale (of a beam above -inf) that is
  *     not positive and finite, or a NaN or +inf among the logits it looks at
  *     gets tokens and parents -1 and totals NaN.
- * Totals are formed in binary64 and rounded once; lse_b's sum is binary32, so
+ * Totals are formed in binary64 and rounded once (one below binary32's range keeps its place by its
+ * rank and comes out as -inf, with its token and parent); lse_b's sum is binary32, so
  * continuations of different beams whose totals differ by less than about 1e-6
  * may come in either order (and equal ones, where the beams' rows do not begin
  * at the same place between two 32-byte boundaries). Within a beam the order is exact.

@@ -29,7 +29,7 @@ _MAX_BEAMS, _MAX_COUNT = _lib.BEAM_MAX_BEAMS, _lib.LOGITS_MAX_TOP
 class BeamSelection(NamedTuple):
     tokens: torch.Tensor   #: [..., count] int64, the best continuation first; -1: none was left
     parents: torch.Tensor  #: [..., count] int64, the beam that it continues; -1: none was left
-    scores: torch.Tensor   #: [..., count] float32, its total; -inf: none was left, NaN: see beam_select
+    scores: torch.Tensor   #: [..., count] float32, its total; NaN: see beam_select
 
 
 def _no_gradient(what, *tensors):
@@ -59,7 +59,8 @@ def beam_select(logits, scores, count: int, *, ended=None, end_token: int = 0, s
 
     A beam with the total -inf has no continuation, and its logits are not looked
     at (a first step: one beam has begun); neither are an ended beam's. Places that no
-    continuation above -inf is left for hold -1, -1 and -inf. An item with a NaN (or +inf) in what is looked at
+    continuation above -inf is left for hold -1, -1 and -inf (a total below float32's range is -inf too, beside its
+    token and parent). An item with a NaN (or +inf) in what is looked at
     holds -1, -1 and NaN. Totals of different beams that differ by less than about 1e-6 may come in
     either order (within a beam the order is exact). Runs on ``stream`` as ``token_logprobs`` does. There is no gradient."""
     if stream is not None and (side := _side(stream, logits)) is not None:

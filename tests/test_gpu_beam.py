@@ -177,6 +177,48 @@ def test_order_within_a_beam_read_by_several_ctas(dtype, beams, cols, count):
                 assert torch.equal(mine, best[i, b, :len(mine)]), (temperature, i, b)
 
 
+@pytest.mark.parametrize("beams", [6, 7, 9, 10, 11, 12, 13, 14, 15])
+def test_clusters_of_every_size(beams):
+    """A cluster of as many CTAs as beams, up to the last item count that gets clusters, and one more."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    most = (2 if beams <= 8 else 1) * sms // beams
+    for items in (1, 3, most, most + 1):
+        rng, x, scores = data(items, beams, 900 + beams, items)
+        ended = np.zeros((items, beams), bool)
+        ended[np.arange(items), rng.integers(0, beams - 1, items)] = True
+        ended[::3] = False
+        scores[:, -1] = -np.inf  # has not begun
+        x[:, -1] = np.nan
+        check(x, "bf16" if beams % 2 else "f32", scores, 2 * beams, ended=ended, end_token=1)
+
+
+@pytest.mark.parametrize("items", [100, 2100])
+def test_logarithm_of_the_sum(items):
+    """n logits of 0 and a total that is ln n but for its rounding to binary32: what comes out lies near 0, so the output's rounding
+    hides nothing of the merge's logarithm, which is off by less than 3e-9 (beam_select.cuh). n is an exact binary32 sum."""
+    cols = 100000
+    rng = np.random.Generator(np.random.PCG64(items))
+    n = rng.integers(1, cols + 1, items)
+    edges = [1, 2, 3, 5, 43690, 43691, 87381, 87382, 21845, 21846, 65535, 65536, 99999, 100000]  # 2/3 of powers of two, and around
+    n[:len(edges)] = edges
+    nd = torch.from_numpy(n).cuda()
+    x = torch.where(torch.arange(cols, device="cuda") < nd[:, None], 0.0, -np.inf).bfloat16()[:, None]
+    s = np.log(n.astype(np.float64)).astype(np.float32)
+    r = A.beam_select(x, torch.from_numpy(s).cuda()[:, None], 1)
+    assert (r.tokens == 0).all() and (r.parents == 0).all()
+    off = np.abs(r.scores[:, 0].double().cpu().numpy() - (s.astype(np.float64) - np.log(n.astype(np.float64))))
+    assert off.max() < 3e-9, off.max()
+
+
+def test_totals_below_the_range():
+    """A total that binary32 holds as -inf, though it is a number: a place by its rank, and over in the next step."""
+    x = torch.full((1, 2, 10), LOWEST["f32"], device="cuda")
+    x[..., 7] = 5.0
+    r = A.beam_select(x, torch.tensor([[-1.0, -1.5]], device="cuda"), 6, temperature=0.5)
+    assert r.tokens.tolist() == [[7, 7, 0, 1, 2, 3]] and r.parents.tolist() == [[0, 1, 0, 0, 0, 0]]
+    assert torch.isfinite(r.scores[0, :2]).all() and (r.scores[0, 2:] == -np.inf).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_options(dtype):
     rng, x, scores = data(6, 5, 3001, 7)
