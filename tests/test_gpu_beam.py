@@ -600,6 +600,82 @@ def test_scratch_is_what_the_library_asks_for(monkeypatch, items, beams):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("temp", [1e-3, 1e4, 1e-38, 1e38])
+def test_temperatures(dtype, temp):
+    """Far from 1, up to where log2(e) / T is still a number."""
+    items, beams, cols = 2, 3, 40000
+    _, x, scores = data(items, beams, cols, 23)
+    x[:, :, 7] = 30.0  # one largest
+    if 1e-5 < temp < 1e5:
+        check(x, dtype, scores, 6, temp=temp)
+        return
+    xd, x64 = on_gpu(x, dtype)
+    s = torch.from_numpy(scores.copy()).float().cuda()
+    r = A.beam_select(xd, s, 6, temperature=temp)
+    if temp < 1.0:  # all of a beam's probability is its largest's
+        assert (r.tokens[:, :3] == 7).all() and (r.parents[:, :3] == torch.arange(3, device="cuda")).all()
+        assert torch.equal(r.scores[:, :3], s)
+    else:  # all tokens alike
+        want = scores.astype(np.float32)[:, :1].astype(np.float64) - np.log(cols)
+        assert (r.parents == 0).all() and (np.abs(r.scores.double().cpu().numpy() - want) <= logits_ref.sum_error(cols) + 4e-6).all()
+        assert torch.equal(r.tokens, torch.sort(xd[:, 0].float(), dim=-1, descending=True, stable=True).indices[:, :6])
+
+
+def test_many_items():
+    """More items than a grid's second dimension would take, one beam and several."""
+    for items, beams, cols in ((70001, 1, 9), (66000, 3, 5)):
+        g = torch.Generator(device="cuda").manual_seed(items)
+        x = torch.randn(items, beams, cols, device="cuda", generator=g)
+        s = torch.zeros(items, beams, device="cuda") - torch.arange(beams, device="cuda") * 100.0
+        r = A.beam_select(x, s, 4)
+        want = torch.sort(x[:, 0], dim=-1, descending=True, stable=True).indices[:, :4]
+        assert torch.equal(r.tokens, want) and (r.parents == 0).all()
+        lp = torch.log_softmax(x[:, 0].double(), -1).gather(1, want)
+        assert (r.scores.double() - lp).abs().max() <= logits_ref.sum_error(cols) + 8 * logits_ref.U32 * lp.abs().max().item()
+        state, parents = torch.arange(items * beams, device="cuda").view(items, beams).clone(), (r.parents[:, :1] + beams - 1).expand(items, beams).contiguous()
+        A.beam_reorder(state, parents)
+        assert (state == state[:, -1:]).all() and torch.equal(state[:, 0] // beams, torch.arange(items, device="cuda"))
+
+
+def test_graphs_beside_one_another():
+    """Two captured steps with scratch, replayed at the same time on two streams."""
+    given = []
+    for i in range(2):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        given.append((torch.randn(30, 17, 5000, device="cuda", generator=g), torch.randn(30, 17, device="cuda", generator=g), 12))
+    want = [A.beam_select(*a) for a in given]
+    side, sides, graphs, got = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    for a in given:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            got.append(A.beam_select(*a))
+    for _ in range(20):
+        for g, st in zip(graphs, sides):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [torch.bool, torch.complex128, torch.complex64, torch.float8_e4m3fn, torch.int16])
+def test_reorder_of_other_types(dtype):
+    """What a state's elements are does not matter: their bytes move. Several types in one call."""
+    p = torch.tensor([[1, 0, 3, 2], [2, 2, -1, 0]], device="cuda")
+    n = torch.tensor([5, 3], device="cuda")
+    raw = filled((8, 3, 6, 7, torch.empty(0, dtype=dtype).element_size()), torch.uint8, 9)
+    if dtype is torch.bool:
+        raw = raw & 1
+    t, other = raw.cuda(), filled((8, 2, 6, 4), torch.bfloat16, 10).cuda()
+    first = other.clone()
+    A.beam_reorder([t.view(dtype).squeeze(-1), other], p, n, dim=2)
+    want = ref.reorder(raw.view(2, 4, 3, 6, 7, -1).numpy(), p.cpu().numpy(), n.cpu().numpy(), 3)
+    assert (t.cpu().numpy().reshape(want.shape) == want).all()
+    want = reference(first, p.cpu().numpy(), n.cpu().numpy(), 2, 2, 4)
+    assert (bits(other).reshape(want.shape) == want).all()
+
+
 @pytest.mark.parametrize("graph", [False, True])
 def test_search(graph):
     """A whole search: a model whose logits are a function of the last two tokens, its states reordered and

@@ -313,6 +313,43 @@ def test_scratch_is_what_the_library_asks_for(monkeypatch, rows, experts):
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(plain.ids, want.ids)
 
 
+@pytest.mark.parametrize("rows,experts,k", [(1, 8, 2), (300, 64, 4), (4000, 8, 1), (9000, 100, 6), (3000, 700, 8)])
+def test_counts_without_the_loss(rows, experts, k):
+    x = torch.randn(rows, experts, device="cuda")
+    valid = torch.rand(rows, device="cuda") < 0.8
+    whole, r = A.route_topk(x, k, valid=valid, balance=True), A.route_topk(x, k, valid=valid, counts=True)
+    assert r.balance is None and torch.equal(r.counts, whole.counts) and torch.equal(r.rows, whole.rows)
+    assert torch.equal(r.rows, valid.sum()) and torch.equal(r.ids, whole.ids) and torch.equal(r.lse, whole.lse)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_views(dtype):
+    """[batch, positions, experts] cut from wider rows, one row for all (a broadcast), a row alone, and a gradient written into a padded tensor."""
+    wide = torch.randn(4, 9, 50, device="cuda").to(DT[dtype]).requires_grad_()
+    x = wide[..., 3:43]
+    r = A.route_topk(x, 5, balance=True)
+    g = torch.randn(4, 9, 5, device="cuda")
+    ((r.weights * g).sum() + r.lse.sum() * 0.1 + r.balance * 7).backward()
+    flat = x.detach().reshape(36, 40)
+    f = A.route_topk(flat, 5, balance=True)
+    given = dict(grad_weights=g.view(36, 5), grad_lse=torch.full((36,), 0.1, device="cuda"), grad_balance=torch.tensor(7.0, device="cuda"))
+    want = A.route_topk_backward(flat, *f[:5], **given)
+    assert torch.equal(r.ids.view(36, 5), f.ids) and torch.equal(wide.grad[..., 3:43].reshape(36, 40), want)
+    assert not wide.grad[..., :3].any() and not wide.grad[..., 43:].any()
+    out = torch.full((36, 47), 3.0, device="cuda", dtype=DT[dtype])
+    assert A.route_topk_backward(flat, *f[:5], grad=out[:, 2:42], **given).data_ptr() == out[:, 2:].data_ptr()
+    assert torch.equal(out[:, 2:42], want) and (out[:, :2] == 3).all() and (out[:, 42:] == 3).all()
+    row = torch.randn(40, device="cuda").to(DT[dtype]).requires_grad_()
+    r = A.route_topk(row.expand(6, 40), 5)
+    (r.weights * g[0, :6]).sum().backward()
+    alone = row.detach().requires_grad_()
+    r = A.route_topk(alone, 5)
+    each = [torch.autograd.grad((r.weights * w).sum(), alone, retain_graph=True)[0].float() for w in g[0, :6]]
+    # the sum over the rows is torch's, in the type: an addition of 6 numbers rounds 6 times at most
+    size = torch.stack(each).abs().sum(0)
+    assert ((row.grad.float() - torch.stack(each).sum(0)).abs() <= 6 * size * torch.finfo(DT[dtype]).eps / 2 + 6 * size * 2.0 ** -24).all()
+
+
 def test_training_step():
     """A layer of experts: routed, balanced, trained; against the same in 64 bits, automatic differentiation of both."""
     torch.manual_seed(1)
