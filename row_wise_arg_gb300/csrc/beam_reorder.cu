@@ -11,8 +11,8 @@
 // all items are dealt to as many CTAs as run at once. (With CTAs for each item, and for segments of the
 // longest, items of different lengths left them waiting in waves: 12 states of 9 items, 5 beams, 77 positions took 21 us.)
 //
-// Bound by memory: each distinct parent read once, each moving beam written once. 32 caches of [16 x 4, 8, 1024, 128] bf16, ragged, 289 to 309 us,
-// 5.9 TB/s of the bytes that move.
+// Bound by memory: each distinct parent read once, each moving beam written once. 32 caches of [16 x 4, 8, 1024, 128] bf16, ragged (1.6 to
+// 1.8 GB move, by parents and lengths): 5.9 to 6.1 TB/s of the bytes that move, 264 us for 1612 MB.
 #include "kernels_impl.cuh"
 #include "select.h"
 
@@ -22,10 +22,12 @@ constexpr int kReorderBlock = 256;
 template <int BEAMS> constexpr int kReorderItems = BEAMS <= 16 ? 32 : 8;  // items at a time
 // CTAs of an SM, at least. What is in flight decides (45 KB an SM at the copy rate), words per thread against threads; for
 // words of 4 bytes and less it is the instructions (addresses, above all). us:
-//   32 bf16 caches of [16, 4, 8, 1024, 128], ragged lengths, words of 16 bytes: 309, 335, 379 with 2, 4, 1 of them to a thread
-//   and 4, 2, 6 CTAs (four times as many CTAs as run at once: 299); 16 of [8, 8, 8, 1024, 128]: 208, 246 with 2, 1 and 2, 4 CTAs;
+//   32 bf16 caches of [16, 4, 8, 1024, 128], one draw of ragged lengths, words of 16 bytes: 309, 335, 379 with 2, 4, 1 of them to a thread
+//   and 4, 2, 6 CTAs; 16 of [8, 8, 8, 1024, 128]: 208, 246 with 2, 1 and 2, 4 CTAs;
 //   words of 4 bytes: 12 states of [9, 5, 3, 77, 129] f32 13.2, 4 of [6, 13, 5, 401, 77] 37; of 2: 8 of [16, 4, 7, 701, 33] 34. Two
 //   words to a thread, an address each: 15.6, 55, 59.
+// The grid: the CTAs that run at once. Four times as many: the caches 258 in place of 264 us (another draw), but 12 states of [9, 5, 3, 77, 129] f32
+// 19.4 in place of 15.1 (every CTA plans its items before its first tile).
 template <int BEAMS, int W> constexpr int kReorderCtas = BEAMS <= 4 ? 4 : BEAMS <= 8 ? (W == 16 ? 2 : 3) : BEAMS <= 16 ? 2 : 1;
 // Words per thread at a time.
 template <int BEAMS, int W>

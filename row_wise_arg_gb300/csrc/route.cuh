@@ -26,8 +26,8 @@
 //
 // [65536, 256] f32, top 8, a tenth of it padding, counts and loss, in a graph of calls: 25 us (2.7 TB/s, 151 instructions a row; 16
 // warps an SM, each with one batch: read, then eight dependent looks into blocks; 3.5 us are the second kernel's). [65536, 8] bf16,
-// top 2, 6.9 us. The gradient, 32 lanes to a row of 256 experts: 28.4 us, 4.8 TB/s, 271 instructions a row in half of the
-// issue slots; [20001, 60] bf16, top 4, 7.5 us.
+// top 2, 6.9 us. The gradient, 32 lanes to a row of 256 experts: 28.9 us, 4.7 TB/s, 298 instructions a row in 55% of the
+// issue slots (with exp(x - lse) as it is 28.4 and 271); [20001, 60] bf16, top 4, 7.6 us.
 #pragma once
 
 #include "logits_forward.cuh"
