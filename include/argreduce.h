@@ -539,7 +539,8 @@ argr_status argreduce_logits_plan(argr_logits_op what, int64_t rows, int64_t col
  * at the same place between two 32-byte boundaries). Within a beam the order is exact.
  * 1 <= beams <= ARGR_BEAM_MAX_BEAMS, items < 2^25, 1 <= count <= ARGR_LOGITS_MAX_TOP. Steps of many
  * rows, and those whose clusters the device has no place for, need scratch
- * (argreduce_beam_scratch_bytes() for the current device, 0 for the others; 16-byte aligned, no preparation), which belongs to the call until it has finished on the stream. Errors as
+ * (argreduce_beam_scratch_bytes() for the current device, 0 for the others; 16-byte aligned, no
+ * preparation), which belongs to the call until it has finished on the stream. Errors as
  * for argreduce_logprobs(); ARGR_ESCRATCH.
  */
 #define ARGR_BEAM_MAX_BEAMS 64
